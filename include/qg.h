@@ -85,7 +85,8 @@ enum {
     QG_ERR_RANGE = 8,   /* a packer field is out of range (sc, m > 63; q above 15 / 31 / 63 / 15
                            for Q4_K / Q5_K / Q6_K / IQ4_XS; Q8_0 q = -128) */
     QG_ERR_VARIANT = 9, /* unknown kernel variant, or a variant that does not take this format */
-    QG_ERR_SCRATCH = 10 /* qg_gemv_noalloc: the call needs more scratch than its fixed array holds */
+    QG_ERR_SCRATCH = 10 /* qg_gemv_noalloc: the call needs more scratch than its fixed array holds;
+                           qg_attn_kv4: the workspace is smaller than qg_attn_kv4_workspace says */
 };
 
 /* Kernel variants of the GEMV (qg_gemv_variant).  QG_VARIANT_AUTO is what qg_gemv uses: when
@@ -292,6 +293,141 @@ int qg_gemv_noalloc(const void *W, int fmt, int64_t N, int64_t K, const uint16_t
  * device), else a nonzero code; a nonzero word also clears the array's band counters.  No
  * counterpart on the pages; it allocates nothing (plain copies to and from the array). */
 int qg_noalloc_device_error(void *stream, int *flag);
+
+/* =============================================================================================
+ * The operators between the GEMVs of a decode step: head norms with the position rotation, the
+ * append to a paged key/value cache held in 4 bits, the attention over that cache, and the sampling
+ * of a token from the output projection's logits.  ("HARDWARE GROUND TRUTH: 2x NVIDIA Tesla T4
+ * (Kaggle)", first prompt, "FULL ATTENTION LAYERS": 48 query and 4 key heads of 256, norms of q and k
+ * per head, the first 64 dimensions rotated.  "Qwen3.6 27B Single-B70 Maximum-Speed Requirements And
+ * Execution Plan", "Phase 3: Maximum Useful Fusion": the rotation and cache write after the QKV
+ * projection, the sampler after the output head.)
+ *
+ * Common to all: pointers are device pointers of the current device; calls are asynchronous on
+ * `stream`, allocate nothing, keep nothing between calls and may be captured into a CUDA graph from
+ * the first call on.  Results are bitwise identical run to run.  Argument errors are found on the host
+ * before anything is enqueued; sizes and indices that stand in device memory (slots, page ids, lengths)
+ * are checked by the kernels, which never read or write outside the arrays that the arguments
+ * describe: each entry says what becomes of a bad one.
+ * ============================================================================================= */
+
+/* Element types of a qg_heads (GGML type ids). */
+enum { QG_TYPE_F32 = 0, QG_TYPE_F16 = 1 };
+
+/* A [tokens][heads][dims] view of device memory with strides in elements.  A GEMV's y[n*B + b] of a
+ * projection to H heads of D is {y, 1, D*B, B, QG_TYPE_F32}; x[k*B + b] of the next GEMV likewise with
+ * QG_TYPE_F16; a row-major [T][H][D] array is {p, H*D, D, 1, type}.  Views with dim == 1 and 16-byte
+ * aligned rows are read and written in wide accesses; any other strides are taken as they are.  Output
+ * views must not overlap themselves, nor an input unless the entry says so. */
+typedef struct {
+    void *ptr;
+    int64_t token, head, dim;
+    int32_t type;
+} qg_heads;
+
+/* How the rotation pairs dimensions: (i, i + R/2), or (2i, 2i + 1). */
+enum { QG_ROPE_HALVES = 0, QG_ROPE_ADJACENT = 1 };
+
+#define QG_MAX_HEADS 1024
+
+/* Norms of q and k for each head and the position rotation, in one pass:
+ *     y = x / sqrt(mean(x^2) + eps) * w        (skipped where w is NULL)
+ *     (y_i, y_j) -> (y_i cos a - y_j sin a, y_j cos a + y_i sin a),  a = pos[t] * inv_freq[f]
+ * for the R/2 pairs (i, j) of the first R dimensions; the other dimensions are not rotated.
+ *   q, k, q_out, k_out  views of [T][Hq][D] and [T][Hk][D], fp32 or fp16 each (ignored where Hq or Hk
+ *                       is 0); q_out may be the very view q is (same pointer, strides and type), k_out
+ *                       likewise
+ *   T          tokens, 0 .. 2^31 - 1;  D  64, 128 or 256
+ *   wq, wk     device, fp32 [D], or NULL for no norm
+ *   eps        >= 0
+ *   pos        device, int32 [T]; inv_freq device, double [R/2] (both may be NULL with R == 0)
+ *   R          rotated dimensions, even, 0 .. D; pairing QG_ROPE_*
+ * Sums in fp32; the angle is reduced in 64 bits, so far positions lose nothing; outputs rounded once.
+ * Errors: QG_ERR_SHAPE, _FMT (a view's type), _VARIANT (pairing), _RANGE (eps), _NULL, _ALIGN (a view's
+ * pointer not a multiple of its element, wq, wk, pos 4 B, inv_freq 8 B), _CUDA. */
+int qg_qk_norm_rope(const qg_heads *q, const qg_heads *k, int64_t T, int Hq, int Hk, int D,
+                    const float *wq, const float *wk, double eps, const int32_t *pos,
+                    const double *inv_freq, int R, int pairing, const qg_heads *q_out,
+                    const qg_heads *k_out, void *stream);
+
+/* The 4-bit key/value cache: uint8 [pages][H][page / 16][18 D], D = 64, 128 or 256, page a multiple of
+ * 16 tokens.  A block of 18 D bytes holds 16 consecutive tokens of one head:
+ *     [K codes 16 x D/2][K scales 16 x D/64 x {fp16 d, fp16 m}][V codes 16 x D/2][V scales]
+ * A value is d * code + m, code 0..15, with the (d, m) of its 64 dimensions (4.5 bits a value).  A
+ * token's codes are D nibbles, the even dimension low, in D/32 chunks of 16 bytes; chunk c of token t of
+ * the block stands at place c ^ (s & (D/32 - 1)), s = (t & 2) | ((t ^ (t >> 2)) & 1) << 2.
+ * Slot p of a cache is token p % page of page p / page.
+ *
+ * qg_kv4_bytes: bytes of a cache, 0 for arguments outside the ranges above (pages >= 0, 1 <= H <=
+ * QG_MAX_HEADS) or too large. */
+size_t qg_kv4_bytes(int64_t pages, int page, int H, int D);
+
+/* Appends keys and values, quantized, with the key's head norm and rotation applied on the way:
+ * per 64 dimensions m = fp16(min), d = fp16((max - min) / 15), code = the whole number nearest to
+ * (x - m) / d (ties to even), within 0..15 (0 where d is 0).
+ *   k, v       views of [T][H][D], fp32 or fp16 each; k before its norm and rotation
+ *   wk, eps, pos, inv_freq, R, pairing   as for qg_qk_norm_rope (wk NULL: no norm; R == 0: no rotation)
+ *   slot       device, int64 [T]: where each token goes; a token whose slot lies outside 0 .. pages *
+ *              page - 1 is not written.  Slots of one call are distinct (of two equal ones, the entry
+ *              ends up with parts of both tokens).
+ *   cache      device, qg_kv4_bytes(pages, page, H, D) bytes, 16-byte aligned; other entries are left
+ *              as they are
+ * Norm, rotation and quantization are evaluated in 64 bits, so that the stored codes are the formula's.
+ * Inputs are finite.  Scales saturate at fp16's largest value.  Errors as qg_qk_norm_rope. */
+int qg_kv4_append(const qg_heads *k, const qg_heads *v, int64_t T, int H, int D, const float *wk,
+                  double eps, const int32_t *pos, const double *inv_freq, int R, int pairing,
+                  const int64_t *slot, void *cache, int64_t pages, int page, void *stream);
+
+/* The values that slots hold: k_out, v_out [T][H][D] (fp32 or fp16), d * code + m rounded once to fp32
+ * (then to fp16 for an fp16 view); zeros for a slot outside the cache. */
+int qg_kv4_read(const void *cache, int64_t pages, int page, int H, int D, const int64_t *slot,
+                int64_t T, const qg_heads *k_out, const qg_heads *v_out, void *stream);
+
+/* Attention of new tokens over the cache, causal at the end of each sequence:
+ *     out[t,h] = sum_p softmax_p(scale * q[t,h] . k[p, h / (Hq/Hk)]) v[p, h / (Hq/Hk)]
+ * Sequence s has kv_len[s] places in the cache, its new tokens the last of them, and the query rows
+ * q_start[s] .. q_start[s+1] - 1 of q, n of them; its i-th row sees places p <= kv_len[s] - n + i.  A row
+ * that sees no place gets zeros; rows of no sequence are left as they were.
+ *   q, out     views of [T][Hq][D], fp16; out must not overlap q
+ *   nseq       sequences; q_start device, int32 [nseq + 1], not decreasing, within 0..T
+ *   max_q      the most query tokens of a sequence, as far as the caller knows (it only steers the
+ *              choice of the kernel; any value gives the same results)
+ *   Hq, Hk     heads; Hq a multiple of Hk
+ *   cache      as for qg_kv4_append, H = Hk
+ *   table      device, int32 [nseq][width]: the pages of each sequence in order; a page outside
+ *              0 .. pages - 1 is skipped as if its places were masked
+ *   kv_len     device, int32 [nseq]; taken as at least 0 and at most width * page
+ *   workspace  device, at least qg_attn_kv4_workspace(D) bytes, 256-byte aligned, contents of no
+ *              matter.  Calls that may overlap on the GPU (two streams, two graphs) need one each.  Its
+ *              first word is nonzero afterwards only if a copy did not arrive within two seconds (the
+ *              results are then void).
+ * Scores, softmax statistics and sums are fp32; cache values and softmax weights enter the products as
+ * fp16, rounded once.  Errors as above, plus QG_ERR_SCRATCH. */
+size_t qg_attn_kv4_workspace(int D);
+int qg_attn_kv4(const qg_heads *q, int64_t T, int nseq, const int32_t *q_start, int max_q, int Hq, int Hk,
+                int D, const void *cache, int64_t pages, int page, const int32_t *table, int width,
+                const int32_t *kv_len, float scale, const qg_heads *out, void *workspace,
+                size_t workspace_bytes, void *stream);
+
+/* One token a row from its logits and a given random number.  With z = logit / temperature, tokens in
+ * descending order of their logits (equal ones: the lower index first) and w = exp(z - z_max):
+ *   top-k keeps the first k tokens (all for k <= 0 or k >= V);
+ *   top-p keeps, of those, each token before which less than p of their weight lies (all for p >= 1; the
+ *         first one always);
+ *   min-p drops tokens with w < min_p (never the first);
+ *   the token is the first, in index order, whose running kept weight exceeds u times all kept weight
+ *   (the last kept token for u >= 1).
+ * A temperature that is not above 0 takes the largest logit, the lowest index of equal ones.  A logit of
+ * -inf or NaN is never chosen; a row of nothing else gets -1.
+ *   logits       device, fp32: row r, token v at logits[r * row_stride + v * elem_stride] (a GEMV's
+ *                y[v*B + b]: strides 1 and B)
+ *   rows, V      rows >= 0, 1 <= V < 2^31
+ *   temperature, top_p, min_p (fp32), top_k (int32)  device, [rows]; NULL for 1, 1, 0 and 0
+ *   u            device, fp32 [rows], 0 <= u < 1;  token  device, int32 [rows]
+ * Weights are summed as 64-bit whole numbers: the token does not depend on timing. */
+int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t row_stride, int64_t elem_stride,
+              const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+              const float *u, int32_t *token, void *stream);
 
 /* Static text for a status code. */
 const char *qg_status_string(int status);

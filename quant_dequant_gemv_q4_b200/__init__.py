@@ -1,4 +1,6 @@
-"""B200-native block-quantized dequant GEMV: y[N,B] = dequant(W[N,K]) . x[K,B].
+"""B200-native block-quantized dequant GEMV: y[N,B] = dequant(W[N,K]) . x[K,B], and the operators between
+the GEMVs of a decode step: head norms with the position rotation, a paged 4-bit key/value cache with its
+append and its attention, and sampling.
 
 A thin ctypes binding over ``libqg.so`` (built from ``csrc/`` for sm_100a by ``build.py``): every
 function here only marshals arguments and calls the C ABI of ``include/qg.h`` under the same name;
@@ -6,7 +8,8 @@ all computation runs in the library's CUDA kernels.  There is no CPU fallback: i
 missing, every call raises.
 
 Pointers may be given as torch tensors (their ``data_ptr()``) or plain integers; ``stream=None``
-means torch's current CUDA stream.
+means torch's current CUDA stream.  The operators around the GEMVs take torch CUDA tensors and read
+sizes and strides from them.
 """
 from __future__ import annotations
 
@@ -40,12 +43,23 @@ QG_ERR_RANGE = 8
 QG_ERR_VARIANT = 9
 QG_ERR_SCRATCH = 10
 
+QG_TYPE_F32 = 0
+QG_TYPE_F16 = 1
+QG_ROPE_HALVES = 0
+QG_ROPE_ADJACENT = 1
+
 # bytes of the fixed device array qg_gemv_noalloc uses as scratch
 QG_NOALLOC_SCRATCH_BYTES = 8 << 20
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqg.so")
 _lib = None
+
+
+class qg_heads(ctypes.Structure):
+    """A [tokens][heads][dims] view of device memory, strides in elements."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("token", ctypes.c_int64), ("head", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("type", ctypes.c_int32)]
 
 
 class QgError(RuntimeError):
@@ -96,6 +110,21 @@ def lib() -> ctypes.CDLL:
         L.qg_hbm_copy.restype = I
         L.qg_hbm_read.argtypes = [P, SZ, P, P]
         L.qg_hbm_read.restype = I
+        F, DBL, HP = ctypes.c_float, ctypes.c_double, ctypes.POINTER(qg_heads)
+        L.qg_qk_norm_rope.argtypes = [HP, HP, I64, I, I, I, P, P, DBL, P, P, I, I, HP, HP, P]
+        L.qg_qk_norm_rope.restype = I
+        L.qg_kv4_bytes.argtypes = [I64, I, I, I]
+        L.qg_kv4_bytes.restype = SZ
+        L.qg_kv4_append.argtypes = [HP, HP, I64, I, I, P, DBL, P, P, I, I, P, P, I64, I, P]
+        L.qg_kv4_append.restype = I
+        L.qg_kv4_read.argtypes = [P, I64, I, I, I, P, I64, HP, HP, P]
+        L.qg_kv4_read.restype = I
+        L.qg_attn_kv4_workspace.argtypes = [I]
+        L.qg_attn_kv4_workspace.restype = SZ
+        L.qg_attn_kv4.argtypes = [HP, I64, I, P, I, I, I, I, P, I64, I, P, I, P, F, HP, P, SZ, P]
+        L.qg_attn_kv4.restype = I
+        L.qg_sample.argtypes = [P, I64, I64, I64, I64, P, P, P, P, P, P, P]
+        L.qg_sample.restype = I
         L.qg_status_string.argtypes = [I]
         L.qg_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -251,6 +280,181 @@ def qg_hbm_copy(src, dst, nbytes: int, stream=None) -> None:
 
 def qg_hbm_read(src, nbytes: int, out, stream=None) -> None:
     _ok(lib().qg_hbm_read(_ptr(src), int(nbytes), _ptr(out), _stream(stream)), "qg_hbm_read")
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_device(what: str, *tensors) -> None:
+    """Every tensor (None apart) is on the current CUDA device, where the kernels run."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise ValueError(f"{what}: every tensor must be on the current CUDA device ({dev}), got {t.device}")
+
+
+def _heads(t, what: str) -> qg_heads:
+    import torch
+    if t.dtype is torch.float32:
+        kind = QG_TYPE_F32
+    elif t.dtype is torch.float16:
+        kind = QG_TYPE_F16
+    else:
+        raise ValueError(f"{what}: fp32 or fp16, got {t.dtype}")
+    _need(t.dim() == 3, f"{what}: [tokens, heads, dims]")
+    return qg_heads(t.data_ptr(), *t.stride(), kind)
+
+
+def _vector(t, dtype: str, n: int, what: str):
+    """A contiguous vector of n elements of the named type, or None."""
+    import torch
+    if t is not None:
+        _need(t.dtype is getattr(torch, dtype) and t.dim() == 1 and t.shape[0] == n and t.is_contiguous(),
+              f"{what}: contiguous {dtype} [{n}], got {t.dtype} {tuple(t.shape)}")
+        return t.data_ptr()
+    return None
+
+
+def _cache_sizes(cache, page: int, what: str):
+    import torch
+    _need(cache.dtype is torch.uint8 and cache.dim() == 4 and cache.is_contiguous(),
+          f"{what}: the cache is contiguous uint8 [pages, heads, page / 16, 18 D]")
+    pages, H, blocks, width = cache.shape
+    _need(page >= 16 and blocks * 16 == page and width % 18 == 0,
+          f"{what}: a cache of shape {tuple(cache.shape)} does not hold pages of {page} tokens")
+    return pages, H, width // 18
+
+
+def _rope(pos, inv_freq, T: int, what: str):
+    R = 0 if inv_freq is None else 2 * inv_freq.shape[0]
+    if R:
+        _need(pos is not None, f"{what}: a rotation needs positions")
+        return _vector(pos, "int32", T, f"{what}: pos"), _vector(inv_freq, "float64", R // 2, f"{what}: inv_freq"), R
+    return None, None, 0
+
+
+def qg_kv4_bytes(pages: int, page: int, H: int, D: int) -> int:
+    """Bytes of a 4-bit cache; 0 for sizes it does not come in."""
+    return int(lib().qg_kv4_bytes(int(pages), int(page), int(H), int(D)))
+
+
+def kv4_cache(pages: int, page: int, H: int, D: int, device=None):
+    """An empty 4-bit cache, uint8 [pages, H, page / 16, 18 D]."""
+    import torch
+    if pages > 0 and qg_kv4_bytes(pages, page, H, D) == 0:
+        raise QgError(QG_ERR_SHAPE, "kv4_cache")
+    return torch.zeros((pages, H, page // 16, 18 * D), dtype=torch.uint8, device=device or "cuda")
+
+
+def qg_qk_norm_rope(q, k, wq, wk, eps: float, pos, inv_freq, pairing: int, q_out, k_out, stream=None) -> None:
+    """Head norms (weights wq, wk fp32 [D]; None: no norm) and the rotation by pos * inv_freq (int32 [T],
+    float64 [R / 2]; inv_freq None: no rotation) of q [T, Hq, D] and k [T, Hk, D] (either may be None)."""
+    what = "qg_qk_norm_rope"
+    some = q if q is not None else k
+    _need(some is not None, f"{what}: q or k")
+    _on_device(what, q, k, wq, wk, pos, inv_freq, q_out, k_out)
+    T, _, D = some.shape
+    hv, H = [], []
+    for x, y, n in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            hv += [None, None]
+            H.append(0)
+            continue
+        _need(y is not None and x.shape == y.shape and x.shape[0] == T and x.shape[2] == D,
+              f"{what}: {n} and {n}_out are [{T}, heads, {D}]")
+        hv += [ctypes.byref(_heads(x, f"{what}: {n}")), ctypes.byref(_heads(y, f"{what}: {n}_out"))]
+        H.append(x.shape[1])
+    pp, pf, R = _rope(pos, inv_freq, T, what)
+    _ok(lib().qg_qk_norm_rope(hv[0], hv[2], T, H[0], H[1], D, _vector(wq, "float32", D, f"{what}: wq"),
+                              _vector(wk, "float32", D, f"{what}: wk"), float(eps), pp, pf, R, int(pairing),
+                              hv[1], hv[3], _stream(stream)), what)
+
+
+def qg_kv4_append(k, v, wk, eps: float, pos, inv_freq, pairing: int, slot, cache, page: int, stream=None) -> None:
+    """Appends k, v [T, H, D] to the 4-bit cache at slot int64 [T] (-1: not written), the key with its head
+    norm (wk None: none) and rotation (inv_freq None: none) applied on the way."""
+    what = "qg_kv4_append"
+    _on_device(what, k, v, wk, pos, inv_freq, slot, cache)
+    pages, H, D = _cache_sizes(cache, page, what)
+    T = k.shape[0]
+    _need(k.shape == v.shape and tuple(k.shape[1:]) == (H, D), f"{what}: k and v are [tokens, {H}, {D}]")
+    pp, pf, R = _rope(pos, inv_freq, T, what)
+    _ok(lib().qg_kv4_append(ctypes.byref(_heads(k, f"{what}: k")), ctypes.byref(_heads(v, f"{what}: v")), T, H, D,
+                            _vector(wk, "float32", D, f"{what}: wk"), float(eps), pp, pf, R, int(pairing),
+                            _vector(slot, "int64", T, f"{what}: slot"), cache.data_ptr(), pages, int(page),
+                            _stream(stream)), what)
+
+
+def qg_kv4_read(cache, page: int, slot, k_out, v_out, stream=None) -> None:
+    """The values that the slots (int64 [T]) of the cache hold, into k_out and v_out [T, H, D]."""
+    what = "qg_kv4_read"
+    _on_device(what, cache, slot, k_out, v_out)
+    pages, H, D = _cache_sizes(cache, page, what)
+    T = slot.shape[0]
+    _need(tuple(k_out.shape) == (T, H, D) and k_out.shape == v_out.shape, f"{what}: k_out and v_out are [{T}, {H}, {D}]")
+    _ok(lib().qg_kv4_read(cache.data_ptr(), pages, int(page), H, D, _vector(slot, "int64", T, f"{what}: slot"), T,
+                          ctypes.byref(_heads(k_out, f"{what}: k_out")), ctypes.byref(_heads(v_out, f"{what}: v_out")),
+                          _stream(stream)), what)
+
+
+_attn_ws: dict = {}
+
+
+def qg_attn_kv4_workspace(D: int) -> int:
+    """Workspace bytes of qg_attn_kv4 on the current device."""
+    import torch
+    key = (torch.cuda.current_device(), int(D))
+    if key not in _attn_ws:
+        n = int(lib().qg_attn_kv4_workspace(int(D)))
+        if n == 0:
+            raise QgError(QG_ERR_SHAPE, "qg_attn_kv4_workspace")
+        _attn_ws[key] = n
+    return _attn_ws[key]
+
+
+def qg_attn_kv4(q, q_start, max_q: int, cache, page: int, table, kv_len, scale: float, out, workspace=None,
+                stream=None) -> None:
+    """Causal attention of the new tokens q [T, Hq, D] (fp16; sequence s: rows q_start[s] .. q_start[s + 1] - 1)
+    over the 4-bit cache, sequence s having kv_len[s] places in the pages table[s], into out [T, Hq, D] (fp16).
+    workspace: uint8, qg_attn_kv4_workspace(D) bytes, not shared with a call that may overlap; None takes one
+    from torch's allocator for this call."""
+    import torch
+    what = "qg_attn_kv4"
+    _on_device(what, q, q_start, cache, table, kv_len, out, workspace)
+    pages, Hk, D = _cache_sizes(cache, page, what)
+    _need(q.dtype is torch.float16 and out.dtype is torch.float16, f"{what}: q and out are fp16")
+    _need(q.dim() == 3 and q.shape == out.shape and q.shape[2] == D, f"{what}: q and out are [tokens, heads, {D}]")
+    T, Hq, _ = q.shape
+    _need(table.dtype is torch.int32 and table.dim() == 2 and table.is_contiguous(), f"{what}: table is contiguous int32 [sequences, pages]")
+    nseq, width = table.shape
+    ps = _vector(q_start, "int32", nseq + 1, f"{what}: q_start")
+    pl = _vector(kv_len, "int32", nseq, f"{what}: kv_len")
+    st = _stream(stream)
+    if workspace is None:
+        _need(st == torch.cuda.current_stream().cuda_stream, f"{what}: a call on a stream that is not torch's current one needs a workspace")
+        workspace = torch.empty(qg_attn_kv4_workspace(D), dtype=torch.uint8, device=q.device)
+    _ok(lib().qg_attn_kv4(ctypes.byref(_heads(q, what)), T, nseq, ps, int(max_q), Hq, Hk, D, cache.data_ptr(), pages,
+                          int(page), table.data_ptr(), width, pl, float(scale), ctypes.byref(_heads(out, what)),
+                          workspace.data_ptr(), workspace.numel() * workspace.element_size(), st), what)
+
+
+def qg_sample(logits, temperature, top_k, top_p, min_p, u, token, stream=None) -> None:
+    """One token a row of logits [rows, V] (fp32, any strides: a GEMV's y.view(V, B).t()) with the row's
+    temperature, top_k (int32), top_p and min_p (None: no such filter) from the random numbers u, into token
+    (int32 [rows])."""
+    import torch
+    what = "qg_sample"
+    _on_device(what, logits, temperature, top_k, top_p, min_p, u, token)
+    _need(logits.dtype is torch.float32 and logits.dim() == 2, f"{what}: logits are fp32 [rows, V]")
+    R, V = logits.shape
+    rs, es = logits.stride()
+    _ok(lib().qg_sample(logits.data_ptr(), R, V, rs, es, _vector(temperature, "float32", R, f"{what}: temperature"),
+                        _vector(top_k, "int32", R, f"{what}: top_k"), _vector(top_p, "float32", R, f"{what}: top_p"),
+                        _vector(min_p, "float32", R, f"{what}: min_p"), _vector(u, "float32", R, f"{what}: u"),
+                        _vector(token, "int32", R, f"{what}: token"), _stream(stream)), what)
 
 
 def gemv(W, fmt: int, N: int, K: int, x, variant: int = QG_VARIANT_AUTO, stream=None):
