@@ -390,20 +390,21 @@ int qg_kv4_read(const void *cache, int64_t pages, int page, int H, int D, const 
  * that sees no place gets zeros; rows of no sequence are left as they were.
  *   q, out     views of [T][Hq][D], fp16; out must not overlap q
  *   nseq       sequences; q_start device, int32 [nseq + 1], not decreasing, within 0..T
- *   max_q      the most query tokens of a sequence, as far as the caller knows (it only steers the
- *              choice of the kernel; any value gives the same results)
+ *   max_q      the most query tokens of a sequence, as far as the caller knows: it chooses how many query
+ *              rows are worked through together.  Any value gives a right result (of a sum in another
+ *              order); one that is too small or too large takes longer
  *   Hq, Hk     heads; Hq a multiple of Hk
  *   cache      as for qg_kv4_append, H = Hk
  *   table      device, int32 [nseq][width]: the pages of each sequence in order; a page outside
  *              0 .. pages - 1 is skipped as if its places were masked
  *   kv_len     device, int32 [nseq]; taken as at least 0 and at most width * page
- *   workspace  device, at least qg_attn_kv4_workspace(D) bytes, 256-byte aligned, contents of no
- *              matter.  Calls that may overlap on the GPU (two streams, two graphs) need one each.  Its
+ *   workspace  device, at least qg_attn_kv4_workspace(Hq, Hk, D, max_q) bytes (0 for arguments out of
+ *              range, or without a device), 256-byte aligned, contents of no matter.  Calls that may overlap on the GPU (two streams, two graphs) need one each.  Its
  *              first word is nonzero afterwards only if a copy did not arrive within two seconds (the
  *              results are then void).
  * Scores, softmax statistics and sums are fp32; cache values and softmax weights enter the products as
  * fp16, rounded once.  Errors as above, plus QG_ERR_SCRATCH. */
-size_t qg_attn_kv4_workspace(int D);
+size_t qg_attn_kv4_workspace(int Hq, int Hk, int D, int max_q);
 int qg_attn_kv4(const qg_heads *q, int64_t T, int nseq, const int32_t *q_start, int max_q, int Hq, int Hk,
                 int D, const void *cache, int64_t pages, int page, const int32_t *table, int width,
                 const int32_t *kv_len, float scale, const qg_heads *out, void *workspace,

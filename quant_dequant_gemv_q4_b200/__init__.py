@@ -119,7 +119,7 @@ def lib() -> ctypes.CDLL:
         L.qg_kv4_append.restype = I
         L.qg_kv4_read.argtypes = [P, I64, I, I, I, P, I64, HP, HP, P]
         L.qg_kv4_read.restype = I
-        L.qg_attn_kv4_workspace.argtypes = [I]
+        L.qg_attn_kv4_workspace.argtypes = [I, I, I, I]
         L.qg_attn_kv4_workspace.restype = SZ
         L.qg_attn_kv4.argtypes = [HP, I64, I, P, I, I, I, I, P, I64, I, P, I, P, F, HP, P, SZ, P]
         L.qg_attn_kv4.restype = I
@@ -403,23 +403,26 @@ def qg_kv4_read(cache, page: int, slot, k_out, v_out, stream=None) -> None:
 _attn_ws: dict = {}
 
 
-def qg_attn_kv4_workspace(D: int) -> int:
+def qg_attn_kv4_workspace(Hq: int, Hk: int, D: int, max_q: int) -> int:
     """Workspace bytes of qg_attn_kv4 on the current device."""
     import torch
-    key = (torch.cuda.current_device(), int(D))
-    if key not in _attn_ws:
-        n = int(lib().qg_attn_kv4_workspace(int(D)))
+    key = (torch.cuda.current_device(), Hq, Hk, D, max_q)
+    n = _attn_ws.get(key)
+    if n is None:
+        n = int(lib().qg_attn_kv4_workspace(int(Hq), int(Hk), int(D), int(max_q)))
         if n == 0:
             raise QgError(QG_ERR_SHAPE, "qg_attn_kv4_workspace")
+        if len(_attn_ws) >= 4096:
+            _attn_ws.clear()
         _attn_ws[key] = n
-    return _attn_ws[key]
+    return n
 
 
 def qg_attn_kv4(q, q_start, max_q: int, cache, page: int, table, kv_len, scale: float, out, workspace=None,
                 stream=None) -> None:
     """Causal attention of the new tokens q [T, Hq, D] (fp16; sequence s: rows q_start[s] .. q_start[s + 1] - 1)
     over the 4-bit cache, sequence s having kv_len[s] places in the pages table[s], into out [T, Hq, D] (fp16).
-    workspace: uint8, qg_attn_kv4_workspace(D) bytes, not shared with a call that may overlap; None takes one
+    workspace: uint8, qg_attn_kv4_workspace(Hq, Hk, D, max_q) bytes, not shared with a call that may overlap; None takes one
     from torch's allocator for this call."""
     import torch
     what = "qg_attn_kv4"
@@ -435,7 +438,7 @@ def qg_attn_kv4(q, q_start, max_q: int, cache, page: int, table, kv_len, scale: 
     st = _stream(stream)
     if workspace is None:
         _need(st == torch.cuda.current_stream().cuda_stream, f"{what}: a call on a stream that is not torch's current one needs a workspace")
-        workspace = torch.empty(qg_attn_kv4_workspace(D), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(qg_attn_kv4_workspace(Hq, Hk, D, max_q), dtype=torch.uint8, device=q.device)
     _ok(lib().qg_attn_kv4(ctypes.byref(_heads(q, what)), T, nseq, ps, int(max_q), Hq, Hk, D, cache.data_ptr(), pages,
                           int(page), table.data_ptr(), width, pl, float(scale), ctypes.byref(_heads(out, what)),
                           workspace.data_ptr(), workspace.numel() * workspace.element_size(), st), what)

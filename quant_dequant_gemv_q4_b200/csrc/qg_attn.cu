@@ -5,76 +5,79 @@
 //
 // for the i-th of the n query tokens of a sequence of len places: k, v = d * code + m.
 //
-// What bounds it.  Each place of a key head is 2 * 4.5 bits a dimension, read once for up to 16 query
-// rows (G heads x n tokens): at 12 rows 9 bytes feed 48 multiply-adds, so a step that decodes few
-// tokens is bound by the cache's bytes as long as the unpacking (about 1.7 instructions a value) and
-// the matrix instructions keep up.
+// An item is a key head of a sequence and up to N of its query rows (G heads x n tokens, N = 16 .. 128); it
+// is worked through in tiles of 128 places.  Both products run on the fifth-generation tensor cores with
+// the cache as the A operand, M = 128, and the query rows as the N columns:
+//   S^T[128 places x N] = K[128 x D] Q^T        A: unpacked keys in tensor memory, lane = place
+//   O^T[D x N]         += V^T[D x 128] P^T      A: unpacked values in tensor memory, lane = dimension
+// so few query rows cost few tensor cycles (at N = 16 both products of a tile take about a tenth of the
+// time its bytes take to arrive), accumulators take no registers, and the unpacked cache never passes
+// through shared memory, whose bandwidth would bound the kernel (16 KB of fp16 written and read back for
+// each 16 places, against 4.6 KB of codes).
+//   Keys: a thread unpacks one place's row and writes it to its tensor-memory lane (tcgen05.st 32x32b).
+//   Values: ldmatrix.trans on 16-bit elements (four nibbles: four dimensions of a place) gives a thread two
+//   neighbouring places of four dimensions; masking out each of the four nibbles leaves the fp16 pair
+//   that one tensor-memory column of that dimension's lane holds, and tcgen05.st 16x128b has just this
+//   fragment's shape: the transposition costs nothing.
+// Which k index a dimension has in the first product, and which lane in the second, is free: the nibble
+// order is left as it falls, q is staged in that order and O is unscrambled when it is written.
 //
-// attn_kv4_kernel.  One warp takes 16 query rows and a tile of 16 places:
-//   S[16 x 16] = Q K^T  and  O[16 x D] += P V  by mma.sync m16n8k16 (f16 operands, fp32 sums).
-// The codes go from shared memory straight into the B fragments: the assignment of dimensions to the
-// k index of the first product, and of dimensions to the n index of the second, is free, and is chosen
-// so that a lane's 4-byte words hold only nibbles of its own fragments (kq_dims, v_dims).  Nothing is
-// transposed, and the unpacked values are never stored.
-// Four warps of a CTA take the four tiles of a 64-place unit; each keeps its own running maximum, sum
-// and O, with no synchronization in the loop, and the four are joined in shared memory at the end of a
-// row tile.  Each warp's lane 0 keeps a ring of bulk copies in flight, a block (18 D bytes) each.
+// Roles of a CTA's warps (one CTA an SM): a producer (a bulk copy of 18 D bytes for each 16 places, several
+// tiles ahead), four warps that unpack keys, four for values, four (N = 128: eight) for the softmax, and
+// one that issues the matrix instructions.  Key and value operands are double-buffered in parts of a tile
+// (kSub), scores and weights in tiles, all handed over by mbarriers.
 //
-// Splitting.  The units of all (sequence, head, row tile) items are numbered in one line and dealt to
-// the CTAs in equal runs, so ragged batches and single long sequences fill the card alike.  An item cut
-// between CTAs leaves partial (O, maximum, sum) in the workspace, which attn_kv4_join_kernel adds up in
-// CTA order: results do not depend on timing.
+// Softmax in base 2 on fp32 scores.  A thread holds one place's scores; the reference maximum of a row is
+// shared by the 128 places and moves only when a score exceeds it by more than 8 (so hardly ever after the
+// first tile), so that in the common tile nothing is reduced across threads: weights are
+// 2^(s - reference + 7), at most 2^15 and of full fp16 precision down to 2^-21 of the reference, and a
+// thread adds up its own places' weights until the item ends.
 //
-// Softmax in base 2 on fp32 scores.  The reference maximum of a row moves only when a score exceeds it
-// by more than 8 (so rarely after the first tiles), and the weights carry a factor 2^7: at most 2^15,
-// and full fp16 precision down to 2^-21 of the reference.
+// Splitting.  The tiles of all items are numbered in one line and dealt to the CTAs in equal runs, so ragged
+// batches and single long sequences fill the card alike.  An item cut between CTAs leaves partial
+// (O, reference, sum) in the workspace, which attn_kv4_join_kernel adds up in CTA order: results do not
+// depend on timing.
 #include <algorithm>
+#include <cstddef>
 
 #include "qg_kv4.cuh"
 #include "qg_ptx.cuh"
+#include "qg_tcgen05.cuh"
 
 namespace {
 
 using namespace qg;
 
-constexpr int kAttnWarps = 4;
-constexpr int kUnit = kAttnWarps * kKvBlock;  // places of a unit
-constexpr int kRows = 16;                     // query rows of an item
-constexpr float kMoveMax = 8.0f;              // a score this far above the reference moves it
-constexpr float kWeightShift = 7.0f;          // weights are 2^(s - reference + 7)
+constexpr int kTile = 128;                      // places of a tile
+constexpr int kTileBlocks = kTile / kKvBlock;
+constexpr float kMoveMax = 8.0f;                // a score this far above the reference moves it
+constexpr float kWeightShift = 7.0f;
+constexpr int kMetas = 16;                      // tiles whose description is kept (more than any role lags)
 
-template <int D> struct AttnCfg;
-template <> struct AttnCfg<256> { static constexpr int kStages = 5, kCtas = 2; };
-template <> struct AttnCfg<128> { static constexpr int kStages = 6, kCtas = 3; };
-template <> struct AttnCfg<64> { static constexpr int kStages = 8, kCtas = 4; };
-
-constexpr int kJoinStride = 68;  // floats of a row of the joining buffer (64 and a shift of four banks)
-
-template <int D> struct AttnSmem {
-    static constexpr int kRing = kAttnWarps * AttnCfg<D>::kStages * Kv4<D>::kBlock;
-    static constexpr int kJoin = kAttnWarps * kRows * kJoinStride * 4;
-    static constexpr int kBytes = kRing + kJoin;
-};
+// flags of a tile
+constexpr int kFirst = 1;      // first of this CTA's part of its item
+constexpr int kLast = 2;       // last of it
+constexpr int kFromStart = 4;  // the part holds the item's first tile
+constexpr int kComplete = 8;   // the part is the whole item
 
 struct AttnArgs {
     HeadsView q, out;
     const uint8_t *cache;
     const int32_t *table, *start, *len;
     int64_t pages, T;
-    float *part;     // [2 grid][kRows][D]
-    float2 *stat;    // [2 grid][kRows] (reference, sum)
-    int4 *cut;       // items cut between CTAs: {sequence, head, row tile, CTAs}, CTAs = 0 for none
+    float *part;   // [2 grid][N][D]
+    float2 *stat;  // [2 grid][N] (reference, sum)
+    int4 *cut;     // items cut between CTAs: {sequence, head | first CTA << 16, row tile, CTAs}, CTAs = 0: none
     int *err;
     float scale_log2;
     int nseq, page, width, Hk, G, by_item;
 };
 
-// What the schedule needs of a sequence.
 struct Seq {
-    int first, n, len, tiles, units;  // first query row in T, query tokens, places, row tiles, units of an item
+    int first, n, len, tiles;  // first query row in T, query tokens, places, row tiles
 };
 
-__device__ __forceinline__ Seq load_seq(const AttnArgs &a, int s)
+template <int N> __device__ __forceinline__ Seq load_seq(const AttnArgs &a, int s)
 {
     Seq q;
     const int64_t lo = a.start[s], hi = a.start[s + 1];
@@ -84,29 +87,53 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs &a, int s)
     const int64_t cap = (int64_t)a.width * a.page;
     const int64_t len = a.len[s];
     q.len = (int)(len < 0 ? 0 : len < cap ? len : cap);
-    q.tiles = (int)(((int64_t)q.n * a.G + kRows - 1) / kRows);
-    q.units = q.len > 0 ? (q.len + kUnit - 1) / kUnit : 1;  // an empty sequence still writes its zeros
+    q.tiles = (int)(((int64_t)q.n * a.G + N - 1) / N);
     return q;
 }
 
-__device__ __forceinline__ int64_t seq_units(const AttnArgs &a, const Seq &q) { return (int64_t)q.tiles * a.Hk * q.units; }
+// Tiles of the item of row tile rt: down to the last place that any of its rows sees (one for rows that see
+// nothing: their zeros are still written).
+template <int N> __device__ __forceinline__ int item_units(const AttnArgs &a, const Seq &q, int rt)
+{
+    const int64_t last = ((int64_t)rt * N + N - 1) / a.G;
+    const int tok = (int)(last < q.n - 1 ? last : q.n - 1);
+    const int seen = q.len - q.n + tok + 1;
+    return seen > 0 ? (seen + kTile - 1) / kTile : 1;
+}
 
-// A place in the line of units.
+template <int N> __device__ __forceinline__ int64_t head_units(const AttnArgs &a, const Seq &q)
+{
+    int64_t u = 0;
+    for (int rt = 0; rt < q.tiles; ++rt) u += item_units<N>(a, q, rt);
+    return u;
+}
+
+// A place in the line of tiles.
 struct Cursor {
     Seq q;
-    int s, item, unit;  // sequence, item of it (head * tiles + row tile), unit of the item
+    int s, head, rt, unit, units;
 };
 
-__device__ __forceinline__ void next_item(const AttnArgs &a, Cursor &c)
+template <int N> __device__ __forceinline__ void next_item(const AttnArgs &a, Cursor &c)
 {
     c.unit = 0;
-    if (++c.item < c.q.tiles * a.Hk) return;
-    c.item = 0;
-    do {
-        if (++c.s >= a.nseq) return;
-        c.q = load_seq(a, c.s);
-    } while (c.q.tiles == 0);
+    if (++c.rt == c.q.tiles) {
+        c.rt = 0;
+        if (++c.head == a.Hk) {
+            c.head = 0;
+            do {
+                if (++c.s >= a.nseq) return;
+                c.q = load_seq<N>(a, c.s);
+            } while (c.q.tiles == 0);
+        }
+    }
+    c.units = item_units<N>(a, c.q, c.rt);
 }
+
+// What the roles need to know of a tile.
+struct Meta {
+    int flags, valid, pos, first, n, len, s, head, rt, ctas, item, pad;
+};
 
 __device__ __forceinline__ uint32_t lop_and_or(uint32_t x, uint32_t m, uint32_t o)
 {
@@ -114,11 +141,10 @@ __device__ __forceinline__ uint32_t lop_and_or(uint32_t x, uint32_t m, uint32_t 
     asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(m), "r"(o));  // (x & m) | o
     return r;
 }
-
 __device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
 
-// Two codes at bits 0-3 (LO) or 4-7 of each half of x as d * code + m: the nibble under an exponent is
+// Two codes at bits 0-3 (lo) or 4-7 (hi) of each half of x as d * code + m: the nibble under an exponent is
 // 1024 + code (or 1024 + 16 code), made the exact code by one f16x2 instruction; the second rounds the
 // value to fp16 once (2^-11 relative, far below the step d).
 __device__ __forceinline__ uint32_t dequant_lo(uint32_t x, __half2 d, __half2 m)
@@ -133,110 +159,228 @@ __device__ __forceinline__ uint32_t dequant_hi(uint32_t x, __half2 d, __half2 m)
     return as_u32(__hfma2(c, d, m));
 }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
-{
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t lds32(const uint8_t *a) { return *reinterpret_cast<const uint32_t *>(a); }
-template <int W> __device__ __forceinline__ void lds_words(const uint8_t *a, uint32_t *w)
-{
-    if constexpr (W == 4) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(a);
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else if constexpr (W == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(a);
-        w[0] = v.x, w[1] = v.y;
-    } else {
-        w[0] = lds32(a);
-    }
-}
-
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) { return as_u32(__floats2half2_rn(lo, hi)); }
-
-// First of the 8 dimensions that word i of lane part t4 (lane % 4) holds of a K row.
-template <int D> __device__ __forceinline__ int kq_dims(int t4, int i)
+__device__ __forceinline__ int float_order(float x)
 {
-    if constexpr (D == 256) return 32 * t4 + 8 * (i & 3) + (i >> 2) * 128;
-    return (D / 4) * t4 + 8 * i;
+    const int b = __float_as_int(x);
+    return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float order_float(int b) { return __int_as_float(b ^ ((b >> 31) & 0x7fffffff)); }
+
+template <int D, int N> struct Cfg {
+    using F = Kv4<D>;
+    static constexpr int kSub = (D == 256 && N == 128) ? 4 : 2;  // operand buffers hold 1 / kSub of a tile
+    static constexpr int kMh = D >= 128 ? D / 128 : 1;           // M = 128 halves of O^T
+    static constexpr int kKCols = D / 2 / kSub;                  // columns of a key buffer: D / kSub dimensions
+    static constexpr int kVTok = kTile / kSub;                   // places of a value buffer
+    static constexpr int kVCols = kVTok / 2;                     // columns of it in each half
+    static constexpr int kSBufs = (D == 256 && N == 128) ? 1 : 2;
+    static constexpr int kPBufs = (D == 256 && N == 128) ? 1 : 2;
+    static constexpr int kSoft = N > 64 ? 2 : 1;                 // softmax warpgroups
+    static constexpr int kNS = N / kSoft;                        // query rows of each
+    static constexpr int kWarps = 8 + 4 * kSoft + 2;
+    // tensor memory columns
+    static constexpr int kK = 0, kV = kK + 2 * kKCols, kS = kV + 2 * kVCols * kMh, kO = kS + kSBufs * N;
+    static constexpr int kCols = kO + kMh * N;
+    static_assert(kCols <= 512, "tensor memory");
+    // shared memory
+    static constexpr int kTileBytes = kTileBlocks * F::kBlock;
+    static constexpr int kStages = D == 256 ? (N == 128 ? 3 : 4) : D == 128 ? 6 : 8;
+    static constexpr int kQ = kStages * kTileBytes;
+    static constexpr int kQBytes = N * D * 2;
+    static constexpr int kP = kQ + kQBytes;
+    static constexpr int kPBytes = N * kTile * 2;
+    static constexpr int kOutStride = D + 4;
+    static constexpr int kOutRows = 8;
+    static constexpr int kOutBytes = kSoft * kOutRows * kOutStride * 4;
+    static constexpr int kPAll = kPBufs * kPBytes > kOutBytes ? kPBufs * kPBytes : kOutBytes;
+    static constexpr int kBytes = kP + kPAll;
+    static_assert(kBytes <= 224 * 1024, "shared memory");
+};
+
+template <int N> struct Small {
+    uint64_t ring_full[8], ring_empty[8];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], p_full[2], p_empty[2];
+    uint64_t q_full, o_full, o_empty;
+    Meta meta[kMetas];
+    Cursor found;
+    int found_item;
+    int64_t scan[20];
+    int iscan[20];
+    uint32_t tmem;
+    int dead, produced;    // produced: tiles described so far
+    alignas(16) float base[N];  // reference - kWeightShift (0 in place of -inf)
+    float ref[N];
+    alignas(16) int lim[N];     // last place that a row sees
+    float wred[8][N];      // by warp
+    float inv[N];
+    float factor[N];
+};
+
+// Waits for a phase; gives up after kWaitNs of wall time, or at once when another warp has.
+__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, int *dead, int *err)
+{
+    const uint32_t b = smem_u32(bar);
+    if (mbar_try_wait(b, parity)) return;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(b, parity)) {
+        if (*(volatile int *)dead) return;
+        if (global_timer_ns() - t0 > kWaitNs) {
+            *(volatile int *)dead = 1;
+            *err = 1;
+            return;
+        }
+    }
 }
 
-template <int D> __global__ void __launch_bounds__(kAttnWarps * 32, AttnCfg<D>::kCtas) attn_kv4_kernel(const AttnArgs a)
+// Waits until `need` tiles are described.
+__device__ __forceinline__ void wait_described(int *produced, int need, int *dead, int *err)
+{
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        int v;
+        asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(produced)) : "memory");
+        if (v >= need || *(volatile int *)dead) return;
+        if (global_timer_ns() - t0 > kWaitNs) {
+            *(volatile int *)dead = 1;
+            *err = 1;
+            return;
+        }
+    }
+}
+
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ bool bar_or(int id, int threads, bool p)
+{
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"((int)p)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// Sums v[i] over the warp's lanes for M values: on return lane l holds the total of value l % M.
+template <int M> __device__ __forceinline__ float reduce_scatter(float (&v)[M], int lane)
+{
+#pragma unroll
+    for (int o = M / 2; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float give = up ? v[i] : v[i + o];
+            const float keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    }
+    float r = v[0];
+#pragma unroll
+    for (int o = M; o < 32; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+    return r;
+}
+
+// The dimension that lane `l` (0 .. 127) of half mh of O^T holds.
+template <int D> __device__ __forceinline__ int o_dim(int l, int mh)
+{
+    const int w = l >> 5, r = l & 15, j = (l >> 4) & 1;
+    if constexpr (D == 256) return 64 * w + 4 * r + 2 * mh + j;
+    return 32 * w + 4 * (r & 7) + 2 * j + (r >> 3);
+}
+
+template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32, 1) attn_kv4_kernel(const AttnArgs a)
 {
     using F = Kv4<D>;
-    constexpr int kStages = AttnCfg<D>::kStages;
-    constexpr int KW = D / 32;  // 4-byte words of a K row a lane holds
-    constexpr int NT = D / 8;   // n tiles of O
-    constexpr int VW = D / 64;  // 4-byte words of a V row a lane holds
+    using C = Cfg<D, N>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t bars[kAttnWarps * kStages];
-    __shared__ int tile_ok[kAttnWarps][kStages];
-    __shared__ Cursor ahead[kAttnWarps];  // where lane 0's copies are
-    __shared__ float2 wstat[kAttnWarps][kRows];
-    __shared__ int64_t scan[kAttnWarps + 1];
-    __shared__ Cursor found;
-    __shared__ int found_item0;
-
+    __shared__ __align__(16) Small<N> sm;
+    static_assert(offsetof(Small<N>, base) % 16 == 0 && offsetof(Small<N>, lim) % 16 == 0, "read four at a time");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = lane >> 2, t4 = lane & 3;
     const int cta = blockIdx.x, grid = gridDim.x;
-    uint8_t *ring = smem + warp * kStages * F::kBlock;
-    const uint32_t bar0 = smem_u32(bars) + warp * kStages * 8;
-    float *join = reinterpret_cast<float *>(smem + AttnSmem<D>::kRing);
+    constexpr int kProducer = C::kWarps - 2, kIssuer = C::kWarps - 1;
 
-    if (lane == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(bar0 + 8 * i, 1);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(smem_u32(&sm.ring_full[i]), 1);
+            mbar_init(smem_u32(&sm.ring_empty[i]), 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sm.k_full[i]), 4);
+            mbar_init(smem_u32(&sm.k_empty[i]), 1);
+            mbar_init(smem_u32(&sm.v_full[i]), 4);
+            mbar_init(smem_u32(&sm.v_empty[i]), 1);
+            mbar_init(smem_u32(&sm.s_full[i]), 1);
+            mbar_init(smem_u32(&sm.s_empty[i]), 4 * C::kSoft);
+            mbar_init(smem_u32(&sm.p_full[i]), 4 * C::kSoft);
+            mbar_init(smem_u32(&sm.p_empty[i]), 1);
+        }
+        mbar_init(smem_u32(&sm.q_full), 4 * C::kSoft);
+        mbar_init(smem_u32(&sm.o_full), 1);
+        mbar_init(smem_u32(&sm.o_empty), 4 * C::kSoft);
         mbar_init_fence();
+        sm.dead = 0;
+        sm.produced = 0;
     }
-    pdl_launch_dependents();
+    // Tensor memory is taken only when the kernels before are done, and the kernels after may start only when
+    // it is taken: neither then holds it while it waits for the other.
     pdl_wait();
+    if (warp == kIssuer) tmem_alloc(smem_u32(&sm.tmem), 512);
     if (cta == 0 && threadIdx.x == 0) *a.err = 0;
 
-    // The run of units of this CTA: the units of all sequences, then the sequence its first one is in.
+    // ---- the run of tiles of this CTA: the tiles of all sequences, then the sequence its first one is in
+    const int threads = C::kWarps * 32;
     int64_t total = 0;
-    for (int s0 = 0; s0 < a.nseq; s0 += kAttnWarps * 32) {
-        const int s = s0 + threadIdx.x;
-        if (s < a.nseq) {
-            const Seq q = load_seq(a, s);
-            total += seq_units(a, q);
-        }
+    for (int s = threadIdx.x; s < a.nseq; s += threads) {
+        const Seq q = load_seq<N>(a, s);
+        total += head_units<N>(a, q) * a.Hk;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) scan[warp] = total;
+    if (lane == 0) sm.scan[warp] = total;
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();
+    const uint32_t tmem = sm.tmem;
     total = 0;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) total += scan[w];
+    for (int w = 0; w < C::kWarps; ++w) total += sm.scan[w];
     const int64_t per = (total + grid - 1) / grid;
     const int64_t begin = per * cta < total ? per * cta : total;
     const int64_t end = begin + per < total ? begin + per : total;
-    if (begin == end) {
+    const int count = (int)(end - begin);
+    if (count == 0) {
         if (threadIdx.x == 0 && !a.by_item) a.cut[cta] = make_int4(0, 0, 0, 0);
         if (cta == 0 && a.by_item)
-            for (int i = threadIdx.x; i < grid; i += blockDim.x) a.cut[i] = make_int4(0, 0, 0, 0);
-        return;
-    }
-    {
+            for (int i = threadIdx.x; i < grid; i += threads) a.cut[i] = make_int4(0, 0, 0, 0);
+    } else {
         int64_t base = 0;
-        int items = 0;  // items of the sequences before
-        for (int s0 = 0; s0 < a.nseq; s0 += kAttnWarps * 32) {
+        int items = 0;
+        for (int s0 = 0; s0 < a.nseq; s0 += threads) {
             const int s = s0 + threadIdx.x;
             Seq q = {};
-            if (s < a.nseq) q = load_seq(a, s);
-            const int64_t u = s < a.nseq ? seq_units(a, q) : 0;
+            int64_t hu = 0;
+            if (s < a.nseq) {
+                q = load_seq<N>(a, s);
+                hu = head_units<N>(a, q);
+            }
+            const int64_t u = hu * a.Hk;
+            const int it = q.tiles * a.Hk;
             int64_t up = u;
-            int it = q.tiles * a.Hk, itp = it;
+            int itp = it;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t v = __shfl_up_sync(0xffffffffu, up, o);
@@ -247,343 +391,542 @@ template <int D> __global__ void __launch_bounds__(kAttnWarps * 32, AttnCfg<D>::
                 }
             }
             __syncthreads();
-            __shared__ int iscan[kAttnWarps];
             if (lane == 31) {
-                scan[warp] = up;
-                iscan[warp] = itp;
+                sm.scan[warp] = up;
+                sm.iscan[warp] = itp;
             }
             __syncthreads();
             int64_t before = base + up - u;
             int ibefore = items + itp - it;
-            for (int w = 0; w < kAttnWarps; ++w) {
+            for (int w = 0; w < C::kWarps; ++w) {
                 if (w < warp) {
-                    before += scan[w];
-                    ibefore += iscan[w];
+                    before += sm.scan[w];
+                    ibefore += sm.iscan[w];
                 }
-                base += scan[w];
-                items += iscan[w];
+                base += sm.scan[w];
+                items += sm.iscan[w];
             }
             if (begin >= before && begin < before + u) {
                 Cursor c;
                 c.q = q;
                 c.s = s;
-                c.item = (int)((begin - before) / q.units);
-                c.unit = (int)((begin - before) % q.units);
-                found = c;
-                found_item0 = ibefore;
+                int64_t rest = begin - before;
+                c.head = (int)(rest / hu);
+                rest -= c.head * hu;
+                c.rt = 0;
+                c.units = item_units<N>(a, q, 0);
+                while (rest >= c.units) {
+                    rest -= c.units;
+                    c.units = item_units<N>(a, q, ++c.rt);
+                }
+                c.unit = (int)rest;
+                sm.found = c;
+                sm.found_item = ibefore + c.head * q.tiles + c.rt;
             }
         }
-        __syncthreads();
         // the join looks at every entry that the argument sizes allow for
         if (cta == 0 && a.by_item)
-            for (int i = items + (int)threadIdx.x; i < grid; i += blockDim.x) a.cut[i] = make_int4(0, 0, 0, 0);
+            for (int i = items + (int)threadIdx.x; i < grid; i += threads) a.cut[i] = make_int4(0, 0, 0, 0);
+        __syncthreads();
     }
-    Cursor cur = found;
-    int item_no = found_item0 + cur.item;  // number of the item among all
-    const int count = (int)(end - begin);
 
-    // Copies: lane 0 walks the same run, kStages - 1 units ahead.
-    int issued = 0;
-    if (lane == 0) ahead[warp] = cur;
-    auto issue = [&]() {  // lane 0 only
-        if (issued >= count) return;
-        Cursor &c = ahead[warp];
-        const int stage = issued % kStages;
-        const int pos = c.unit * kUnit + warp * kKvBlock;
-        const int head = c.item / c.q.tiles;
-        int64_t pg = -1;
-        const int pi = pos / a.page;
-        if (pos < c.q.len) pg = a.table[(int64_t)c.s * a.width + pi];
-        const bool ok = pg >= 0 && pg < a.pages;
-        tile_ok[warp][stage] = ok;
-        const uint32_t bar = bar0 + 8 * stage;
-        mbar_arrive_expect_tx(bar, ok ? F::kBlock : 0);
-        if (ok) {
-            const int64_t blk = (pg * a.Hk + head) * (a.page / kKvBlock) + (pos - pi * a.page) / kKvBlock;
-            bulk_g2s_plain(smem_u32(ring + stage * F::kBlock), a.cache + blk * F::kBlock, F::kBlock, bar);
+    int *dead = &sm.dead;
+    if (warp == kProducer) {
+        // ---- copies and descriptions of the tiles
+        Cursor c = sm.found;
+        int item = sm.found_item;
+        bool any_cut = false, from_start = false;
+        for (int i = 0; i < count; ++i) {
+            const int st = i % C::kStages;
+            if (i >= C::kStages) wait(&sm.ring_empty[st], ((i / C::kStages) & 1) ^ 1, dead, a.err);
+            if (*(volatile int *)dead) break;
+            const int pos = c.unit * kTile;
+            const bool first = i == 0 || c.unit == 0;
+            if (first) from_start = c.unit == 0;
+            const bool whole_end = c.unit + 1 == c.units;
+            const bool last = whole_end || i + 1 == count;
+            const bool complete = whole_end && from_start;
+            // a lane looks up a block's page
+            const int p = pos + lane * kKvBlock;
+            int64_t pg = -1;
+            int in_page = 0;
+            if (lane < kTileBlocks && p < c.q.len) {
+                const int pi = p / a.page;
+                in_page = p - pi * a.page;
+                pg = a.table[(int64_t)c.s * a.width + pi];
+            }
+            const bool ok = pg >= 0 && pg < a.pages;
+            const uint32_t valid = __ballot_sync(0xffffffffu, ok);
+            const uint32_t bar = smem_u32(&sm.ring_full[st]);
+            if (lane == 0) {
+                Meta &m = sm.meta[i % kMetas];
+                const int left = c.units - c.unit - 1;
+                m.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (from_start ? kFromStart : 0) | (complete ? kComplete : 0);
+                m.valid = valid;
+                m.pos = pos;
+                m.first = c.q.first;
+                m.n = c.q.n;
+                m.len = c.q.len;
+                m.s = c.s;
+                m.head = c.head;
+                m.rt = c.rt;
+                m.item = item;
+                asm volatile("st.release.cta.shared.s32 [%0], %1;" ::"r"(smem_u32(&sm.produced)), "r"(i + 1) : "memory");
+                mbar_arrive_expect_tx(bar, __popc(valid) * F::kBlock);
+                if (last && from_start) {
+                    const int4 e = complete ? make_int4(0, 0, 0, 0)
+                                            : make_int4(c.s, c.head | (cta << 16), c.rt, (int)(1 + (left + per - 1) / per));
+                    if (a.by_item) {
+                        if (item < grid) a.cut[item] = e;
+                    } else if (!complete) {
+                        a.cut[cta] = e;
+                        any_cut = true;
+                    }
+                }
+            }
+            __syncwarp();
+            if (ok) {
+                const int64_t blk = (pg * a.Hk + c.head) * (a.page / kKvBlock) + in_page / kKvBlock;
+                bulk_g2s_plain(smem_u32(smem + st * C::kTileBytes + lane * F::kBlock), a.cache + blk * F::kBlock, F::kBlock, bar);
+            }
+            if (++c.unit == c.units) {
+                next_item<N>(a, c);
+                ++item;
+            }
         }
-        ++issued;
-        if (++c.unit == c.q.units) next_item(a, c);
-    };
-    __syncwarp();
-    if (lane == 0)
-        for (int i = 0; i < kStages - 1; ++i) issue();
-
-    uint32_t qf[D / 16][4];
-    float o[NT][4];
-    float ref[2], sum[2];  // rows g and g + 8
-    int lim[2];            // the last place each row sees
-    bool dead = false, fresh = true;
-    bool any_cut = false;
-
-    for (int i = 0; i < count; ++i) {
-        const int head = cur.item / cur.q.tiles;
-        const int rt = cur.item - head * cur.q.tiles;
-        if (fresh) {  // a new item, or this CTA's part of it
-            fresh = false;
+        if (*(volatile int *)dead)  // copies in flight land before the shared memory is given up
+            for (int st = 0; st < C::kStages; ++st) {
+                (void)mbar_wait_bounded(smem_u32(&sm.ring_full[st]), 0);
+                (void)mbar_wait_bounded(smem_u32(&sm.ring_full[st]), 1);
+            }
+        if (lane == 0 && count > 0 && !a.by_item && !any_cut) a.cut[cta] = make_int4(0, 0, 0, 0);
+    } else if (warp == kIssuer) {
+        // ---- the matrix instructions, one thread
+        if (lane == 0) {
+            constexpr uint32_t kIdesc1 = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
+            constexpr uint32_t kIdesc2 = kIdesc1 | (1u << 16);  // B (the weights) with the query rows contiguous
+            const uint32_t qa = smem_u32(smem + C::kQ), pa = smem_u32(smem + C::kP);
+            int seg = 0;  // parts of items begun
+            auto scores = [&](int i) {
+                const int sb = i % C::kSBufs;
+                wait_described(&sm.produced, i + 1, dead, a.err);
+                if (sm.meta[i % kMetas].flags & kFirst) {
+                    wait(&sm.q_full, seg & 1, dead, a.err);
+                    ++seg;
+                }
+                if (i >= C::kSBufs) wait(&sm.s_empty[sb], ((i / C::kSBufs) & 1) ^ 1, dead, a.err);
+                for (int h = 0; h < C::kSub; ++h) {
+                    const int u = i * C::kSub + h, b = u & 1;
+                    wait(&sm.k_full[b], (u >> 1) & 1, dead, a.err);
+                    tc_fence_after();
 #pragma unroll
-            for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+                    for (int k = 0; k < D / C::kSub / 16; ++k) {
+                        const int step = h * (D / C::kSub / 16) + k;
+                        umma_f16_ts(tmem + C::kS + sb * N, tmem + C::kK + b * C::kKCols + 8 * k,
+                                    umma_desc_none(qa + step * 32 * N, 16 * N, 128), kIdesc1, step > 0);
+                    }
+                    umma_commit(smem_u32(&sm.k_empty[b]));
+                }
+                umma_commit(smem_u32(&sm.s_full[sb]));
+            };
+            if (count > 0) scores(0);
+            int done = 0;  // parts of items finished
+            for (int i = 0; i < count; ++i) {
+                const int flags = sm.meta[i % kMetas].flags;
+                if (C::kSBufs > 1 && i + 1 < count) scores(i + 1);
+                const int pb = i % C::kPBufs;
+                if ((flags & kFirst) && done > 0) wait(&sm.o_empty, (done - 1) & 1, dead, a.err);
+                wait(&sm.p_full[pb], (i / C::kPBufs) & 1, dead, a.err);
+                for (int h = 0; h < C::kSub; ++h) {
+                    const int u = i * C::kSub + h, b = u & 1;
+                    wait(&sm.v_full[b], (u >> 1) & 1, dead, a.err);
+                    tc_fence_after();
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                ref[r] = -INFINITY;
-                sum[r] = 0.0f;
-                const int row = rt * kRows + g + 8 * r;
-                const int tok = row / a.G;
-                const bool ok = tok < cur.q.n;
-                lim[r] = ok ? cur.q.len - cur.q.n + tok : -1;
-                const __half *qp = static_cast<const __half *>(a.q.p) + (int64_t)(cur.q.first + tok) * a.q.st +
-                                   (int64_t)(head * a.G + row - tok * a.G) * a.q.sh;
+                    for (int k = 0; k < C::kVTok / 16; ++k)
 #pragma unroll
-                for (int w = 0; w < KW; ++w) {
-                    const int dim = kq_dims<D>(t4, w);
-                    uint32_t v[4] = {0, 0, 0, 0};  // dimension pairs (0,1) (2,3) (4,5) (6,7)
-                    if (ok) {
-                        if (a.q.vec > 1) {
-                            const uint4 u = *reinterpret_cast<const uint4 *>(qp + dim);
-                            v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+                        for (int mh = 0; mh < C::kMh; ++mh)
+                            umma_f16_ts(tmem + C::kO + mh * N, tmem + C::kV + (b * C::kMh + mh) * C::kVCols + 8 * k,
+                                        umma_desc_none(pa + pb * C::kPBytes + (h * (C::kVTok / 16) + k) * 256, 128, 16 * kTile), kIdesc2,
+                                        !((flags & kFirst) && h == 0 && k == 0));
+                    umma_commit(smem_u32(&sm.v_empty[b]));
+                }
+                umma_commit(smem_u32(&sm.p_empty[pb]));
+                if (flags & kLast) {
+                    umma_commit(smem_u32(&sm.o_full));
+                    ++done;
+                }
+                if (C::kSBufs == 1 && i + 1 < count) scores(i + 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // ---- keys: one place a thread
+        const int t = warp * 32 + lane;
+        const int blk = t / kKvBlock, tok = t % kKvBlock;
+        const int sw = kv4_swizzle(tok) & F::kChunkMask;
+        constexpr int kChunks = D / 32 / C::kSub;  // of a buffer
+        for (int i = 0; i < count; ++i) {
+            const int st = i % C::kStages;
+            wait(&sm.ring_full[st], (i / C::kStages) & 1, dead, a.err);
+            const uint8_t *kb = smem + st * C::kTileBytes + blk * F::kBlock;
+            for (int h = 0; h < C::kSub; ++h) {
+                const int u = i * C::kSub + h, b = u & 1;
+                uint4 w[kChunks];
+                uint32_t sc[kChunks];
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const int ch = h * kChunks + c;
+                    w[c] = *reinterpret_cast<const uint4 *>(kb + tok * F::kCodeRow + ((ch ^ sw) << 4));
+                    sc[c] = *reinterpret_cast<const uint32_t *>(kb + F::kCodes + (tok * F::kGroups + (ch >> 1)) * 4);
+                }
+                if (u >= 2) {
+                    wait(&sm.k_empty[b], ((u >> 1) & 1) ^ 1, dead, a.err);
+                    tc_fence_after();
+                }
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const __half2 d = __low2half2(as_h2(sc[c])), m = __high2half2(as_h2(sc[c]));
+                    const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                    uint32_t r[16];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t x8 = x[e] >> 8;
+                        r[4 * e] = dequant_lo(x[e], d, m);
+                        r[4 * e + 1] = dequant_hi(x[e], d, m);
+                        r[4 * e + 2] = dequant_lo(x8, d, m);
+                        r[4 * e + 3] = dequant_hi(x8, d, m);
+                    }
+                    tmem_st_32x32b(tmem + ((uint32_t)(warp * 32) << 16) + C::kK + b * C::kKCols + 16 * c, r);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.k_full[b]));
+            }
+            if (lane == 0) mbar_arrive(smem_u32(&sm.ring_empty[st]));
+        }
+    } else if (warp < 8) {
+        // ---- values: 64 (D = 256) or 32 dimensions a warp, four nibbles of two places a register
+        const int w = warp - 4;
+        constexpr int kStep = D == 256 ? 16 : 32;  // places of one ldmatrix
+        const bool idle = D == 64 && w >= 2;       // lanes 64 .. 127 of O^T hold nothing
+        const int group = D == 256 ? w : D == 128 ? w >> 1 : 0;
+        // the row this lane addresses: place and 16-byte chunk
+        const int at = D == 256 ? (lane >> 4) * 8 + (lane & 7) : lane;
+        const int chunk = D == 256 ? 2 * w + ((lane >> 3) & 1) : w & F::kChunkMask;
+        for (int i = 0; i < count; ++i) {
+            const int st = i % C::kStages;
+            wait(&sm.ring_full[st], (i / C::kStages) & 1, dead, a.err);
+            const Meta &m = sm.meta[i % kMetas];
+            const int valid = m.valid, room = m.len - m.pos;  // places of the tile that are there
+            const bool edge = valid != (1 << kTileBlocks) - 1 || room < kTile;
+            const uint8_t *vb = smem + st * C::kTileBytes + F::kPart;
+            for (int h = 0; h < C::kSub; ++h) {
+                const int u = i * C::kSub + h, b = u & 1;
+                if (u >= 2) {
+                    wait(&sm.v_empty[b], ((u >> 1) & 1) ^ 1, dead, a.err);
+                    tc_fence_after();
+                }
+                if (!idle) {
+#pragma unroll
+                    for (int p = 0; p < C::kVTok; p += kStep) {
+                        const int p0 = h * C::kVTok + p;
+                        uint32_t x[4];
+                        {
+                            const int pl = p0 + at, tok = pl % kKvBlock;
+                            ldmatrix_x4_trans(smem_u32(vb + (pl / kKvBlock) * F::kBlock + tok * F::kCodeRow +
+                                                       ((chunk ^ (kv4_swizzle(tok) & F::kChunkMask)) << 4)),
+                                              x);
+                        }
+                        // (d, m) of this thread's two places of each group of eight
+                        __half2 dd[kStep / 8], mm[kStep / 8];
+#pragma unroll
+                        for (int e = 0; e < kStep / 8; ++e) {
+                            const int pl = p0 + 8 * e + 2 * (lane & 3), tok = pl % kKvBlock;
+                            const uint8_t *sp = vb + (pl / kKvBlock) * F::kBlock + F::kCodes + (tok * F::kGroups + group) * 4;
+                            uint32_t s0 = *reinterpret_cast<const uint32_t *>(sp);
+                            uint32_t s1 = *reinterpret_cast<const uint32_t *>(sp + F::kGroups * 4);
+                            if (edge) {  // places that are not there hold anything, NaN among it
+                                const bool there = (valid >> (pl / kKvBlock)) & 1;
+                                if (!there || pl >= room) s0 = 0;
+                                if (!there || pl + 1 >= room) s1 = 0;
+                            }
+                            dd[e] = as_h2(__byte_perm(s0, s1, 0x5410));
+                            mm[e] = as_h2(__byte_perm(s0, s1, 0x7632));
+                        }
+                        const uint32_t col = tmem + ((uint32_t)(w * 32) << 16) + C::kV + b * C::kMh * C::kVCols + p / 2;
+                        uint32_t r[4][4];  // by nibble
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int g = D == 256 ? e >> 1 : e;
+                            const uint32_t x8 = x[e] >> 8;
+                            r[0][e] = dequant_lo(x[e], dd[g], mm[g]);
+                            r[1][e] = dequant_hi(x[e], dd[g], mm[g]);
+                            r[2][e] = dequant_lo(x8, dd[g], mm[g]);
+                            r[3][e] = dequant_hi(x8, dd[g], mm[g]);
+                        }
+                        if constexpr (D == 256) {
+                            // registers: (chunk 2w, 2w + 1) of places 0-7, then of places 8-15
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                tmem_st_16x128b_x2(col + ((uint32_t)(16 * (j & 1)) << 16) + (j >> 1) * C::kVCols, r[j]);
                         } else {
+                            // nibbles 2q and 2q + 1 in lanes 0-7 and 8-15 of a group of 16
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                v[e] = as_u32(__halves2half2(qp[(dim + 2 * e) * a.q.sd], qp[(dim + 2 * e + 1) * a.q.sd]));
+                            for (int q = 0; q < 2; ++q) {
+                                const uint32_t y[8] = {r[2 * q][0], r[2 * q + 1][0], r[2 * q][1], r[2 * q + 1][1],
+                                                       r[2 * q][2], r[2 * q + 1][2], r[2 * q][3], r[2 * q + 1][3]};
+                                tmem_st_16x128b_x4(col + ((uint32_t)(16 * q) << 16), y);
+                            }
                         }
                     }
-                    // the pairs that the nibbles of a word come in: (0,4) (1,5) (2,6) (3,7)
-                    qf[2 * w][r] = __byte_perm(v[0], v[2], 0x5410);
-                    qf[2 * w][2 + r] = __byte_perm(v[0], v[2], 0x7632);
-                    qf[2 * w + 1][r] = __byte_perm(v[1], v[3], 0x5410);
-                    qf[2 * w + 1][2 + r] = __byte_perm(v[1], v[3], 0x7632);
+                    tmem_wait_st();
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.v_full[b]));
             }
+            if (lane == 0) mbar_arrive(smem_u32(&sm.ring_empty[st]));
         }
-        const int stage = i % kStages;
-        if (lane == 0) issue();  // into the stage that the previous tile left
-        if (!dead && !mbar_wait_bounded(bar0 + 8 * stage, (uint32_t)((i / kStages) & 1))) {
-            dead = true;
-            if (lane == 0) *a.err = 1;
-        }
-        const int pos = cur.unit * kUnit + warp * kKvBlock;
-        // the last place that any row of the item sees
-        const int tmax = min(cur.q.n - 1, (rt * kRows + kRows - 1) / a.G);
-        const int seen = cur.q.len - cur.q.n + tmax;
-        if (!dead && pos <= seen && tile_ok[warp][stage]) {
-            const uint8_t *kb = ring + stage * F::kBlock;
-            const uint8_t *vb = kb + F::kPart;
-            const bool masked = pos + kKvBlock - 1 > cur.q.len - cur.q.n + (rt * kRows) / a.G;
-            // S = Q K^T: n tile j holds places 8 j .. 8 j + 7, two accumulator chains each
-            float sc[2][2][4];
+    } else {
+        // ---- softmax: one place a thread, kNS query rows; and q in, O out
+        constexpr int NS = C::kNS;
+        constexpr int NC = NS < 32 ? NS : 32;    // query rows worked at once
+        const int wg = (warp - 8) >> 2;          // softmax warpgroup
+        const int n0 = wg * NS;                  // its first query row
+        const int w = (warp - 8) & 3;            // tensor-memory quadrant
+        const int t = w * 32 + lane;
+        const int bar_id = 1 + wg;
+        const uint32_t quad = tmem + ((uint32_t)(w * 32) << 16);
+        float sum[NS];
+        int seg = 0;
+        float *stage = reinterpret_cast<float *>(smem + C::kP) + wg * C::kOutRows * C::kOutStride;
+        // Stages q of an item, rows of other items at zero; k index in the order that the codes are unpacked in.
+        auto stage_q = [&](const Meta &m) {
+            const int64_t row0 = (int64_t)m.rt * N;
+            for (int x = t; x < NS * (D / 8); x += 128) {
+                const int n = n0 + x % NS, g = x / NS;
+                const int64_t row = row0 + n;
+                const int tok = (int)(row / a.G);
+                uint32_t v[4] = {0, 0, 0, 0};
+                if (tok < m.n) {
+                    const __half *qp = static_cast<const __half *>(a.q.p) + (int64_t)(m.first + tok) * a.q.st +
+                                       (int64_t)(m.head * a.G + (int)(row - (int64_t)tok * a.G)) * a.q.sh;
+                    if (a.q.vec > 1) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(qp + 8 * g);
+                        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+                    } else {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[j][0][e] = sc[j][1][e] = 0.0f;
-                const int tok = g + 8 * j;
-                const int sw = kv4_swizzle(tok) & F::kChunkMask;
-                uint32_t w[KW];
-                __half2 d[2], m[2];
-                if constexpr (D == 256) {
-                    lds_words<4>(kb + tok * F::kCodeRow + ((t4 ^ sw) << 4), w);
-                    lds_words<4>(kb + tok * F::kCodeRow + (((t4 + 4) ^ sw) << 4), w + 4);
-                    const uint32_t s0 = lds32(kb + F::kCodes + (tok * F::kGroups + (t4 >> 1)) * 4);
-                    const uint32_t s1 = lds32(kb + F::kCodes + (tok * F::kGroups + 2 + (t4 >> 1)) * 4);
-                    d[0] = __low2half2(as_h2(s0)), m[0] = __high2half2(as_h2(s0));
-                    d[1] = __low2half2(as_h2(s1)), m[1] = __high2half2(as_h2(s1));
-                } else if constexpr (D == 128) {
-                    lds_words<4>(kb + tok * F::kCodeRow + ((t4 ^ sw) << 4), w);
-                    const uint32_t s0 = lds32(kb + F::kCodes + (tok * F::kGroups + (t4 >> 1)) * 4);
-                    d[0] = d[1] = __low2half2(as_h2(s0)), m[0] = m[1] = __high2half2(as_h2(s0));
-                } else {
-                    lds_words<2>(kb + tok * F::kCodeRow + (((t4 >> 1) ^ sw) << 4) + (t4 & 1) * 8, w);
-                    const uint32_t s0 = lds32(kb + F::kCodes + tok * F::kGroups * 4);
-                    d[0] = d[1] = __low2half2(as_h2(s0)), m[0] = m[1] = __high2half2(as_h2(s0));
-                }
-#pragma unroll
-                for (int k = 0; k < KW; ++k) {
-                    const __half2 dd = d[k >> 2], mm = m[k >> 2];
-                    const uint32_t w8 = w[k] >> 8;
-                    mma16816(sc[j][0], qf[2 * k][0], qf[2 * k][1], qf[2 * k][2], qf[2 * k][3], dequant_lo(w[k], dd, mm),
-                             dequant_hi(w[k], dd, mm));
-                    mma16816(sc[j][1], qf[2 * k + 1][0], qf[2 * k + 1][1], qf[2 * k + 1][2], qf[2 * k + 1][3],
-                             dequant_lo(w8, dd, mm), dequant_hi(w8, dd, mm));
-                }
-            }
-            float s[2][4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[j][e] = (sc[j][0][e] + sc[j][1][e]) * a.scale_log2;
-            if (masked) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (pos + 8 * j + 2 * t4 + (e & 1) > lim[e >> 1]) s[j][e] = -INFINITY;
-            }
-            float top[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-            if (__any_sync(0xffffffffu, top[0] > ref[0] + kMoveMax || top[1] > ref[1] + kMoveMax)) {
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float t = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                    t = fmaxf(t, ref[r]);
-                    const float f = t == -INFINITY ? 1.0f : ex2(ref[r] - t);
-                    ref[r] = t;
-                    sum[r] *= f;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        o[n][2 * r] *= f;
-                        o[n][2 * r + 1] *= f;
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = as_u32(__halves2half2(qp[(8 * g + 2 * e) * a.q.sd], qp[(8 * g + 2 * e + 1) * a.q.sd]));
                     }
                 }
+                *reinterpret_cast<uint4 *>(smem + C::kQ + g * 16 * N + (n >> 3) * 128 + (n & 7) * 16) =
+                    make_uint4(__byte_perm(v[0], v[2], 0x5410), __byte_perm(v[0], v[2], 0x7632), __byte_perm(v[1], v[3], 0x5410),
+                               __byte_perm(v[1], v[3], 0x7632));
             }
-            uint32_t p[4];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float base = (ref[r] == -INFINITY ? 0.0f : ref[r]) - kWeightShift;
-                float e[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    e[x] = ex2(s[x >> 1][2 * r + (x & 1)] - base);
-                    sum[r] += e[x];
-                }
-                p[r] = pack_h2(e[0], e[1]);
-                p[2 + r] = pack_h2(e[2], e[3]);
+            for (int n = t; n < NS; n += 128) {
+                const int tok = (int)((row0 + n0 + n) / a.G);
+                sm.lim[n0 + n] = tok < m.n ? m.len - m.n + tok : -1;
             }
-            // O += P V: the k index is the place, 2 t4 + {0, 1} and 8 more; word i of a lane's V
-            // row holds n tiles 8 i .. 8 i + 7 of column g
-            uint32_t w[4][VW];
-            uint32_t sv[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int tok = 2 * t4 + (x & 1) + 8 * (x >> 1);
-                const int sw = kv4_swizzle(tok) & F::kChunkMask;
-                const int dim = (D / 8) * g;
-                lds_words<VW>(vb + tok * F::kCodeRow + (((dim >> 5) ^ sw) << 4) + ((dim & 31) >> 1), w[x]);
-                sv[x] = lds32(vb + F::kCodes + (tok * F::kGroups + dim / kKvGroup) * 4);
-                // places past the sequence hold anything, NaN among it
-                if (masked && pos + tok >= cur.q.len) sv[x] = 0;
-            }
-            const __half2 d0 = as_h2(__byte_perm(sv[0], sv[1], 0x5410)), m0 = as_h2(__byte_perm(sv[0], sv[1], 0x7632));
-            const __half2 d1 = as_h2(__byte_perm(sv[2], sv[3], 0x5410)), m1 = as_h2(__byte_perm(sv[2], sv[3], 0x7632));
-#pragma unroll
-            for (int v = 0; v < VW; ++v) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t sel = half ? 0x7632 : 0x5410;
-                    const uint32_t x = __byte_perm(w[0][v], w[1][v], sel), y = __byte_perm(w[2][v], w[3][v], sel);
-                    const uint32_t x8 = x >> 8, y8 = y >> 8;
-                    const int n = 8 * v + 4 * half;
-                    mma16816(o[n], p[0], p[1], p[2], p[3], dequant_lo(x, d0, m0), dequant_lo(y, d1, m1));
-                    mma16816(o[n + 1], p[0], p[1], p[2], p[3], dequant_hi(x, d0, m0), dequant_hi(y, d1, m1));
-                    mma16816(o[n + 2], p[0], p[1], p[2], p[3], dequant_lo(x8, d0, m0), dequant_lo(y8, d1, m1));
-                    mma16816(o[n + 3], p[0], p[1], p[2], p[3], dequant_hi(x8, d0, m0), dequant_hi(y8, d1, m1));
-                }
-            }
+            fence_proxy_async_smem();
+            bar_sync(bar_id, 128);
+            if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+        };
+        if (count > 0) {
+            wait_described(&sm.produced, 1, dead, a.err);
+            stage_q(sm.meta[0]);
         }
-        __syncwarp();  // every lane has read the stage before lane 0 fills it again
-        const bool whole_end = cur.unit + 1 == cur.q.units;
-        if (whole_end || i + 1 == count) {
-            // ---- end of this CTA's part of the item: join the warps
-            const bool from_start = cur.unit + 1 <= i + 1;  // unit 0 was in this run
-            const bool complete = whole_end && from_start;
+        for (int i = 0; i < count; ++i) {
+            const int sb = i % C::kSBufs, pb = i % C::kPBufs;
+            wait(&sm.s_full[sb], (i / C::kSBufs) & 1, dead, a.err);
+            tc_fence_after();
+            const Meta m = sm.meta[i % kMetas];
+            const bool first = m.flags & kFirst;
+            if (first) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-                sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-                if (t4 == 0) wstat[warp][g + 8 * r] = make_float2(ref[r], sum[r]);
+                for (int n = 0; n < NS; ++n) sum[n] = 0.0f;
             }
-            __syncthreads();
-            float f[2];
+            const int pos = m.pos + t;
+            const bool there = ((m.valid >> (t / kKvBlock)) & 1) && pos < m.len;
+            const bool edge = m.valid != (1 << kTileBlocks) - 1 || m.pos + kTile > m.len - m.n + (int)(((int64_t)m.rt * N) / a.G) + 1;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float t = -INFINITY;
+            for (int c = 0; c < NS; c += NC) {
+                const int nc = n0 + c;
+                float s[NC];
+                TmemRead<NC>::run(quad + C::kS + sb * N + nc, s);
+                if (c + NC == NS) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty[sb]));
+                }
+                if (edge) {
 #pragma unroll
-                for (int w = 0; w < kAttnWarps; ++w) t = fmaxf(t, wstat[w][g + 8 * r].x);
-                f[r] = ref[r] == -INFINITY ? 0.0f : ex2(ref[r] - t);
-            }
-            // the thread's element of the joined tile: a row and D / 8 dimensions of it
-            const int jr = threadIdx.x >> 3, jn = threadIdx.x & 7;
-            float top = -INFINITY, den = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) top = fmaxf(top, wstat[w][jr].x);
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) {
-                const float2 st = wstat[w][jr];
-                if (st.x != -INFINITY) den += st.y * ex2(st.x - top);
-            }
-            const float inv = den > 0.0f ? 1.0f / den : 0.0f;
-            const int row = rt * kRows + jr;
-            const int tok = row / a.G;
-            const bool row_ok = tok < cur.q.n;
-            const int slot = 2 * cta + (from_start ? 1 : 0);
-#pragma unroll
-            for (int c = 0; c < NT / 8; ++c) {
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float *dst = join + ((warp * kRows) + g + 8 * r) * kJoinStride + (2 * t4 + e) * 8;
-#pragma unroll
-                        for (int h = 0; h < 8; h += 4)
-                            *reinterpret_cast<float4 *>(dst + h) =
-                                make_float4(o[8 * c + h][2 * r + e] * f[r], o[8 * c + h + 1][2 * r + e] * f[r],
-                                            o[8 * c + h + 2][2 * r + e] * f[r], o[8 * c + h + 3][2 * r + e] * f[r]);
-                    }
-                __syncthreads();
-                float v[8] = {};
-#pragma unroll
-                for (int w = 0; w < kAttnWarps; ++w) {
-                    const float *src = join + (w * kRows + jr) * kJoinStride + jn * 8;
-#pragma unroll
-                    for (int h = 0; h < 8; h += 4) {
-                        const float4 x = *reinterpret_cast<const float4 *>(src + h);
-                        v[h] += x.x, v[h + 1] += x.y, v[h + 2] += x.z, v[h + 3] += x.w;
+                    for (int n = 0; n < NC; n += 4) {
+                        const int4 l = *reinterpret_cast<const int4 *>(&sm.lim[nc + n]);
+                        if (!there || pos > l.x) s[n] = -INFINITY;
+                        if (!there || pos > l.y) s[n + 1] = -INFINITY;
+                        if (!there || pos > l.z) s[n + 2] = -INFINITY;
+                        if (!there || pos > l.w) s[n + 3] = -INFINITY;
                     }
                 }
-                const int dim = (D / 8) * jn + 8 * c;
-                if (complete) {
-                    if (row_ok) {
+                bool move = first;
+                if (!first) {
+                    float over = -INFINITY;
 #pragma unroll
-                        for (int h = 0; h < 8; ++h) v[h] *= inv;
-                        store_dims<8>(a.out, cur.q.first + tok, head * a.G + row - tok * a.G, dim, v);
+                    for (int n = 0; n < NC; n += 4) {
+                        const float4 b = *reinterpret_cast<const float4 *>(&sm.base[nc + n]);
+                        over = fmaxf(over, fmaf(s[n], a.scale_log2, -b.x));
+                        over = fmaxf(over, fmaf(s[n + 1], a.scale_log2, -b.y));
+                        over = fmaxf(over, fmaf(s[n + 2], a.scale_log2, -b.z));
+                        over = fmaxf(over, fmaf(s[n + 3], a.scale_log2, -b.w));
                     }
-                } else {
-                    float *dst = a.part + ((int64_t)slot * kRows + jr) * D + dim;
+                    move = over > kMoveMax + kWeightShift;
+                }
+                if (bar_or(bar_id, 128, move)) {
+                    // the rows' maxima over the 128 places; O and the sums follow the reference
 #pragma unroll
-                    for (int h = 0; h < 8; h += 4) *reinterpret_cast<float4 *>(dst + h) = make_float4(v[h], v[h + 1], v[h + 2], v[h + 3]);
+                    for (int n = 0; n < NC; ++n) {
+                        const int top = __reduce_max_sync(0xffffffffu, float_order(s[n] * a.scale_log2));
+                        if (lane == 0) sm.wred[wg * 4 + w][n] = order_float(top);
+                    }
+                    bar_sync(bar_id, 128);
+                    if (t < NC) {
+                        const float old = first ? -INFINITY : sm.ref[nc + t];
+                        float top = old;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) top = fmaxf(top, sm.wred[wg * 4 + x][t]);
+                        if (sm.lim[nc + t] < 0) top = fmaxf(top, 0.0f);  // a row that sees nothing stays out of this
+                        sm.ref[nc + t] = top;
+                        // a row that has seen nothing yet moves at its first score
+                        sm.base[nc + t] = top == -INFINITY ? -1e30f : top - kWeightShift;
+                        sm.factor[nc + t] = top == -INFINITY ? 1.0f : ex2(old - top);
+                    }
+                    bar_sync(bar_id, 128);
+                    if (!first) {
+#pragma unroll
+                        for (int n = 0; n < NC; ++n) sum[c + n] *= sm.factor[nc + n];
+                        // every product before this tile is in O
+                        wait(&sm.p_empty[(i - 1) % C::kPBufs], ((i - 1) / C::kPBufs) & 1, dead, a.err);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int x = 0; x < C::kMh * NC; x += 16) {
+                            const uint32_t at = quad + C::kO + (x / NC) * N + nc + x % NC;
+                            float o[16];
+                            uint32_t r[16];
+                            TmemRead<16>::run(at, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e] * sm.factor[nc + x % NC + e]);
+                            tmem_st_32x32b(at, r);
+                        }
+                        tmem_wait_st();
+                        tc_fence_before();
+                    }
                 }
-                __syncthreads();
-            }
-            if (!complete && jn == 0) a.stat[slot * kRows + jr] = make_float2(top, den);
-            if (from_start && threadIdx.x == 0) {
-                const int left = cur.q.units - cur.unit - 1;  // units of the item in the CTAs after this one
-                const int4 c = complete ? make_int4(0, 0, 0, 0)
-                                        : make_int4(cur.s, head, rt, (int)(1 + (left + per - 1) / per));
-                if (a.by_item) {
-                    if (item_no < grid) a.cut[item_no] = make_int4(c.x, c.y | (cta << 16), c.z, c.w);
-                } else if (!complete) {
-                    a.cut[cta] = make_int4(c.x, c.y | (cta << 16), c.z, c.w);
-                    any_cut = true;
+                if (c == 0 && i >= C::kPBufs) wait(&sm.p_empty[pb], ((i / C::kPBufs) & 1) ^ 1, dead, a.err);
+                uint8_t *pp = smem + C::kP + pb * C::kPBytes + (nc >> 3) * (16 * kTile) + (t >> 3) * 128 + (t & 7) * 16;
+#pragma unroll
+                for (int n = 0; n < NC; n += 8) {
+                    const float4 b0 = *reinterpret_cast<const float4 *>(&sm.base[nc + n]);
+                    const float4 b1 = *reinterpret_cast<const float4 *>(&sm.base[nc + n + 4]);
+                    const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+                    float e[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        e[x] = ex2(fmaf(s[n + x], a.scale_log2, -b[x]));
+                        sum[c + n + x] += e[x];
+                    }
+                    *reinterpret_cast<uint4 *>(pp + (n >> 3) * (16 * kTile)) =
+                        make_uint4(pack_h2(e[0], e[1]), pack_h2(e[2], e[3]), pack_h2(e[4], e[5]), pack_h2(e[6], e[7]));
                 }
             }
-            fresh = true;
-        }
-        if (++cur.unit == cur.q.units) {
-            next_item(a, cur);
-            ++item_no;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[pb]));
+            if (m.flags & kLast) {
+                // q of the next item while the last products run (all first products of this one are done:
+                // their scores have been read)
+                if (C::kSoft > 1) bar_sync(3, 256);  // both warpgroups have
+                if (i + 1 < count) {
+                    wait_described(&sm.produced, i + 2, dead, a.err);
+                    stage_q(sm.meta[(i + 1) % kMetas]);
+                }
+                // ---- the sums over the places
+#pragma unroll
+                for (int c = 0; c < NS; c += 16) {
+                    float v[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = sum[c + e];
+                    const float r = reduce_scatter<16>(v, lane);
+                    if (lane < 16) sm.wred[wg * 4 + w][c + lane] = r;
+                }
+                bar_sync(bar_id, 128);
+                const int slot = 2 * cta + ((m.flags & kFromStart) ? 1 : 0);
+                const bool complete = m.flags & kComplete;
+                for (int n = t; n < NS; n += 128) {
+                    const float den = (sm.wred[wg * 4][n] + sm.wred[wg * 4 + 1][n]) + (sm.wred[wg * 4 + 2][n] + sm.wred[wg * 4 + 3][n]);
+                    sm.inv[n0 + n] = complete ? (den > 0.0f ? 1.0f / den : 0.0f) : 1.0f;
+                    if (!complete) a.stat[(int64_t)slot * N + n0 + n] = make_float2(sm.ref[n0 + n], den);
+                }
+                wait(&sm.o_full, seg & 1, dead, a.err);
+                ++seg;
+                tc_fence_after();
+                bar_sync(bar_id, 128);
+                // ---- O, eight rows at a time through shared memory (the weights' buffers are free now)
+                const int64_t row0 = (int64_t)m.rt * N + n0;
+                for (int c = 0; c < NS; c += 8) {
+                    if ((row0 + c) / a.G >= m.n) break;  // no more rows
+#pragma unroll
+                    for (int mh = 0; mh < C::kMh; ++mh) {
+                        float o[8];
+                        TmemRead<8>::run(quad + C::kO + mh * N + n0 + c, o);
+                        const int dim = o_dim<D>(t, mh);
+                        if (D > 64 || t < 64) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) stage[e * C::kOutStride + dim] = o[e] * sm.inv[n0 + c + e];
+                        }
+                    }
+                    bar_sync(bar_id, 128);
+                    for (int x = t; x < 8 * (D / 8); x += 128) {
+                        const int e = x / (D / 8), g = x % (D / 8);
+                        const int64_t row = row0 + c + e;
+                        const int tok = (int)(row / a.G);
+                        const float4 v0 = *reinterpret_cast<const float4 *>(stage + e * C::kOutStride + 8 * g);
+                        const float4 v1 = *reinterpret_cast<const float4 *>(stage + e * C::kOutStride + 8 * g + 4);
+                        if (tok < m.n) {
+                            if (complete) {
+                                const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                                store_dims<8>(a.out, m.first + tok, m.head * a.G + (int)(row - (int64_t)tok * a.G), 8 * g, v);
+                            } else {
+                                float *dst = a.part + ((int64_t)slot * N + n0 + c + e) * D + 8 * g;
+                                *reinterpret_cast<float4 *>(dst) = v0;
+                                *reinterpret_cast<float4 *>(dst + 4) = v1;
+                            }
+                        }
+                    }
+                    bar_sync(bar_id, 128);
+                }
+                tc_fence_before();
+                if (C::kSoft > 1) bar_sync(3, 256);  // the other warpgroup may still read the staging area
+                if (lane == 0) mbar_arrive(smem_u32(&sm.o_empty));
+            }
         }
     }
-    if (!a.by_item && threadIdx.x == 0 && !any_cut) a.cut[cta] = make_int4(0, 0, 0, 0);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kIssuer) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
 }
 
 // The items that were cut between CTAs: out = sum_i 2^(ref_i - ref) O_i / sum_i 2^(ref_i - ref) sum_i,
 // in CTA order.  One block takes RB rows of one item; D / 4 threads share a row's dimensions and the
 // rest of its threads the parts.
-template <int D, int RB> __global__ void __launch_bounds__(256) attn_kv4_join_kernel(const AttnArgs a)
+template <int D, int N, int RB> __global__ void __launch_bounds__(256) attn_kv4_join_kernel(const AttnArgs a)
 {
-    constexpr int TX = D / 4;              // threads across a row
-    constexpr int TY = 256 / (TX * RB);    // threads that share its parts
+    constexpr int TX = D / 4;            // threads across a row
+    constexpr int TY = 256 / (TX * RB);  // threads that share its parts
     static_assert(TY >= 1, "a row's threads fit the block");
     __shared__ float4 acc[RB][TY][TX];
     __shared__ float den[RB][TY];
@@ -594,24 +937,26 @@ template <int D, int RB> __global__ void __launch_bounds__(256) attn_kv4_join_ke
     const int head = c.y & 0xffff, cta = c.y >> 16;
     const int x = threadIdx.x % TX, y = threadIdx.x / TX % TY, rl = threadIdx.x / (TX * TY);
     const int r = blockIdx.y * RB + rl;
-    const Seq q = load_seq(a, c.x);
-    const int row = c.z * kRows + r;
-    const int tok = row / a.G;
+    const Seq q = load_seq<N>(a, c.x);
+    const int64_t row = (int64_t)c.z * N + r;
+    const int tok = (int)(row / a.G);
     float top = -INFINITY;
-    for (int i = 0; i < c.w; ++i) top = fmaxf(top, a.stat[(i ? 2 * (cta + i) : 2 * cta + 1) * kRows + r].x);
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float l = 0.0f;
+    if (tok < q.n) {
+        for (int i = 0; i < c.w; ++i) top = fmaxf(top, a.stat[(int64_t)(i ? 2 * (cta + i) : 2 * cta + 1) * N + r].x);
 #pragma unroll 4
-    for (int i = y; i < c.w; i += TY) {
-        const int slot = i ? 2 * (cta + i) : 2 * cta + 1;
-        const float2 st = a.stat[slot * kRows + r];
-        const float f = st.x == -INFINITY ? 0.0f : ex2(st.x - top);
-        const float4 u = *reinterpret_cast<const float4 *>(a.part + ((int64_t)slot * kRows + r) * D + 4 * x);
-        l = fmaf(st.y, f, l);
-        v.x = fmaf(u.x, f, v.x);
-        v.y = fmaf(u.y, f, v.y);
-        v.z = fmaf(u.z, f, v.z);
-        v.w = fmaf(u.w, f, v.w);
+        for (int i = y; i < c.w; i += TY) {
+            const int64_t slot = i ? 2 * (cta + i) : 2 * cta + 1;
+            const float2 st = a.stat[slot * N + r];
+            const float f = st.x == -INFINITY ? 0.0f : ex2(st.x - top);
+            const float4 u = *reinterpret_cast<const float4 *>(a.part + (slot * N + r) * D + 4 * x);
+            l = fmaf(st.y, f, l);
+            v.x = fmaf(u.x, f, v.x);
+            v.y = fmaf(u.y, f, v.y);
+            v.z = fmaf(u.z, f, v.z);
+            v.w = fmaf(u.w, f, v.w);
+        }
     }
     acc[rl][y][x] = v;
     if (x == 0) den[rl][y] = l;
@@ -625,44 +970,57 @@ template <int D, int RB> __global__ void __launch_bounds__(256) attn_kv4_join_ke
     for (int i = 0; i < TY; ++i) l += den[rl][i];
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     const float w[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-    store_dims<4>(a.out, q.first + tok, head * a.G + row - tok * a.G, 4 * x, w);
+    store_dims<4>(a.out, q.first + tok, head * a.G + (int)(row - (int64_t)tok * a.G), 4 * x, w);
 }
 
-template <int D> int ctas(int sms) { return sms * AttnCfg<D>::kCtas; }
-
-int attn_grid(int D, int sms) { return D == 256 ? ctas<256>(sms) : D == 128 ? ctas<128>(sms) : ctas<64>(sms); }
+// Query rows of an item: the fewest columns that hold what a sequence has (by the caller's max_q), so that
+// few rows leave tensor time and shared memory to the copies; many rows share each unpacked tile.
+int rows_of(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
 struct WsLayout {
     size_t part, stat, cut, bytes;
 };
 
-WsLayout ws_layout(int D, int grid)
+WsLayout ws_layout(int D, int N, int grid)
 {
     WsLayout w;
     w.part = 256;  // the error word first
-    w.stat = w.part + (size_t)2 * grid * kRows * D * sizeof(float);
-    w.cut = w.stat + (size_t)2 * grid * kRows * sizeof(float2);
+    w.stat = w.part + (size_t)2 * grid * N * D * sizeof(float);
+    w.cut = w.stat + (size_t)2 * grid * N * sizeof(float2);
     w.bytes = w.cut + (size_t)grid * sizeof(int4);
     return w;
 }
 
-template <int D> int launch_attn(const AttnArgs &a, int grid, int64_t items, void *stream)
+template <int D, int N> int launch_attn(AttnArgs &a, int grid, int nseq, void *stream)
 {
     static std::atomic<uint64_t> raised{0};  // devices whose shared-memory limit is raised
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return QG_ERR_CUDA;
     if (dev >= 64 || !(raised.load() >> dev & 1)) {
-        if (cudaFuncSetAttribute(attn_kv4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnSmem<D>::kBytes) != cudaSuccess)
+        if (cudaFuncSetAttribute(attn_kv4_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, N>::kBytes) != cudaSuccess)
             return QG_ERR_CUDA;
         if (dev < 64) raised.fetch_or(uint64_t(1) << dev);
     }
-    int rc = launch_pdl(attn_kv4_kernel<D>, dim3(grid), dim3(kAttnWarps * 32), AttnSmem<D>::kBytes, stream, a);
+    // items at most: a row tile may be short in every sequence
+    const int64_t items = (int64_t)a.Hk * (nseq + a.T * a.G / N);
+    a.by_item = items <= grid;
+    const int rc = launch_pdl(attn_kv4_kernel<D, N>, dim3(grid), dim3(Cfg<D, N>::kWarps * 32), Cfg<D, N>::kBytes, stream, a);
     if (rc != QG_OK) return rc;
-    // no item is cut when none has more than one unit
-    if ((int64_t)a.width * a.page <= kUnit) return QG_OK;
+    // no item is cut when none has more than one tile
+    if ((int64_t)a.width * a.page <= kTile) return QG_OK;
     if (a.by_item)
-        return launch_pdl(attn_kv4_join_kernel<D, 1>, dim3((unsigned)items, kRows), dim3(256), 0, stream, a);
-    return launch_pdl(attn_kv4_join_kernel<D, 4>, dim3(grid, kRows / 4), dim3(256), 0, stream, a);
+        return launch_pdl(attn_kv4_join_kernel<D, N, 1>, dim3((unsigned)items, N), dim3(256), 0, stream, a);
+    return launch_pdl(attn_kv4_join_kernel<D, N, 4>, dim3(grid, N / 4), dim3(256), 0, stream, a);
+}
+
+template <int D> int launch_rows(AttnArgs &a, int N, int grid, int nseq, void *stream)
+{
+    switch (N) {
+    case 16: return launch_attn<D, 16>(a, grid, nseq, stream);
+    case 32: return launch_attn<D, 32>(a, grid, nseq, stream);
+    case 64: return launch_attn<D, 64>(a, grid, nseq, stream);
+    default: return launch_attn<D, 128>(a, grid, nseq, stream);
+    }
 }
 
 bool good_dim(int D) { return D == 64 || D == 128 || D == 256; }
@@ -671,11 +1029,11 @@ bool good_dim(int D) { return D == 64 || D == 128 || D == 256; }
 
 extern "C" {
 
-size_t qg_attn_kv4_workspace(int D)
+size_t qg_attn_kv4_workspace(int Hq, int Hk, int D, int max_q)
 {
     int sms = 0;
-    if (!good_dim(D) || current_sms(&sms) != QG_OK) return 0;
-    return ws_layout(D, attn_grid(D, sms)).bytes;
+    if (!good_dim(D) || Hk < 1 || Hq < Hk || Hq % Hk || Hq > QG_MAX_HEADS || max_q < 0 || current_sms(&sms) != QG_OK) return 0;
+    return ws_layout(D, rows_of((int64_t)max_q * (Hq / Hk)), sms).bytes;
 }
 
 int qg_attn_kv4(const qg_heads *q, int64_t T, int nseq, const int32_t *q_start, int max_q, int Hq, int Hk, int D,
@@ -697,8 +1055,9 @@ int qg_attn_kv4(const qg_heads *q, int64_t T, int nseq, const int32_t *q_start, 
         return QG_ERR_ALIGN;
     int sms = 0;
     if ((rc = current_sms(&sms)) != QG_OK) return rc;
-    const int grid = attn_grid(D, sms);
-    const WsLayout w = ws_layout(D, grid);
+    a.G = Hq / Hk;
+    const int N = rows_of((int64_t)max_q * a.G);
+    const WsLayout w = ws_layout(D, N, sms);
     if (workspace_bytes < w.bytes) return QG_ERR_SCRATCH;
     uint8_t *base = static_cast<uint8_t *>(workspace);
     a.err = reinterpret_cast<int *>(base);
@@ -716,14 +1075,10 @@ int qg_attn_kv4(const qg_heads *q, int64_t T, int nseq, const int32_t *q_start, 
     a.page = page;
     a.width = width;
     a.Hk = Hk;
-    a.G = Hq / Hk;
-    // items at most: a row tile may be short in every sequence
-    const int64_t items = (int64_t)Hk * (nseq + T * a.G / kRows);
-    a.by_item = items <= grid;
     switch (D) {
-    case 64: return launch_attn<64>(a, grid, items, stream);
-    case 128: return launch_attn<128>(a, grid, items, stream);
-    default: return launch_attn<256>(a, grid, items, stream);
+    case 64: return launch_rows<64>(a, N, sms, nseq, stream);
+    case 128: return launch_rows<128>(a, N, sms, nseq, stream);
+    default: return launch_rows<256>(a, N, sms, nseq, stream);
     }
 }
 

@@ -311,7 +311,7 @@ def test_attention_is_the_same_every_time_and_on_any_stream(qg):
         other = run_attention(qg, c)
     s.synchronize()
     assert torch.equal(other, first)
-    ws = torch.full((qg.qg_attn_kv4_workspace(128),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((qg.qg_attn_kv4_workspace(12, 2, 128, c["max_q"]),), 255, dtype=torch.uint8, device="cuda")
     assert torch.equal(run_attention(qg, c, workspace=ws), first)  # a workspace's contents do not matter
     assert ws[:4].view(torch.int32).item() == 0
     with pytest.raises(qg.QgError):
