@@ -44,6 +44,12 @@
 #include "qg_ptx.cuh"
 #include "qg_tcgen05.cuh"
 
+#ifndef QG_W2
+#define QG_W2 32
+#endif
+#ifndef QG_KU
+#define QG_KU 1
+#endif
 namespace {
 
 using namespace qg;
@@ -52,6 +58,7 @@ constexpr int kTile = 128;                      // places of a tile
 constexpr int kTileBlocks = kTile / kKvBlock;
 constexpr float kMoveMax = 8.0f;                // a score this far above the reference moves it
 constexpr float kWeightShift = 7.0f;
+constexpr int kKeyUnroll = QG_KU;
 constexpr int kMetas = 16;                      // tiles whose description is kept (more than any role lags)
 
 // flags of a tile
@@ -59,6 +66,9 @@ constexpr int kFirst = 1;      // first of this CTA's part of its item
 constexpr int kLast = 2;       // last of it
 constexpr int kFromStart = 4;  // the part holds the item's first tile
 constexpr int kComplete = 8;   // the part is the whole item
+constexpr int kEdge = 16;      // some row does not see some place of the tile
+constexpr int kHole = 32;      // some place of the tile is not there
+constexpr int kNext = 64;      // (of a first tile) another part follows: `next`
 
 struct AttnArgs {
     HeadsView q, out;
@@ -130,9 +140,13 @@ template <int N> __device__ __forceinline__ void next_item(const AttnArgs &a, Cu
     c.units = item_units<N>(a, c.q, c.rt);
 }
 
-// What the roles need to know of a tile.
+// What the roles need to know of a tile, and of the part of an item after its own.
+struct Item {
+    int first, n, len, head, rt;
+};
 struct Meta {
-    int flags, valid, pos, first, n, len, s, head, rt, ctas, item, pad;
+    int flags, valid, pos, room;  // valid: blocks that are there; room: places down to the sequence's end
+    Item item, next;
 };
 
 __device__ __forceinline__ uint32_t lop_and_or(uint32_t x, uint32_t m, uint32_t o)
@@ -182,43 +196,46 @@ template <int D, int N> struct Cfg {
     static constexpr int kVCols = kVTok / 2;                     // columns of it in each half
     static constexpr int kSBufs = (D == 256 && N == 128) ? 1 : 2;
     static constexpr int kPBufs = (D == 256 && N == 128) ? 1 : 2;
-    static constexpr int kSoft = N > 64 ? 2 : 1;                 // softmax warpgroups
+    static constexpr int kSoft = N > 32 ? N / 32 : 1;            // softmax warpgroups
     static constexpr int kNS = N / kSoft;                        // query rows of each
-    static constexpr int kWarps = 8 + 4 * kSoft + 2;
+    static constexpr int kWork = N <= QG_W2 ? 2 : 1;             // warpgroups for the keys, and for the values
+    static constexpr int kWarps = 4 * (2 * kWork + kSoft) + 2;
     // tensor memory columns
     static constexpr int kK = 0, kV = kK + 2 * kKCols, kS = kV + 2 * kVCols * kMh, kO = kS + kSBufs * N;
     static constexpr int kCols = kO + kMh * N;
     static_assert(kCols <= 512, "tensor memory");
     // shared memory
     static constexpr int kTileBytes = kTileBlocks * F::kBlock;
-    static constexpr int kStages = D == 256 ? (N == 128 ? 3 : 4) : D == 128 ? 6 : 8;
+    static constexpr int kStages = D == 256 ? (N >= 64 ? 3 : 4) : D == 128 ? (N == 128 ? 4 : 6) : 8;
+    static constexpr int kQBufs = (D == 256 && N == 128) ? 1 : 2;
     static constexpr int kQ = kStages * kTileBytes;
     static constexpr int kQBytes = N * D * 2;
-    static constexpr int kP = kQ + kQBytes;
+    static constexpr int kP = kQ + kQBufs * kQBytes;
     static constexpr int kPBytes = N * kTile * 2;
     static constexpr int kOutStride = D + 4;
-    static constexpr int kOutRows = 8;
+    static constexpr int kOutRows = N <= 32 ? 16 : 8;            // rows of O that pass through shared memory at once
     static constexpr int kOutBytes = kSoft * kOutRows * kOutStride * 4;
     static constexpr int kPAll = kPBufs * kPBytes > kOutBytes ? kPBufs * kPBytes : kOutBytes;
     static constexpr int kBytes = kP + kPAll;
-    static_assert(kBytes <= 224 * 1024, "shared memory");
 };
 
 template <int N> struct Small {
     uint64_t ring_full[8], ring_empty[8];
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], p_full[2], p_empty[2];
-    uint64_t q_full, o_full, o_empty;
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], p_full[2], p_empty[2], q_full[2];
+    uint64_t o_full, o_empty;
     Meta meta[kMetas];
     Cursor found;
     int found_item;
-    int64_t scan[20];
-    int iscan[20];
+    int64_t scan[32];
+    int iscan[32];
     uint32_t tmem;
-    int dead, produced;    // produced: tiles described so far
-    alignas(16) float base[N];  // reference - kWeightShift (0 in place of -inf)
+    int dead, produced;  // produced: tiles described so far
+    alignas(16) float base[N];    // reference - kWeightShift
+    alignas(16) int lim[2][N];    // last place that a row sees (of the parts of items in turn)
+    int64_t orow[2][N];           // where a row of out starts, -1: no such row
+    int64_t qrow[N];
     float ref[N];
-    alignas(16) int lim[N];     // last place that a row sees
-    float wred[8][N];      // by warp
+    float wred[4][N];             // by warp of the warpgroup
     float inv[N];
     float factor[N];
 };
@@ -308,15 +325,16 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
     using C = Cfg<D, N>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) Small<N> sm;
+    static_assert(C::kBytes + sizeof(Small<N>) <= 227 * 1024, "shared memory of a block");
     static_assert(offsetof(Small<N>, base) % 16 == 0 && offsetof(Small<N>, lim) % 16 == 0, "read four at a time");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp-uniform)
     const int cta = blockIdx.x, grid = gridDim.x;
     constexpr int kProducer = C::kWarps - 2, kIssuer = C::kWarps - 1;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(smem_u32(&sm.ring_full[i]), 1);
-            mbar_init(smem_u32(&sm.ring_empty[i]), 8);
+            mbar_init(smem_u32(&sm.ring_empty[i]), 8 * C::kWork);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.k_full[i]), 4);
@@ -327,8 +345,8 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
             mbar_init(smem_u32(&sm.s_empty[i]), 4 * C::kSoft);
             mbar_init(smem_u32(&sm.p_full[i]), 4 * C::kSoft);
             mbar_init(smem_u32(&sm.p_empty[i]), 1);
+            mbar_init(smem_u32(&sm.q_full[i]), 4 * C::kSoft);
         }
-        mbar_init(smem_u32(&sm.q_full), 4 * C::kSoft);
         mbar_init(smem_u32(&sm.o_full), 1);
         mbar_init(smem_u32(&sm.o_empty), 4 * C::kSoft);
         mbar_init_fence();
@@ -355,13 +373,13 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
     __syncthreads();
     tc_fence_after();
     pdl_launch_dependents();
-    const uint32_t tmem = sm.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
     total = 0;
     for (int w = 0; w < C::kWarps; ++w) total += sm.scan[w];
     const int64_t per = (total + grid - 1) / grid;
     const int64_t begin = per * cta < total ? per * cta : total;
     const int64_t end = begin + per < total ? begin + per : total;
-    const int count = (int)(end - begin);
+    const int count = __shfl_sync(0xffffffffu, (int)(end - begin), 0);
     if (count == 0) {
         if (threadIdx.x == 0 && !a.by_item) a.cut[cta] = make_int4(0, 0, 0, 0);
         if (cta == 0 && a.by_item)
@@ -461,16 +479,23 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
             if (lane == 0) {
                 Meta &m = sm.meta[i % kMetas];
                 const int left = c.units - c.unit - 1;
-                m.flags = (first ? kFirst : 0) | (last ? kLast : 0) | (from_start ? kFromStart : 0) | (complete ? kComplete : 0);
+                const int tok0 = (int)((uint32_t)(c.rt * N) / (uint32_t)a.G);  // the row tile's first query token
+                int flags = (first ? kFirst : 0) | (last ? kLast : 0) | (from_start ? kFromStart : 0) | (complete ? kComplete : 0);
+                if (valid != (1 << kTileBlocks) - 1 || pos + kTile > c.q.len) flags |= kHole | kEdge;
+                if (pos + kTile > c.q.len - c.q.n + tok0 + 1) flags |= kEdge;
+                if (first) {
+                    m.item = {c.q.first, c.q.n, c.q.len, c.head, c.rt};
+                    if (i + left + 1 < count) {
+                        Cursor n = c;
+                        next_item<N>(a, n);
+                        m.next = {n.q.first, n.q.n, n.q.len, n.head, n.rt};
+                        flags |= kNext;
+                    }
+                }
+                m.flags = flags;
                 m.valid = valid;
                 m.pos = pos;
-                m.first = c.q.first;
-                m.n = c.q.n;
-                m.len = c.q.len;
-                m.s = c.s;
-                m.head = c.head;
-                m.rt = c.rt;
-                m.item = item;
+                m.room = c.q.len - pos;
                 asm volatile("st.release.cta.shared.s32 [%0], %1;" ::"r"(smem_u32(&sm.produced)), "r"(i + 1) : "memory");
                 mbar_arrive_expect_tx(bar, __popc(valid) * F::kBlock);
                 if (last && from_start) {
@@ -501,17 +526,19 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
             }
         if (lane == 0 && count > 0 && !a.by_item && !any_cut) a.cut[cta] = make_int4(0, 0, 0, 0);
     } else if (warp == kIssuer) {
-        // ---- the matrix instructions, one thread
-        if (lane == 0) {
+        // ---- the matrix instructions: the warp stays together, an elected lane issues
+        {
             constexpr uint32_t kIdesc1 = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
             constexpr uint32_t kIdesc2 = kIdesc1 | (1u << 16);  // B (the weights) with the query rows contiguous
             const uint32_t qa = smem_u32(smem + C::kQ), pa = smem_u32(smem + C::kP);
             int seg = 0;  // parts of items begun
+            uint32_t qb = qa;
             auto scores = [&](int i) {
                 const int sb = i % C::kSBufs;
                 wait_described(&sm.produced, i + 1, dead, a.err);
-                if (sm.meta[i % kMetas].flags & kFirst) {
-                    wait(&sm.q_full, seg & 1, dead, a.err);
+                if (__shfl_sync(0xffffffffu, sm.meta[i % kMetas].flags, 0) & kFirst) {
+                    wait(&sm.q_full[seg % C::kQBufs], (seg / C::kQBufs) & 1, dead, a.err);
+                    qb = qa + (seg % C::kQBufs) * C::kQBytes;
                     ++seg;
                 }
                 if (i >= C::kSBufs) wait(&sm.s_empty[sb], ((i / C::kSBufs) & 1) ^ 1, dead, a.err);
@@ -522,17 +549,17 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
 #pragma unroll
                     for (int k = 0; k < D / C::kSub / 16; ++k) {
                         const int step = h * (D / C::kSub / 16) + k;
-                        umma_f16_ts(tmem + C::kS + sb * N, tmem + C::kK + b * C::kKCols + 8 * k,
-                                    umma_desc_none(qa + step * 32 * N, 16 * N, 128), kIdesc1, step > 0);
+                        umma_f16_ts_elect(tmem + C::kS + sb * N, tmem + C::kK + b * C::kKCols + 8 * k,
+                                    umma_desc_none(qb + step * 32 * N, 16 * N, 128), kIdesc1, step > 0);
                     }
-                    umma_commit(smem_u32(&sm.k_empty[b]));
+                    umma_commit_elect(smem_u32(&sm.k_empty[b]));
                 }
-                umma_commit(smem_u32(&sm.s_full[sb]));
+                umma_commit_elect(smem_u32(&sm.s_full[sb]));
             };
             if (count > 0) scores(0);
             int done = 0;  // parts of items finished
             for (int i = 0; i < count; ++i) {
-                const int flags = sm.meta[i % kMetas].flags;
+                const int flags = __shfl_sync(0xffffffffu, sm.meta[i % kMetas].flags, 0);
                 if (C::kSBufs > 1 && i + 1 < count) scores(i + 1);
                 const int pb = i % C::kPBufs;
                 if ((flags & kFirst) && done > 0) wait(&sm.o_empty, (done - 1) & 1, dead, a.err);
@@ -545,48 +572,49 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                     for (int k = 0; k < C::kVTok / 16; ++k)
 #pragma unroll
                         for (int mh = 0; mh < C::kMh; ++mh)
-                            umma_f16_ts(tmem + C::kO + mh * N, tmem + C::kV + (b * C::kMh + mh) * C::kVCols + 8 * k,
+                            umma_f16_ts_elect(tmem + C::kO + mh * N, tmem + C::kV + (b * C::kMh + mh) * C::kVCols + 8 * k,
                                         umma_desc_none(pa + pb * C::kPBytes + (h * (C::kVTok / 16) + k) * 256, 128, 16 * kTile), kIdesc2,
                                         !((flags & kFirst) && h == 0 && k == 0));
-                    umma_commit(smem_u32(&sm.v_empty[b]));
+                    umma_commit_elect(smem_u32(&sm.v_empty[b]));
                 }
-                umma_commit(smem_u32(&sm.p_empty[pb]));
+                umma_commit_elect(smem_u32(&sm.p_empty[pb]));
                 if (flags & kLast) {
-                    umma_commit(smem_u32(&sm.o_full));
+                    umma_commit_elect(smem_u32(&sm.o_full));
                     ++done;
                 }
                 if (C::kSBufs == 1 && i + 1 < count) scores(i + 1);
             }
         }
-        __syncwarp();
-    } else if (warp < 4) {
-        // ---- keys: one place a thread
-        const int t = warp * 32 + lane;
+    } else if (warp < 4 * C::kWork) {
+        // ---- keys: one place a thread; of two warpgroups, each takes every other buffer
+        const int wk = C::kWork > 1 ? warp >> 2 : 0;
+        const int t = (warp & 3) * 32 + lane;
         const int blk = t / kKvBlock, tok = t % kKvBlock;
         const int sw = kv4_swizzle(tok) & F::kChunkMask;
         constexpr int kChunks = D / 32 / C::kSub;  // of a buffer
         for (int i = 0; i < count; ++i) {
             const int st = i % C::kStages;
             wait(&sm.ring_full[st], (i / C::kStages) & 1, dead, a.err);
-            const uint8_t *kb = smem + st * C::kTileBytes + blk * F::kBlock;
-            for (int h = 0; h < C::kSub; ++h) {
+            const uint8_t *row = smem + st * C::kTileBytes + blk * F::kBlock + tok * F::kCodeRow;
+            const uint8_t *scales = smem + st * C::kTileBytes + blk * F::kBlock + F::kCodes + tok * F::kGroups * 4;
+            uint4 next = *reinterpret_cast<const uint4 *>(row + (((wk * kChunks) ^ sw) << 4));
+            // short loops: three roles' instructions have to fit the instruction caches
+#pragma unroll 1
+            for (int h = wk; h < C::kSub; h += C::kWork) {
                 const int u = i * C::kSub + h, b = u & 1;
-                uint4 w[kChunks];
-                uint32_t sc[kChunks];
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    const int ch = h * kChunks + c;
-                    w[c] = *reinterpret_cast<const uint4 *>(kb + tok * F::kCodeRow + ((ch ^ sw) << 4));
-                    sc[c] = *reinterpret_cast<const uint32_t *>(kb + F::kCodes + (tok * F::kGroups + (ch >> 1)) * 4);
-                }
                 if (u >= 2) {
                     wait(&sm.k_empty[b], ((u >> 1) & 1) ^ 1, dead, a.err);
                     tc_fence_after();
                 }
-#pragma unroll
+                const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kK + b * C::kKCols;
+#pragma unroll kKeyUnroll
                 for (int c = 0; c < kChunks; ++c) {
-                    const __half2 d = __low2half2(as_h2(sc[c])), m = __high2half2(as_h2(sc[c]));
-                    const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                    const int ch = h * kChunks + c;
+                    const uint32_t x[4] = {next.x, next.y, next.z, next.w};
+                    const uint32_t sc = *reinterpret_cast<const uint32_t *>(scales + (ch >> 1) * 4);
+                    const int after = c + 1 < kChunks ? ch + 1 : ch + 1 + (C::kWork - 1) * kChunks;
+                    next = *reinterpret_cast<const uint4 *>(row + (((after & F::kChunkMask) ^ sw) << 4));
+                    const __half2 d = __low2half2(as_h2(sc)), m = __high2half2(as_h2(sc));
                     uint32_t r[16];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -596,7 +624,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                         r[4 * e + 2] = dequant_lo(x8, d, m);
                         r[4 * e + 3] = dequant_hi(x8, d, m);
                     }
-                    tmem_st_32x32b(tmem + ((uint32_t)(warp * 32) << 16) + C::kK + b * C::kKCols + 16 * c, r);
+                    tmem_st_32x32b(to + 16 * c, r);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -605,48 +633,49 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
             }
             if (lane == 0) mbar_arrive(smem_u32(&sm.ring_empty[st]));
         }
-    } else if (warp < 8) {
-        // ---- values: 64 (D = 256) or 32 dimensions a warp, four nibbles of two places a register
-        const int w = warp - 4;
+    } else if (warp < 8 * C::kWork) {
+        // ---- values: 64 (D = 256) or 32 dimensions a warp, four nibbles of two places a register; of two
+        // warpgroups, each takes every other buffer
+        const int w = warp & 3;
+        const int wv = C::kWork > 1 ? (warp >> 2) - 2 : 0;
         constexpr int kStep = D == 256 ? 16 : 32;  // places of one ldmatrix
         const bool idle = D == 64 && w >= 2;       // lanes 64 .. 127 of O^T hold nothing
         const int group = D == 256 ? w : D == 128 ? w >> 1 : 0;
-        // the row this lane addresses: place and 16-byte chunk
+        // where this lane reads within a step: the row it addresses (a 16-byte chunk of a place), and the
+        // (d, m) of its two places of each eight
         const int at = D == 256 ? (lane >> 4) * 8 + (lane & 7) : lane;
         const int chunk = D == 256 ? 2 * w + ((lane >> 3) & 1) : w & F::kChunkMask;
+        const int tok = at % kKvBlock;
+        const int code_at = (at / kKvBlock) * F::kBlock + tok * F::kCodeRow + ((chunk ^ (kv4_swizzle(tok) & F::kChunkMask)) << 4);
+        const int scale_at = F::kCodes + (2 * (lane & 3) * F::kGroups + group) * 4;
+        const uint32_t lanes = tmem + ((uint32_t)(w * 32) << 16) + C::kV;
         for (int i = 0; i < count; ++i) {
             const int st = i % C::kStages;
             wait(&sm.ring_full[st], (i / C::kStages) & 1, dead, a.err);
             const Meta &m = sm.meta[i % kMetas];
-            const int valid = m.valid, room = m.len - m.pos;  // places of the tile that are there
-            const bool edge = valid != (1 << kTileBlocks) - 1 || room < kTile;
-            const uint8_t *vb = smem + st * C::kTileBytes + F::kPart;
-            for (int h = 0; h < C::kSub; ++h) {
+            const bool hole = m.flags & kHole;
+            const int valid = m.valid, room = m.room;  // places of the tile that are there
+#pragma unroll 1
+            for (int h = wv; h < C::kSub; h += C::kWork) {
                 const int u = i * C::kSub + h, b = u & 1;
+                const uint8_t *vb = smem + st * C::kTileBytes + F::kPart + h * (C::kVTok / kKvBlock) * F::kBlock;
                 if (u >= 2) {
                     wait(&sm.v_empty[b], ((u >> 1) & 1) ^ 1, dead, a.err);
                     tc_fence_after();
                 }
                 if (!idle) {
-#pragma unroll
-                    for (int p = 0; p < C::kVTok; p += kStep) {
-                        const int p0 = h * C::kVTok + p;
+#pragma unroll 1
+                    for (int p = 0; p < C::kVTok; p += kStep, vb += (kStep / kKvBlock) * F::kBlock) {
                         uint32_t x[4];
-                        {
-                            const int pl = p0 + at, tok = pl % kKvBlock;
-                            ldmatrix_x4_trans(smem_u32(vb + (pl / kKvBlock) * F::kBlock + tok * F::kCodeRow +
-                                                       ((chunk ^ (kv4_swizzle(tok) & F::kChunkMask)) << 4)),
-                                              x);
-                        }
-                        // (d, m) of this thread's two places of each group of eight
+                        ldmatrix_x4_trans(smem_u32(vb + code_at), x);
                         __half2 dd[kStep / 8], mm[kStep / 8];
 #pragma unroll
                         for (int e = 0; e < kStep / 8; ++e) {
-                            const int pl = p0 + 8 * e + 2 * (lane & 3), tok = pl % kKvBlock;
-                            const uint8_t *sp = vb + (pl / kKvBlock) * F::kBlock + F::kCodes + (tok * F::kGroups + group) * 4;
+                            const uint8_t *sp = vb + scale_at + (e >> 1) * F::kBlock + (e & 1) * 8 * F::kGroups * 4;
                             uint32_t s0 = *reinterpret_cast<const uint32_t *>(sp);
                             uint32_t s1 = *reinterpret_cast<const uint32_t *>(sp + F::kGroups * 4);
-                            if (edge) {  // places that are not there hold anything, NaN among it
+                            if (hole) {  // places that are not there hold anything, NaN among it
+                                const int pl = h * C::kVTok + p + 8 * e + 2 * (lane & 3);
                                 const bool there = (valid >> (pl / kKvBlock)) & 1;
                                 if (!there || pl >= room) s0 = 0;
                                 if (!there || pl + 1 >= room) s1 = 0;
@@ -654,30 +683,31 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                             dd[e] = as_h2(__byte_perm(s0, s1, 0x5410));
                             mm[e] = as_h2(__byte_perm(s0, s1, 0x7632));
                         }
-                        const uint32_t col = tmem + ((uint32_t)(w * 32) << 16) + C::kV + b * C::kMh * C::kVCols + p / 2;
-                        uint32_t r[4][4];  // by nibble
+                        // the operand's registers: D = 256, by nibble, (chunk 2w, 2w + 1) of each 8 places;
+                        // else by pair of nibbles, (nibble 2q, 2q + 1) of each 8 places
+                        uint32_t r[D == 256 ? 4 : 2][kStep / 4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int g = D == 256 ? e >> 1 : e;
                             const uint32_t x8 = x[e] >> 8;
-                            r[0][e] = dequant_lo(x[e], dd[g], mm[g]);
-                            r[1][e] = dequant_hi(x[e], dd[g], mm[g]);
-                            r[2][e] = dequant_lo(x8, dd[g], mm[g]);
-                            r[3][e] = dequant_hi(x8, dd[g], mm[g]);
+                            const uint32_t v[4] = {dequant_lo(x[e], dd[g], mm[g]), dequant_hi(x[e], dd[g], mm[g]),
+                                                   dequant_lo(x8, dd[g], mm[g]), dequant_hi(x8, dd[g], mm[g])};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                if constexpr (D == 256)
+                                    r[j][e] = v[j];
+                                else
+                                    r[j >> 1][2 * e + (j & 1)] = v[j];
+                            }
                         }
+                        const uint32_t col = lanes + b * C::kMh * C::kVCols + p / 2;
                         if constexpr (D == 256) {
-                            // registers: (chunk 2w, 2w + 1) of places 0-7, then of places 8-15
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                tmem_st_16x128b_x2(col + ((uint32_t)(16 * (j & 1)) << 16) + (j >> 1) * C::kVCols, r[j]);
+                                TmemWrite16<2>::run(col + ((uint32_t)(16 * (j & 1)) << 16) + (j >> 1) * C::kVCols, r[j]);
                         } else {
-                            // nibbles 2q and 2q + 1 in lanes 0-7 and 8-15 of a group of 16
 #pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                const uint32_t y[8] = {r[2 * q][0], r[2 * q + 1][0], r[2 * q][1], r[2 * q + 1][1],
-                                                       r[2 * q][2], r[2 * q + 1][2], r[2 * q][3], r[2 * q + 1][3]};
-                                tmem_st_16x128b_x4(col + ((uint32_t)(16 * q) << 16), y);
-                            }
+                            for (int q = 0; q < 2; ++q) TmemWrite16<4>::run(col + ((uint32_t)(16 * q) << 16), r[q]);
                         }
                     }
                     tmem_wait_st();
@@ -691,166 +721,187 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
     } else {
         // ---- softmax: one place a thread, kNS query rows; and q in, O out
         constexpr int NS = C::kNS;
-        constexpr int NC = NS < 32 ? NS : 32;    // query rows worked at once
-        const int wg = (warp - 8) >> 2;          // softmax warpgroup
+        constexpr int kVec = D / 8;              // 16-byte pieces of a row of q
+        const int wg = (warp - 8 * C::kWork) >> 2;  // softmax warpgroup
         const int n0 = wg * NS;                  // its first query row
-        const int w = (warp - 8) & 3;            // tensor-memory quadrant
+        const int w = warp & 3;                  // tensor-memory quadrant
         const int t = w * 32 + lane;
         const int bar_id = 1 + wg;
+        constexpr int kAllBar = 1 + C::kSoft;
         const uint32_t quad = tmem + ((uint32_t)(w * 32) << 16);
+        float *stage = reinterpret_cast<float *>(smem + C::kP) + wg * C::kOutRows * C::kOutStride;
         float sum[NS];
         int seg = 0;
-        float *stage = reinterpret_cast<float *>(smem + C::kP) + wg * C::kOutRows * C::kOutStride;
-        // Stages q of an item, rows of other items at zero; k index in the order that the codes are unpacked in.
-        auto stage_q = [&](const Meta &m) {
-            const int64_t row0 = (int64_t)m.rt * N;
-            for (int x = t; x < NS * (D / 8); x += 128) {
-                const int n = n0 + x % NS, g = x / NS;
-                const int64_t row = row0 + n;
-                const int tok = (int)(row / a.G);
-                uint32_t v[4] = {0, 0, 0, 0};
-                if (tok < m.n) {
-                    const __half *qp = static_cast<const __half *>(a.q.p) + (int64_t)(m.first + tok) * a.q.st +
-                                       (int64_t)(m.head * a.G + (int)(row - (int64_t)tok * a.G)) * a.q.sh;
-                    if (a.q.vec > 1) {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(qp + 8 * g);
-                        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-                    } else {
+        // q of a part of an item into its buffer, with what each row sees and where it goes; k index in the
+        // order that the codes are unpacked in; rows that are not there zero
+        auto stage_q = [&](const Item &m, int which) {
+            const int qb = which % C::kQBufs;
+            if (t < NS) {
+                const uint32_t row = (uint32_t)(m.rt * N + n0 + t);
+                const int tok = (int)(row / (uint32_t)a.G);
+                const bool ok = tok < m.n;
+                const int64_t tt = m.first + tok, hh = m.head * a.G + (int)(row - (uint32_t)tok * (uint32_t)a.G);
+                sm.lim[which & 1][n0 + t] = ok ? m.len - m.n + tok : -1;
+                sm.orow[which & 1][n0 + t] = ok ? tt * a.out.st + hh * a.out.sh : -1;
+                sm.qrow[n0 + t] = ok ? tt * a.q.st + hh * a.q.sh : -1;
+            }
+            bar_sync(bar_id, 128);
+            constexpr int kBatch = NS * kVec / 128 < 4 ? NS * kVec / 128 : 4;
+#pragma unroll 1
+            for (int x0 = t; x0 < NS * kVec; x0 += 128 * kBatch) {
+                uint32_t v[kBatch][4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = as_u32(__halves2half2(qp[(8 * g + 2 * e) * a.q.sd], qp[(8 * g + 2 * e + 1) * a.q.sd]));
+                for (int y = 0; y < kBatch; ++y) {
+                    const int x = x0 + 128 * y;
+                    const int n = n0 + (x >> 1) % NS, g = 2 * (x / (2 * NS)) + (x & 1);  // two pieces of a row side by side
+                    const int64_t at = sm.qrow[n];
+                    v[y][0] = v[y][1] = v[y][2] = v[y][3] = 0;
+                    if (at >= 0) {
+                        const __half *qp = static_cast<const __half *>(a.q.p) + at;
+                        if (a.q.vec > 1) {
+                            const uint4 u = *reinterpret_cast<const uint4 *>(qp + 8 * g);
+                            v[y][0] = u.x, v[y][1] = u.y, v[y][2] = u.z, v[y][3] = u.w;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                v[y][e] = as_u32(__halves2half2(qp[(8 * g + 2 * e) * a.q.sd], qp[(8 * g + 2 * e + 1) * a.q.sd]));
+                        }
                     }
                 }
-                *reinterpret_cast<uint4 *>(smem + C::kQ + g * 16 * N + (n >> 3) * 128 + (n & 7) * 16) =
-                    make_uint4(__byte_perm(v[0], v[2], 0x5410), __byte_perm(v[0], v[2], 0x7632), __byte_perm(v[1], v[3], 0x5410),
-                               __byte_perm(v[1], v[3], 0x7632));
-            }
-            for (int n = t; n < NS; n += 128) {
-                const int tok = (int)((row0 + n0 + n) / a.G);
-                sm.lim[n0 + n] = tok < m.n ? m.len - m.n + tok : -1;
+#pragma unroll
+                for (int y = 0; y < kBatch; ++y) {
+                    const int x = x0 + 128 * y;
+                    const int n = n0 + (x >> 1) % NS, g = 2 * (x / (2 * NS)) + (x & 1);
+                    *reinterpret_cast<uint4 *>(smem + C::kQ + qb * C::kQBytes + g * 16 * N + (n >> 3) * 128 + (n & 7) * 16) =
+                        make_uint4(__byte_perm(v[y][0], v[y][2], 0x5410), __byte_perm(v[y][0], v[y][2], 0x7632),
+                                   __byte_perm(v[y][1], v[y][3], 0x5410), __byte_perm(v[y][1], v[y][3], 0x7632));
+                }
             }
             fence_proxy_async_smem();
             bar_sync(bar_id, 128);
-            if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
+            if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[qb]));
         };
         if (count > 0) {
             wait_described(&sm.produced, 1, dead, a.err);
-            stage_q(sm.meta[0]);
+            stage_q(sm.meta[0].item, 0);
         }
+        Item next = {};
+        bool has_next = false;
+        int flags = 0;
         for (int i = 0; i < count; ++i) {
             const int sb = i % C::kSBufs, pb = i % C::kPBufs;
             wait(&sm.s_full[sb], (i / C::kSBufs) & 1, dead, a.err);
             tc_fence_after();
-            const Meta m = sm.meta[i % kMetas];
-            const bool first = m.flags & kFirst;
+            const Meta &m = sm.meta[i % kMetas];
+            flags = m.flags;
+            const bool first = flags & kFirst;
             if (first) {
+                next = m.next;
+                has_next = flags & kNext;
 #pragma unroll
                 for (int n = 0; n < NS; ++n) sum[n] = 0.0f;
             }
             const int pos = m.pos + t;
-            const bool there = ((m.valid >> (t / kKvBlock)) & 1) && pos < m.len;
-            const bool edge = m.valid != (1 << kTileBlocks) - 1 || m.pos + kTile > m.len - m.n + (int)(((int64_t)m.rt * N) / a.G) + 1;
+            const bool there = ((m.valid >> (t / kKvBlock)) & 1) && t < m.room;
+            float x[NS];
+            // this place's scores, less the rows' references; -inf where a row does not see the place
+            auto load = [&](bool less) {
+                TmemRead<NS>::run(quad + C::kS + sb * N + n0, x);
 #pragma unroll
-            for (int c = 0; c < NS; c += NC) {
-                const int nc = n0 + c;
-                float s[NC];
-                TmemRead<NC>::run(quad + C::kS + sb * N + nc, s);
-                if (c + NC == NS) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty[sb]));
+                for (int n = 0; n < NS; n += 4) {
+                    float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (less) b = *reinterpret_cast<const float4 *>(&sm.base[n0 + n]);
+                    x[n] = fmaf(x[n], a.scale_log2, -b.x);
+                    x[n + 1] = fmaf(x[n + 1], a.scale_log2, -b.y);
+                    x[n + 2] = fmaf(x[n + 2], a.scale_log2, -b.z);
+                    x[n + 3] = fmaf(x[n + 3], a.scale_log2, -b.w);
                 }
-                if (edge) {
+                if (flags & kEdge) {
 #pragma unroll
-                    for (int n = 0; n < NC; n += 4) {
-                        const int4 l = *reinterpret_cast<const int4 *>(&sm.lim[nc + n]);
-                        if (!there || pos > l.x) s[n] = -INFINITY;
-                        if (!there || pos > l.y) s[n + 1] = -INFINITY;
-                        if (!there || pos > l.z) s[n + 2] = -INFINITY;
-                        if (!there || pos > l.w) s[n + 3] = -INFINITY;
+                    for (int n = 0; n < NS; n += 4) {
+                        const int4 l = *reinterpret_cast<const int4 *>(&sm.lim[seg & 1][n0 + n]);
+                        if (!there || pos > l.x) x[n] = -INFINITY;
+                        if (!there || pos > l.y) x[n + 1] = -INFINITY;
+                        if (!there || pos > l.z) x[n + 2] = -INFINITY;
+                        if (!there || pos > l.w) x[n + 3] = -INFINITY;
                     }
                 }
-                bool move = first;
+            };
+            load(!first);
+            bool move = first;
+            if (!first) {
+                float over = x[0];
+#pragma unroll
+                for (int n = 1; n < NS; ++n) over = fmaxf(over, x[n]);
+                move = over > kMoveMax + kWeightShift;
+            }
+            if (bar_or(bar_id, 128, move)) {
+                // the rows' maxima over the 128 places; O and the sums follow the reference
+                if (!first) load(false);
+#pragma unroll
+                for (int n = 0; n < NS; ++n) {
+                    const int top = __reduce_max_sync(0xffffffffu, float_order(x[n]));
+                    if (lane == (n & 31)) sm.wred[w][n0 + n] = order_float(top);
+                }
+                bar_sync(bar_id, 128);
+                if (t < NS) {
+                    const float old = first ? -INFINITY : sm.ref[n0 + t];
+                    float top = old;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) top = fmaxf(top, sm.wred[y][n0 + t]);
+                    if (sm.lim[seg & 1][n0 + t] < 0) top = fmaxf(top, 0.0f);  // a row that sees nothing stays out of this
+                    sm.ref[n0 + t] = top;
+                    // a row that has seen nothing yet moves at its first score
+                    sm.base[n0 + t] = top == -INFINITY ? -1e30f : top - kWeightShift;
+                    sm.factor[n0 + t] = top == -INFINITY ? 1.0f : ex2(old - top);
+                }
+                bar_sync(bar_id, 128);
                 if (!first) {
-                    float over = -INFINITY;
 #pragma unroll
-                    for (int n = 0; n < NC; n += 4) {
-                        const float4 b = *reinterpret_cast<const float4 *>(&sm.base[nc + n]);
-                        over = fmaxf(over, fmaf(s[n], a.scale_log2, -b.x));
-                        over = fmaxf(over, fmaf(s[n + 1], a.scale_log2, -b.y));
-                        over = fmaxf(over, fmaf(s[n + 2], a.scale_log2, -b.z));
-                        over = fmaxf(over, fmaf(s[n + 3], a.scale_log2, -b.w));
-                    }
-                    move = over > kMoveMax + kWeightShift;
-                }
-                if (bar_or(bar_id, 128, move)) {
-                    // the rows' maxima over the 128 places; O and the sums follow the reference
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) {
-                        const int top = __reduce_max_sync(0xffffffffu, float_order(s[n] * a.scale_log2));
-                        if (lane == 0) sm.wred[wg * 4 + w][n] = order_float(top);
-                    }
-                    bar_sync(bar_id, 128);
-                    if (t < NC) {
-                        const float old = first ? -INFINITY : sm.ref[nc + t];
-                        float top = old;
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) top = fmaxf(top, sm.wred[wg * 4 + x][t]);
-                        if (sm.lim[nc + t] < 0) top = fmaxf(top, 0.0f);  // a row that sees nothing stays out of this
-                        sm.ref[nc + t] = top;
-                        // a row that has seen nothing yet moves at its first score
-                        sm.base[nc + t] = top == -INFINITY ? -1e30f : top - kWeightShift;
-                        sm.factor[nc + t] = top == -INFINITY ? 1.0f : ex2(old - top);
-                    }
-                    bar_sync(bar_id, 128);
-                    if (!first) {
-#pragma unroll
-                        for (int n = 0; n < NC; ++n) sum[c + n] *= sm.factor[nc + n];
-                        // every product before this tile is in O
-                        wait(&sm.p_empty[(i - 1) % C::kPBufs], ((i - 1) / C::kPBufs) & 1, dead, a.err);
-                        tc_fence_after();
+                    for (int n = 0; n < NS; ++n) sum[n] *= sm.factor[n0 + n];
+                    // every product before this tile is in O
+                    wait(&sm.p_empty[(i - 1) % C::kPBufs], ((i - 1) / C::kPBufs) & 1, dead, a.err);
+                    tc_fence_after();
 #pragma unroll 1
-                        for (int x = 0; x < C::kMh * NC; x += 16) {
-                            const uint32_t at = quad + C::kO + (x / NC) * N + nc + x % NC;
-                            float o[16];
-                            uint32_t r[16];
-                            TmemRead<16>::run(at, o);
+                    for (int y = 0; y < C::kMh * NS; y += 16) {
+                        const uint32_t at = quad + C::kO + (y / NS) * N + n0 + y % NS;
+                        float o[16];
+                        uint32_t r[16];
+                        TmemRead<16>::run(at, o);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e] * sm.factor[nc + x % NC + e]);
-                            tmem_st_32x32b(at, r);
-                        }
-                        tmem_wait_st();
-                        tc_fence_before();
+                        for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e] * sm.factor[n0 + y % NS + e]);
+                        tmem_st_32x32b(at, r);
                     }
+                    tmem_wait_st();
                 }
-                if (c == 0 && i >= C::kPBufs) wait(&sm.p_empty[pb], ((i / C::kPBufs) & 1) ^ 1, dead, a.err);
-                uint8_t *pp = smem + C::kP + pb * C::kPBytes + (nc >> 3) * (16 * kTile) + (t >> 3) * 128 + (t & 7) * 16;
+                load(true);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty[sb]));
+            if (i >= C::kPBufs) wait(&sm.p_empty[pb], ((i / C::kPBufs) & 1) ^ 1, dead, a.err);
+            uint8_t *pp = smem + C::kP + pb * C::kPBytes + (n0 >> 3) * (16 * kTile) + (t >> 3) * 128 + (t & 7) * 16;
 #pragma unroll
-                for (int n = 0; n < NC; n += 8) {
-                    const float4 b0 = *reinterpret_cast<const float4 *>(&sm.base[nc + n]);
-                    const float4 b1 = *reinterpret_cast<const float4 *>(&sm.base[nc + n + 4]);
-                    const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-                    float e[8];
+            for (int n = 0; n < NS; n += 8) {
+                float e[8];
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        e[x] = ex2(fmaf(s[n + x], a.scale_log2, -b[x]));
-                        sum[c + n + x] += e[x];
-                    }
-                    *reinterpret_cast<uint4 *>(pp + (n >> 3) * (16 * kTile)) =
-                        make_uint4(pack_h2(e[0], e[1]), pack_h2(e[2], e[3]), pack_h2(e[4], e[5]), pack_h2(e[6], e[7]));
+                for (int y = 0; y < 8; ++y) {
+                    e[y] = ex2(x[n + y]);
+                    sum[n + y] += e[y];
                 }
+                *reinterpret_cast<uint4 *>(pp + (n >> 3) * (16 * kTile)) =
+                    make_uint4(pack_h2(e[0], e[1]), pack_h2(e[2], e[3]), pack_h2(e[4], e[5]), pack_h2(e[6], e[7]));
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[pb]));
-            if (m.flags & kLast) {
-                // q of the next item while the last products run (all first products of this one are done:
-                // their scores have been read)
-                if (C::kSoft > 1) bar_sync(3, 256);  // both warpgroups have
-                if (i + 1 < count) {
-                    wait_described(&sm.produced, i + 2, dead, a.err);
-                    stage_q(sm.meta[(i + 1) % kMetas]);
-                }
+            // q of the next part: in its own buffer while this part runs (the first products of the part before
+            // this one are done: their scores came before this tile's), or when this part's are done
+            if (C::kQBufs > 1 ? first && has_next : (flags & kLast) && has_next) {
+                if (C::kQBufs == 1 && C::kSoft > 1) bar_sync(kAllBar, 128 * C::kSoft);
+                stage_q(next, seg + 1);
+            }
+            if (flags & kLast) {
                 // ---- the sums over the places
 #pragma unroll
                 for (int c = 0; c < NS; c += 16) {
@@ -858,45 +909,49 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] = sum[c + e];
                     const float r = reduce_scatter<16>(v, lane);
-                    if (lane < 16) sm.wred[wg * 4 + w][c + lane] = r;
+                    if (lane < 16) sm.wred[w][n0 + c + lane] = r;
                 }
                 bar_sync(bar_id, 128);
-                const int slot = 2 * cta + ((m.flags & kFromStart) ? 1 : 0);
-                const bool complete = m.flags & kComplete;
-                for (int n = t; n < NS; n += 128) {
-                    const float den = (sm.wred[wg * 4][n] + sm.wred[wg * 4 + 1][n]) + (sm.wred[wg * 4 + 2][n] + sm.wred[wg * 4 + 3][n]);
-                    sm.inv[n0 + n] = complete ? (den > 0.0f ? 1.0f / den : 0.0f) : 1.0f;
-                    if (!complete) a.stat[(int64_t)slot * N + n0 + n] = make_float2(sm.ref[n0 + n], den);
+                const int slot = 2 * cta + ((flags & kFromStart) ? 1 : 0);
+                const bool complete = flags & kComplete;
+                if (t < NS) {
+                    const int n = n0 + t;
+                    const float den = (sm.wred[0][n] + sm.wred[1][n]) + (sm.wred[2][n] + sm.wred[3][n]);
+                    sm.inv[n] = complete ? (den > 0.0f ? 1.0f / den : 0.0f) : 1.0f;
+                    if (!complete) a.stat[(int64_t)slot * N + n] = make_float2(sm.ref[n], den);
                 }
                 wait(&sm.o_full, seg & 1, dead, a.err);
-                ++seg;
                 tc_fence_after();
                 bar_sync(bar_id, 128);
-                // ---- O, eight rows at a time through shared memory (the weights' buffers are free now)
-                const int64_t row0 = (int64_t)m.rt * N + n0;
-                for (int c = 0; c < NS; c += 8) {
-                    if ((row0 + c) / a.G >= m.n) break;  // no more rows
+                // ---- O, some rows at a time through shared memory (the weights' buffers are free now)
+#pragma unroll 1
+                for (int c = 0; c < NS; c += C::kOutRows) {
 #pragma unroll
                     for (int mh = 0; mh < C::kMh; ++mh) {
-                        float o[8];
-                        TmemRead<8>::run(quad + C::kO + mh * N + n0 + c, o);
                         const int dim = o_dim<D>(t, mh);
-                        if (D > 64 || t < 64) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) stage[e * C::kOutStride + dim] = o[e] * sm.inv[n0 + c + e];
+                        for (int c8 = 0; c8 < C::kOutRows; c8 += 8) {
+                            float o[8];
+                            TmemRead<8>::run(quad + C::kO + mh * N + n0 + c + c8, o);
+                            if (D > 64 || t < 64) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) stage[(c8 + e) * C::kOutStride + dim] = o[e] * sm.inv[n0 + c + c8 + e];
+                            }
                         }
                     }
                     bar_sync(bar_id, 128);
-                    for (int x = t; x < 8 * (D / 8); x += 128) {
-                        const int e = x / (D / 8), g = x % (D / 8);
-                        const int64_t row = row0 + c + e;
-                        const int tok = (int)(row / a.G);
+#pragma unroll 2
+                    for (int y = t; y < C::kOutRows * kVec; y += 128) {
+                        const int e = y / kVec, g = y % kVec;
+                        const int64_t at = sm.orow[seg & 1][n0 + c + e];
                         const float4 v0 = *reinterpret_cast<const float4 *>(stage + e * C::kOutStride + 8 * g);
                         const float4 v1 = *reinterpret_cast<const float4 *>(stage + e * C::kOutStride + 8 * g + 4);
-                        if (tok < m.n) {
+                        if (at >= 0) {
                             if (complete) {
                                 const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-                                store_dims<8>(a.out, m.first + tok, m.head * a.G + (int)(row - (int64_t)tok * a.G), 8 * g, v);
+                                HeadsView o = a.out;
+                                o.p = static_cast<__half *>(a.out.p) + at;
+                                store_dims<8>(o, 0, 0, 8 * g, v);
                             } else {
                                 float *dst = a.part + ((int64_t)slot * N + n0 + c + e) * D + 8 * g;
                                 *reinterpret_cast<float4 *>(dst) = v0;
@@ -904,11 +959,16 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                             }
                         }
                     }
-                    bar_sync(bar_id, 128);
+                    if (c + C::kOutRows < NS) bar_sync(bar_id, 128);
                 }
                 tc_fence_before();
-                if (C::kSoft > 1) bar_sync(3, 256);  // the other warpgroup may still read the staging area
+                // no warpgroup writes weights over another's staging area
+                if (C::kSoft > 1)
+                    bar_sync(kAllBar, 128 * C::kSoft);
+                else
+                    bar_sync(bar_id, 128);
                 if (lane == 0) mbar_arrive(smem_u32(&sm.o_empty));
+                ++seg;
             }
         }
     }
@@ -1044,6 +1104,7 @@ int qg_attn_kv4(const qg_heads *q, int64_t T, int nseq, const int32_t *q_start, 
         page < kKvBlock || page % kKvBlock || width < 0 || pages < 0 || (int64_t)width * page > 0x7fffff00)
         return QG_ERR_SHAPE;
     if (pages > 0 && qg_kv4_bytes(pages, page, Hk, D) == 0) return QG_ERR_SHAPE;
+    if (T * (Hq / Hk) > 0x7fffffff - 256) return QG_ERR_SHAPE;
     if (T == 0 || nseq == 0) return QG_OK;
     if (!q_start || !kv_len || (width > 0 && !table) || (pages > 0 && !cache) || !workspace) return QG_ERR_NULL;
     AttnArgs a = {};
