@@ -454,6 +454,13 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
         Cursor c = sm.found;
         int item = sm.found_item;
         bool any_cut = false, from_start = false;
+        const int page_blocks = a.page / kKvBlock;
+        // page of block 8 unit + lane of the cursor's item, and the block's place in it
+        auto look_up = [&](const Cursor &k, int unit) -> int {
+            const int blk = unit * kTileBlocks + lane;
+            return blk * kKvBlock < k.q.len ? a.table[(int64_t)k.s * a.width + blk / page_blocks] : -1;
+        };
+        int ahead = 0, pages = -1, pages_next = -1;
         for (int i = 0; i < count; ++i) {
             const int st = i % C::kStages;
             if (i >= C::kStages) wait(&sm.ring_empty[st], ((i / C::kStages) & 1) ^ 1, dead, a.err);
@@ -464,18 +471,31 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
             const bool whole_end = c.unit + 1 == c.units;
             const bool last = whole_end || i + 1 == count;
             const bool complete = whole_end && from_start;
-            // a lane looks up a block's page
-            const int p = pos + lane * kKvBlock;
-            int64_t pg = -1;
-            int in_page = 0;
-            if (lane < kTileBlocks && p < c.q.len) {
-                const int pi = p / a.page;
-                in_page = p - pi * a.page;
-                pg = a.table[(int64_t)c.s * a.width + pi];
+            // the pages of the tile's blocks: looked up for four tiles of an item at a time, the next four while
+            // these are copied (a look-up takes as long as half a tile)
+            if (first || c.unit == ahead) {
+                if (first) ahead = c.unit;
+                pages = first ? look_up(c, ahead) : pages_next;
+                ahead += 4;
+                pages_next = ahead < c.units ? look_up(c, ahead) : -1;
             }
-            const bool ok = pg >= 0 && pg < a.pages;
+            const int64_t pg = __shfl_sync(0xffffffffu, pages, (c.unit - (ahead - 4)) * kTileBlocks + (lane & 7));
+            const bool ok = lane < kTileBlocks && pg >= 0 && pg < a.pages;
             const uint32_t valid = __ballot_sync(0xffffffffu, ok);
             const uint32_t bar = smem_u32(&sm.ring_full[st]);
+            // one copy for each run of neighbouring blocks of a page
+            const int in_page = (int)((uint32_t)(c.unit * kTileBlocks + lane) % (uint32_t)page_blocks);
+            const int64_t blk = (pg * a.Hk + c.head) * page_blocks + in_page;
+            uint32_t heads = __ballot_sync(0xffffffffu, ok && (lane == 0 || in_page == 0));
+            while (heads) {
+                const int l = __ffs(heads) - 1;
+                heads &= heads - 1;
+                const int64_t from = __shfl_sync(0xffffffffu, blk, l);
+                // down to the next run, or the last block that is there (a run has no gaps: one page)
+                const uint32_t rest = heads ? (1u << (__ffs(heads) - 1)) - 1 : 0xffffffffu;
+                const int run = __popc(valid & rest & ~((1u << l) - 1));
+                bulk_g2s_elect(smem_u32(smem + st * C::kTileBytes + l * F::kBlock), a.cache + from * F::kBlock, run * F::kBlock, bar);
+            }
             if (lane == 0) {
                 Meta &m = sm.meta[i % kMetas];
                 const int left = c.units - c.unit - 1;
@@ -510,10 +530,6 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                 }
             }
             __syncwarp();
-            if (ok) {
-                const int64_t blk = (pg * a.Hk + c.head) * (a.page / kKvBlock) + in_page / kKvBlock;
-                bulk_g2s_plain(smem_u32(smem + st * C::kTileBytes + lane * F::kBlock), a.cache + blk * F::kBlock, F::kBlock, bar);
-            }
             if (++c.unit == c.units) {
                 next_item<N>(a, c);
                 ++item;
@@ -560,7 +576,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
             int done = 0;  // parts of items finished
             for (int i = 0; i < count; ++i) {
                 const int flags = __shfl_sync(0xffffffffu, sm.meta[i % kMetas].flags, 0);
-                if (C::kSBufs > 1 && i + 1 < count) scores(i + 1);
+                if (i + 1 < count) scores(i + 1);  // (with one score buffer: once the softmax has read it)
                 const int pb = i % C::kPBufs;
                 if ((flags & kFirst) && done > 0) wait(&sm.o_empty, (done - 1) & 1, dead, a.err);
                 wait(&sm.p_full[pb], (i / C::kPBufs) & 1, dead, a.err);
@@ -582,7 +598,6 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                     umma_commit_elect(smem_u32(&sm.o_full));
                     ++done;
                 }
-                if (C::kSBufs == 1 && i + 1 < count) scores(i + 1);
             }
         }
     } else if (warp < 4 * C::kWork) {
