@@ -226,7 +226,7 @@ template <int N> struct Small {
     Meta meta[kMetas];
     Cursor found;
     int found_item;
-    int64_t scan[32];
+    int64_t scan[2][32];
     int iscan[32];
     uint32_t tmem;
     int dead, produced;  // produced: tiles described so far
@@ -362,20 +362,23 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
     // ---- the run of tiles of this CTA: the tiles of all sequences, then the sequence its first one is in
     const int threads = C::kWarps * 32;
     int64_t total = 0;
+    Seq mine = {};       // this thread's sequence of the last round, and the tiles of one of its heads
+    int64_t mine_units = 0;
     for (int s = threadIdx.x; s < a.nseq; s += threads) {
-        const Seq q = load_seq<N>(a, s);
-        total += head_units<N>(a, q) * a.Hk;
+        mine = load_seq<N>(a, s);
+        mine_units = head_units<N>(a, mine);
+        total += mine_units * a.Hk;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) sm.scan[warp] = total;
+    if (lane == 0) sm.scan[0][warp] = total;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     pdl_launch_dependents();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
     total = 0;
-    for (int w = 0; w < C::kWarps; ++w) total += sm.scan[w];
+    for (int w = 0; w < C::kWarps; ++w) total += sm.scan[0][w];
     const int64_t per = (total + grid - 1) / grid;
     const int64_t begin = per * cta < total ? per * cta : total;
     const int64_t end = begin + per < total ? begin + per : total;
@@ -389,14 +392,17 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
         int items = 0;
         for (int s0 = 0; s0 < a.nseq; s0 += threads) {
             const int s = s0 + threadIdx.x;
-            Seq q = {};
-            int64_t hu = 0;
-            if (s < a.nseq) {
-                q = load_seq<N>(a, s);
-                hu = head_units<N>(a, q);
+            if (a.nseq > threads) {  // (else the first pass has left it)
+                mine = {};
+                mine_units = 0;
+                if (s < a.nseq) {
+                    mine = load_seq<N>(a, s);
+                    mine_units = head_units<N>(a, mine);
+                }
+                if (s0 > 0) __syncthreads();  // the sums of the round before have been read
             }
-            const int64_t u = hu * a.Hk;
-            const int it = q.tiles * a.Hk;
+            const int64_t u = mine_units * a.Hk;
+            const int it = mine.tiles * a.Hk;
             int64_t up = u;
             int itp = it;
 #pragma unroll
@@ -408,9 +414,8 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                     itp += w;
                 }
             }
-            __syncthreads();
             if (lane == 31) {
-                sm.scan[warp] = up;
+                sm.scan[1][warp] = up;
                 sm.iscan[warp] = itp;
             }
             __syncthreads();
@@ -418,28 +423,28 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
             int ibefore = items + itp - it;
             for (int w = 0; w < C::kWarps; ++w) {
                 if (w < warp) {
-                    before += sm.scan[w];
+                    before += sm.scan[1][w];
                     ibefore += sm.iscan[w];
                 }
-                base += sm.scan[w];
+                base += sm.scan[1][w];
                 items += sm.iscan[w];
             }
             if (begin >= before && begin < before + u) {
                 Cursor c;
-                c.q = q;
+                c.q = mine;
                 c.s = s;
                 int64_t rest = begin - before;
-                c.head = (int)(rest / hu);
-                rest -= c.head * hu;
+                c.head = (int)(rest / mine_units);
+                rest -= c.head * mine_units;
                 c.rt = 0;
-                c.units = item_units<N>(a, q, 0);
+                c.units = item_units<N>(a, mine, 0);
                 while (rest >= c.units) {
                     rest -= c.units;
-                    c.units = item_units<N>(a, q, ++c.rt);
+                    c.units = item_units<N>(a, mine, ++c.rt);
                 }
                 c.unit = (int)rest;
                 sm.found = c;
-                sm.found_item = ibefore + c.head * q.tiles + c.rt;
+                sm.found_item = ibefore + c.head * mine.tiles + c.rt;
             }
         }
         // the join looks at every entry that the argument sizes allow for
@@ -996,56 +1001,73 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
 }
 
 // The items that were cut between CTAs: out = sum_i 2^(ref_i - ref) O_i / sum_i 2^(ref_i - ref) sum_i,
-// in CTA order.  One block takes RB rows of one item; D / 4 threads share a row's dimensions and the
+// in a fixed order.  One block takes RB rows of one item; D / 4 threads share a row's dimensions and the
 // rest of its threads the parts.
-template <int D, int N, int RB> __global__ void __launch_bounds__(256) attn_kv4_join_kernel(const AttnArgs a)
+constexpr int kMostParts = 1024;  // an item has at most one part a CTA
+
+template <int D, int N, int RB> __global__ void __launch_bounds__(512) attn_kv4_join_kernel(const AttnArgs a)
 {
     constexpr int TX = D / 4;            // threads across a row
-    constexpr int TY = 256 / (TX * RB);  // threads that share its parts
+    constexpr int TY = 512 / (TX * RB);  // threads that share its parts
     static_assert(TY >= 1, "a row's threads fit the block");
     __shared__ float4 acc[RB][TY][TX];
-    __shared__ float den[RB][TY];
+    __shared__ float factor[RB][kMostParts / (RB > 1 ? 4 : 1)];
+    __shared__ float den[RB];
     pdl_launch_dependents();
     pdl_wait();
     const int4 c = a.cut[blockIdx.x];
     if (c.w == 0) return;
     const int head = c.y & 0xffff, cta = c.y >> 16;
     const int x = threadIdx.x % TX, y = threadIdx.x / TX % TY, rl = threadIdx.x / (TX * TY);
-    const int r = blockIdx.y * RB + rl;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Seq q = load_seq<N>(a, c.x);
-    const int64_t row = (int64_t)c.z * N + r;
-    const int tok = (int)(row / a.G);
-    float top = -INFINITY;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f;
-    if (tok < q.n) {
-        for (int i = 0; i < c.w; ++i) top = fmaxf(top, a.stat[(int64_t)(i ? 2 * (cta + i) : 2 * cta + 1) * N + r].x);
-#pragma unroll 4
-        for (int i = y; i < c.w; i += TY) {
-            const int64_t slot = i ? 2 * (cta + i) : 2 * cta + 1;
-            const float2 st = a.stat[slot * N + r];
+    auto slot = [&](int i) -> int64_t { return i ? 2 * (cta + i) : 2 * cta + 1; };
+    // a warp a row: the reference of all parts, each part's factor, the sum
+    if (warp < RB) {
+        const int r = blockIdx.y * RB + warp;
+        float top = -INFINITY;
+        for (int i = lane; i < c.w; i += 32) top = fmaxf(top, a.stat[slot(i) * N + r].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float l = 0.0f;
+        for (int i = lane; i < c.w; i += 32) {
+            const float2 st = a.stat[slot(i) * N + r];
             const float f = st.x == -INFINITY ? 0.0f : ex2(st.x - top);
-            const float4 u = *reinterpret_cast<const float4 *>(a.part + (slot * N + r) * D + 4 * x);
+            factor[warp][i] = f;
             l = fmaf(st.y, f, l);
+        }
+        l = warp_sum(l);
+        if (lane == 0) den[warp] = l;
+    }
+    __syncthreads();
+    const int r = blockIdx.y * RB + rl;
+    const uint32_t row = (uint32_t)(c.z * N + r);
+    const int tok = (int)(row / (uint32_t)a.G);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (tok < q.n) {
+#pragma unroll 8
+        for (int i = y; i < c.w; i += TY) {
+            const float f = factor[rl][i];
+            const float4 u = *reinterpret_cast<const float4 *>(a.part + (slot(i) * N + r) * D + 4 * x);
             v.x = fmaf(u.x, f, v.x);
             v.y = fmaf(u.y, f, v.y);
             v.z = fmaf(u.z, f, v.z);
             v.w = fmaf(u.w, f, v.w);
         }
     }
-    acc[rl][y][x] = v;
-    if (x == 0) den[rl][y] = l;
-    __syncthreads();
-    if (y != 0 || tok >= q.n) return;
-    for (int i = 1; i < TY; ++i) {
-        const float4 u = acc[rl][i][x];
-        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    if (TY > 1) {
+        acc[rl][y][x] = v;
+        __syncthreads();
+        if (y != 0) return;
+        for (int i = 1; i < TY; ++i) {
+            const float4 u = acc[rl][i][x];
+            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+        }
     }
-    l = 0.0f;
-    for (int i = 0; i < TY; ++i) l += den[rl][i];
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    if (tok >= q.n) return;
+    const float inv = den[rl] > 0.0f ? 1.0f / den[rl] : 0.0f;
     const float w[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-    store_dims<4>(a.out, q.first + tok, head * a.G + (int)(row - (int64_t)tok * a.G), 4 * x, w);
+    store_dims<4>(a.out, q.first + tok, head * a.G + (int)(row - (uint32_t)tok * (uint32_t)a.G), 4 * x, w);
 }
 
 // Query rows of an item: the fewest columns that hold what a sequence has (by the caller's max_q), so that
@@ -1084,8 +1106,8 @@ template <int D, int N> int launch_attn(AttnArgs &a, int grid, int nseq, void *s
     // no item is cut when none has more than one tile
     if ((int64_t)a.width * a.page <= kTile) return QG_OK;
     if (a.by_item)
-        return launch_pdl(attn_kv4_join_kernel<D, N, 1>, dim3((unsigned)items, N), dim3(256), 0, stream, a);
-    return launch_pdl(attn_kv4_join_kernel<D, N, 4>, dim3(grid, N / 4), dim3(256), 0, stream, a);
+        return launch_pdl(attn_kv4_join_kernel<D, N, 1>, dim3((unsigned)items, N), dim3(512), 0, stream, a);
+    return launch_pdl(attn_kv4_join_kernel<D, N, 4>, dim3(grid, N / 4), dim3(512), 0, stream, a);
 }
 
 template <int D> int launch_rows(AttnArgs &a, int N, int grid, int nseq, void *stream)
@@ -1131,6 +1153,7 @@ int qg_attn_kv4(const qg_heads *q, int64_t T, int nseq, const int32_t *q_start, 
         return QG_ERR_ALIGN;
     int sms = 0;
     if ((rc = current_sms(&sms)) != QG_OK) return rc;
+    if (sms > kMostParts / 4) return QG_ERR_SHAPE;  // (no such device)
     a.G = Hq / Hk;
     const int N = rows_of((int64_t)max_q * a.G);
     const WsLayout w = ws_layout(D, N, sms);
