@@ -44,8 +44,8 @@
 #include "qg_ptx.cuh"
 #include "qg_tcgen05.cuh"
 
-#ifndef QG_W2
-#define QG_W2 32
+#ifndef QG_VU
+#define QG_VU 1
 #endif
 #ifndef QG_KU
 #define QG_KU 1
@@ -58,7 +58,8 @@ constexpr int kTile = 128;                      // places of a tile
 constexpr int kTileBlocks = kTile / kKvBlock;
 constexpr float kMoveMax = 8.0f;                // a score this far above the reference moves it
 constexpr float kWeightShift = 7.0f;
-constexpr int kKeyUnroll = QG_KU;
+constexpr int kKeyUnroll = QG_KU, kValueUnroll = QG_VU;
+constexpr int kHoleBar = 10;                    // named barriers 10, 11: the value warpgroups
 constexpr int kMetas = 16;                      // tiles whose description is kept (more than any role lags)
 
 // flags of a tile
@@ -189,7 +190,10 @@ __device__ __forceinline__ float order_float(int b) { return __int_as_float(b ^ 
 
 template <int D, int N> struct Cfg {
     using F = Kv4<D>;
-    static constexpr int kSub = (D == 256 && N == 128) ? 4 : 2;  // operand buffers hold 1 / kSub of a tile
+    static constexpr int kWork = N <= 32 ? 2 : 1;                // warpgroups for the keys, and for the values
+    // operand buffers hold 1 / kSub of a tile; with two warpgroups there is one more than they fill at once
+    static constexpr int kSub = D == 256 ? (N == 128 ? 4 : 2) : (N <= 32 ? 1 : 2);
+    static constexpr int kBufs = N <= 32 ? 3 : 2;
     static constexpr int kMh = D >= 128 ? D / 128 : 1;           // M = 128 halves of O^T
     static constexpr int kKCols = D / 2 / kSub;                  // columns of a key buffer: D / kSub dimensions
     static constexpr int kVTok = kTile / kSub;                   // places of a value buffer
@@ -198,10 +202,9 @@ template <int D, int N> struct Cfg {
     static constexpr int kPBufs = (D == 256 && N == 128) ? 1 : 2;
     static constexpr int kSoft = N > 32 ? N / 32 : 1;            // softmax warpgroups
     static constexpr int kNS = N / kSoft;                        // query rows of each
-    static constexpr int kWork = N <= QG_W2 ? 2 : 1;             // warpgroups for the keys, and for the values
-    static constexpr int kWarps = 4 * (2 * kWork + kSoft) + 2;
+    static constexpr int kWarps = 4 * (2 * kWork + kSoft) + 3;
     // tensor memory columns
-    static constexpr int kK = 0, kV = kK + 2 * kKCols, kS = kV + 2 * kVCols * kMh, kO = kS + kSBufs * N;
+    static constexpr int kK = 0, kV = kK + kBufs * kKCols, kS = kV + kBufs * kVCols * kMh, kO = kS + kSBufs * N;
     static constexpr int kCols = kO + kMh * N;
     static_assert(kCols <= 512, "tensor memory");
     // shared memory
@@ -221,7 +224,7 @@ template <int D, int N> struct Cfg {
 
 template <int N> struct Small {
     uint64_t ring_full[8], ring_empty[8];
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], p_full[2], p_empty[2], q_full[2];
+    uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3], s_full[2], s_empty[2], p_full[2], p_empty[2], q_full[2];
     uint64_t o_full, o_empty;
     Meta meta[kMetas];
     Cursor found;
@@ -246,7 +249,11 @@ __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, int *dead, 
     const uint32_t b = smem_u32(bar);
     if (mbar_try_wait(b, parity)) return;
     const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(b, parity)) {
+    for (;;) {
+        // (a try suspends the warp for a while only: keep what is issued between tries short)
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(b, parity)) return;
         if (*(volatile int *)dead) return;
         if (global_timer_ns() - t0 > kWaitNs) {
             *(volatile int *)dead = 1;
@@ -323,24 +330,26 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
 {
     using F = Kv4<D>;
     using C = Cfg<D, N>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(16) Small<N> sm;
     static_assert(C::kBytes + sizeof(Small<N>) <= 227 * 1024, "shared memory of a block");
     static_assert(offsetof(Small<N>, base) % 16 == 0 && offsetof(Small<N>, lim) % 16 == 0, "read four at a time");
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp-uniform)
     const int cta = blockIdx.x, grid = gridDim.x;
-    constexpr int kProducer = C::kWarps - 2, kIssuer = C::kWarps - 1;
+    constexpr int kProducer = C::kWarps - 3, kIssuer = C::kWarps - 2;  // (and the second products' issuer)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(smem_u32(&sm.ring_full[i]), 1);
             mbar_init(smem_u32(&sm.ring_empty[i]), 8 * C::kWork);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(smem_u32(&sm.k_full[i]), 4);
             mbar_init(smem_u32(&sm.k_empty[i]), 1);
             mbar_init(smem_u32(&sm.v_full[i]), 4);
             mbar_init(smem_u32(&sm.v_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.s_full[i]), 1);
             mbar_init(smem_u32(&sm.s_empty[i]), 4 * C::kSoft);
             mbar_init(smem_u32(&sm.p_full[i]), 4 * C::kSoft);
@@ -491,16 +500,15 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
             // one copy for each run of neighbouring blocks of a page
             const int in_page = (int)((uint32_t)(c.unit * kTileBlocks + lane) % (uint32_t)page_blocks);
             const int64_t blk = (pg * a.Hk + c.head) * page_blocks + in_page;
-            uint32_t heads = __ballot_sync(0xffffffffu, ok && (lane == 0 || in_page == 0));
-            while (heads) {
-                const int l = __ffs(heads) - 1;
-                heads &= heads - 1;
-                const int64_t from = __shfl_sync(0xffffffffu, blk, l);
+            const uint32_t heads = __ballot_sync(0xffffffffu, ok && (lane == 0 || in_page == 0));
+            if ((heads >> lane) & 1) {
                 // down to the next run, or the last block that is there (a run has no gaps: one page)
-                const uint32_t rest = heads ? (1u << (__ffs(heads) - 1)) - 1 : 0xffffffffu;
-                const int run = __popc(valid & rest & ~((1u << l) - 1));
-                bulk_g2s_elect(smem_u32(smem + st * C::kTileBytes + l * F::kBlock), a.cache + from * F::kBlock, run * F::kBlock, bar);
+                const uint32_t later = heads & ~((2u << lane) - 1);
+                const uint32_t rest = later ? (1u << (__ffs(later) - 1)) - 1 : 0xffffffffu;
+                const int run = __popc(valid & rest & ~((1u << lane) - 1));
+                bulk_g2s_plain(smem_u32(smem + st * C::kTileBytes + lane * F::kBlock), a.cache + blk * F::kBlock, run * F::kBlock, bar);
             }
+            __syncwarp();
             if (lane == 0) {
                 Meta &m = sm.meta[i % kMetas];
                 const int left = c.units - c.unit - 1;
@@ -546,15 +554,16 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                 (void)mbar_wait_bounded(smem_u32(&sm.ring_full[st]), 1);
             }
         if (lane == 0 && count > 0 && !a.by_item && !any_cut) a.cut[cta] = make_int4(0, 0, 0, 0);
-    } else if (warp == kIssuer) {
-        // ---- the matrix instructions: the warp stays together, an elected lane issues
-        {
-            constexpr uint32_t kIdesc1 = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
-            constexpr uint32_t kIdesc2 = kIdesc1 | (1u << 16);  // B (the weights) with the query rows contiguous
-            const uint32_t qa = smem_u32(smem + C::kQ), pa = smem_u32(smem + C::kP);
-            int seg = 0;  // parts of items begun
+    } else if (warp >= kIssuer) {
+        // ---- the matrix instructions: a warp for the scores and one for the weighted sums, so that neither waits
+        // for the other's operands; a warp stays together, an elected lane issues
+        constexpr uint32_t kIdesc1 = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
+        constexpr uint32_t kIdesc2 = kIdesc1 | (1u << 16);  // B (the weights) with the query rows contiguous
+        int seg = 0;  // parts of items begun
+        if (warp == kIssuer) {
+            const uint32_t qa = smem_u32(smem + C::kQ);
             uint32_t qb = qa;
-            auto scores = [&](int i) {
+            for (int i = 0; i < count; ++i) {
                 const int sb = i % C::kSBufs;
                 wait_described(&sm.produced, i + 1, dead, a.err);
                 if (__shfl_sync(0xffffffffu, sm.meta[i % kMetas].flags, 0) & kFirst) {
@@ -564,45 +573,45 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                 }
                 if (i >= C::kSBufs) wait(&sm.s_empty[sb], ((i / C::kSBufs) & 1) ^ 1, dead, a.err);
                 for (int h = 0; h < C::kSub; ++h) {
-                    const int u = i * C::kSub + h, b = u & 1;
-                    wait(&sm.k_full[b], (u >> 1) & 1, dead, a.err);
+                    const int u = i * C::kSub + h, b = u % C::kBufs;
+                    wait(&sm.k_full[b], (u / C::kBufs) & 1, dead, a.err);
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < D / C::kSub / 16; ++k) {
                         const int step = h * (D / C::kSub / 16) + k;
                         umma_f16_ts_elect(tmem + C::kS + sb * N, tmem + C::kK + b * C::kKCols + 8 * k,
-                                    umma_desc_none(qb + step * 32 * N, 16 * N, 128), kIdesc1, step > 0);
+                                          umma_desc_none(qb + step * 32 * N, 16 * N, 128), kIdesc1, step > 0);
                     }
                     umma_commit_elect(smem_u32(&sm.k_empty[b]));
                 }
                 umma_commit_elect(smem_u32(&sm.s_full[sb]));
-            };
-            if (count > 0) scores(0);
-            int done = 0;  // parts of items finished
+            }
+        } else {
+            const uint32_t pa = smem_u32(smem + C::kP);
             for (int i = 0; i < count; ++i) {
-                const int flags = __shfl_sync(0xffffffffu, sm.meta[i % kMetas].flags, 0);
-                if (i + 1 < count) scores(i + 1);  // (with one score buffer: once the softmax has read it)
                 const int pb = i % C::kPBufs;
-                if ((flags & kFirst) && done > 0) wait(&sm.o_empty, (done - 1) & 1, dead, a.err);
+                wait_described(&sm.produced, i + 1, dead, a.err);
+                const int flags = __shfl_sync(0xffffffffu, sm.meta[i % kMetas].flags, 0);
+                if (flags & kFirst) {
+                    if (seg > 0) wait(&sm.o_empty, (seg - 1) & 1, dead, a.err);
+                    ++seg;
+                }
                 wait(&sm.p_full[pb], (i / C::kPBufs) & 1, dead, a.err);
                 for (int h = 0; h < C::kSub; ++h) {
-                    const int u = i * C::kSub + h, b = u & 1;
-                    wait(&sm.v_full[b], (u >> 1) & 1, dead, a.err);
+                    const int u = i * C::kSub + h, b = u % C::kBufs;
+                    wait(&sm.v_full[b], (u / C::kBufs) & 1, dead, a.err);
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < C::kVTok / 16; ++k)
 #pragma unroll
                         for (int mh = 0; mh < C::kMh; ++mh)
                             umma_f16_ts_elect(tmem + C::kO + mh * N, tmem + C::kV + (b * C::kMh + mh) * C::kVCols + 8 * k,
-                                        umma_desc_none(pa + pb * C::kPBytes + (h * (C::kVTok / 16) + k) * 256, 128, 16 * kTile), kIdesc2,
-                                        !((flags & kFirst) && h == 0 && k == 0));
+                                              umma_desc_none(pa + pb * C::kPBytes + (h * (C::kVTok / 16) + k) * 256, 128, 16 * kTile), kIdesc2,
+                                              !((flags & kFirst) && h == 0 && k == 0));
                     umma_commit_elect(smem_u32(&sm.v_empty[b]));
                 }
                 umma_commit_elect(smem_u32(&sm.p_empty[pb]));
-                if (flags & kLast) {
-                    umma_commit_elect(smem_u32(&sm.o_full));
-                    ++done;
-                }
+                if (flags & kLast) umma_commit_elect(smem_u32(&sm.o_full));
             }
         }
     } else if (warp < 4 * C::kWork) {
@@ -610,30 +619,32 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
         const int wk = C::kWork > 1 ? warp >> 2 : 0;
         const int t = (warp & 3) * 32 + lane;
         const int blk = t / kKvBlock, tok = t % kKvBlock;
-        const int sw = kv4_swizzle(tok) & F::kChunkMask;
+        // offsets in a tile of this place's first chunk and scales: a chunk's number is xored in, since rows
+        // of chunks are aligned to their size
+        const int code_at = blk * F::kBlock + tok * F::kCodeRow + ((kv4_swizzle(tok) & F::kChunkMask) << 4);
+        const int scale_at = blk * F::kBlock + F::kCodes + tok * F::kGroups * 4;
+        static_assert(F::kBlock % F::kCodeRow == 0 && C::kTileBytes % F::kCodeRow == 0, "rows of chunks are aligned");
         constexpr int kChunks = D / 32 / C::kSub;  // of a buffer
         for (int i = 0; i < count; ++i) {
             const int st = i % C::kStages;
             wait(&sm.ring_full[st], (i / C::kStages) & 1, dead, a.err);
-            const uint8_t *row = smem + st * C::kTileBytes + blk * F::kBlock + tok * F::kCodeRow;
-            const uint8_t *scales = smem + st * C::kTileBytes + blk * F::kBlock + F::kCodes + tok * F::kGroups * 4;
-            uint4 next = *reinterpret_cast<const uint4 *>(row + (((wk * kChunks) ^ sw) << 4));
+            const uint8_t *kb = smem + st * C::kTileBytes;
             // short loops: three roles' instructions have to fit the instruction caches
 #pragma unroll 1
-            for (int h = wk; h < C::kSub; h += C::kWork) {
-                const int u = i * C::kSub + h, b = u & 1;
-                if (u >= 2) {
-                    wait(&sm.k_empty[b], ((u >> 1) & 1) ^ 1, dead, a.err);
+            for (int h = (wk + i * C::kSub) % C::kWork; h < C::kSub; h += C::kWork) {
+                const int u = i * C::kSub + h, b = u % C::kBufs;
+                if (u >= C::kBufs) {
+                    wait(&sm.k_empty[b], ((u / C::kBufs) & 1) ^ 1, dead, a.err);
                     tc_fence_after();
                 }
                 const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kK + b * C::kKCols;
+                uint4 next = *reinterpret_cast<const uint4 *>(kb + (code_at ^ (h * kChunks << 4)));
 #pragma unroll kKeyUnroll
                 for (int c = 0; c < kChunks; ++c) {
                     const int ch = h * kChunks + c;
                     const uint32_t x[4] = {next.x, next.y, next.z, next.w};
-                    const uint32_t sc = *reinterpret_cast<const uint32_t *>(scales + (ch >> 1) * 4);
-                    const int after = c + 1 < kChunks ? ch + 1 : ch + 1 + (C::kWork - 1) * kChunks;
-                    next = *reinterpret_cast<const uint4 *>(row + (((after & F::kChunkMask) ^ sw) << 4));
+                    const uint32_t sc = *reinterpret_cast<const uint32_t *>(kb + scale_at + (ch >> 1) * 4);
+                    if (c + 1 < kChunks) next = *reinterpret_cast<const uint4 *>(kb + (code_at ^ ((ch + 1) << 4)));
                     const __half2 d = __low2half2(as_h2(sc)), m = __high2half2(as_h2(sc));
                     uint32_t r[16];
 #pragma unroll
@@ -673,18 +684,26 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
             const int st = i % C::kStages;
             wait(&sm.ring_full[st], (i / C::kStages) & 1, dead, a.err);
             const Meta &m = sm.meta[i % kMetas];
-            const bool hole = m.flags & kHole;
-            const int valid = m.valid, room = m.room;  // places of the tile that are there
+            if (m.flags & kHole) {
+                // places that are not there hold anything, NaN among it: this warpgroup zeroes the scales of its own
+                // places, a thread a place
+                const int pl = w * 32 + lane;
+                if ((C::kWork == 1 || (i * C::kSub + pl / C::kVTok) % 2 == wv) && (!((m.valid >> (pl / kKvBlock)) & 1) || pl >= m.room))
+                    for (int g = 0; g < F::kGroups; ++g)
+                        *reinterpret_cast<uint32_t *>(smem + st * C::kTileBytes + (pl / kKvBlock) * F::kBlock + F::kPart + F::kCodes +
+                                                      ((pl % kKvBlock) * F::kGroups + g) * 4) = 0;
+                bar_sync(kHoleBar + wv, 128);
+            }
 #pragma unroll 1
-            for (int h = wv; h < C::kSub; h += C::kWork) {
-                const int u = i * C::kSub + h, b = u & 1;
+            for (int h = (wv + i * C::kSub) % C::kWork; h < C::kSub; h += C::kWork) {
+                const int u = i * C::kSub + h, b = u % C::kBufs;
                 const uint8_t *vb = smem + st * C::kTileBytes + F::kPart + h * (C::kVTok / kKvBlock) * F::kBlock;
-                if (u >= 2) {
-                    wait(&sm.v_empty[b], ((u >> 1) & 1) ^ 1, dead, a.err);
+                if (u >= C::kBufs) {
+                    wait(&sm.v_empty[b], ((u / C::kBufs) & 1) ^ 1, dead, a.err);
                     tc_fence_after();
                 }
                 if (!idle) {
-#pragma unroll 1
+#pragma unroll kValueUnroll
                     for (int p = 0; p < C::kVTok; p += kStep, vb += (kStep / kKvBlock) * F::kBlock) {
                         uint32_t x[4];
                         ldmatrix_x4_trans(smem_u32(vb + code_at), x);
@@ -692,14 +711,8 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
 #pragma unroll
                         for (int e = 0; e < kStep / 8; ++e) {
                             const uint8_t *sp = vb + scale_at + (e >> 1) * F::kBlock + (e & 1) * 8 * F::kGroups * 4;
-                            uint32_t s0 = *reinterpret_cast<const uint32_t *>(sp);
-                            uint32_t s1 = *reinterpret_cast<const uint32_t *>(sp + F::kGroups * 4);
-                            if (hole) {  // places that are not there hold anything, NaN among it
-                                const int pl = h * C::kVTok + p + 8 * e + 2 * (lane & 3);
-                                const bool there = (valid >> (pl / kKvBlock)) & 1;
-                                if (!there || pl >= room) s0 = 0;
-                                if (!there || pl + 1 >= room) s1 = 0;
-                            }
+                            const uint32_t s0 = *reinterpret_cast<const uint32_t *>(sp);
+                            const uint32_t s1 = *reinterpret_cast<const uint32_t *>(sp + F::kGroups * 4);
                             dd[e] = as_h2(__byte_perm(s0, s1, 0x5410));
                             mm[e] = as_h2(__byte_perm(s0, s1, 0x7632));
                         }
@@ -944,38 +957,44 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                 tc_fence_after();
                 bar_sync(bar_id, 128);
                 // ---- O, some rows at a time through shared memory (the weights' buffers are free now)
+                // (loops kept rolled: this code is seldom in the instruction caches)
 #pragma unroll 1
                 for (int c = 0; c < NS; c += C::kOutRows) {
+#pragma unroll 1
+                    for (int z = 0; z < C::kMh * C::kOutRows; z += 8) {
+                        const int mh = z / C::kOutRows, c8 = z % C::kOutRows;
+                        float o[8];
+                        TmemRead<8>::run(quad + C::kO + mh * N + n0 + c + c8, o);
+                        float *to = stage + c8 * C::kOutStride + o_dim<D>(t, mh);
+                        if (D > 64 || t < 64) {
 #pragma unroll
-                    for (int mh = 0; mh < C::kMh; ++mh) {
-                        const int dim = o_dim<D>(t, mh);
-#pragma unroll
-                        for (int c8 = 0; c8 < C::kOutRows; c8 += 8) {
-                            float o[8];
-                            TmemRead<8>::run(quad + C::kO + mh * N + n0 + c + c8, o);
-                            if (D > 64 || t < 64) {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) stage[(c8 + e) * C::kOutStride + dim] = o[e] * sm.inv[n0 + c + c8 + e];
-                            }
+                            for (int e = 0; e < 8; ++e) to[e * C::kOutStride] = o[e] * sm.inv[n0 + c + c8 + e];
                         }
                     }
                     bar_sync(bar_id, 128);
-#pragma unroll 2
+#pragma unroll 1
                     for (int y = t; y < C::kOutRows * kVec; y += 128) {
                         const int e = y / kVec, g = y % kVec;
                         const int64_t at = sm.orow[seg & 1][n0 + c + e];
                         const float4 v0 = *reinterpret_cast<const float4 *>(stage + e * C::kOutStride + 8 * g);
                         const float4 v1 = *reinterpret_cast<const float4 *>(stage + e * C::kOutStride + 8 * g + 4);
-                        if (at >= 0) {
-                            if (complete) {
-                                const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-                                HeadsView o = a.out;
-                                o.p = static_cast<__half *>(a.out.p) + at;
-                                store_dims<8>(o, 0, 0, 8 * g, v);
+                        if (at < 0) continue;
+                        if (!complete) {
+                            float *dst = a.part + ((int64_t)slot * N + n0 + c + e) * D + 8 * g;
+                            *reinterpret_cast<float4 *>(dst) = v0;
+                            *reinterpret_cast<float4 *>(dst + 4) = v1;
+                        } else {
+                            __half *dst = static_cast<__half *>(a.out.p) + at + 8 * g * a.out.sd;
+                            const uint4 h = make_uint4(pack_h2(v0.x, v0.y), pack_h2(v0.z, v0.w), pack_h2(v1.x, v1.y), pack_h2(v1.z, v1.w));
+                            if (a.out.vec > 1) {
+                                *reinterpret_cast<uint4 *>(dst) = h;
                             } else {
-                                float *dst = a.part + ((int64_t)slot * N + n0 + c + e) * D + 8 * g;
-                                *reinterpret_cast<float4 *>(dst) = v0;
-                                *reinterpret_cast<float4 *>(dst + 4) = v1;
+                                const uint32_t hh[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) {
+                                    dst[2 * x * a.out.sd] = __low2half(as_h2(hh[x]));
+                                    dst[(2 * x + 1) * a.out.sd] = __high2half(as_h2(hh[x]));
+                                }
                             }
                         }
                     }
