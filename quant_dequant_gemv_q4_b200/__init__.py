@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -110,7 +111,7 @@ def lib() -> ctypes.CDLL:
         L.qg_hbm_copy.restype = I
         L.qg_hbm_read.argtypes = [P, SZ, P, P]
         L.qg_hbm_read.restype = I
-        F, DBL, HP = ctypes.c_float, ctypes.c_double, ctypes.POINTER(qg_heads)
+        F, DBL, HP = ctypes.c_float, ctypes.c_double, ctypes.c_void_p  # (HP: a qg_heads by reference, or its bytes)
         L.qg_qk_norm_rope.argtypes = [HP, HP, I64, I, I, I, P, P, DBL, P, P, I, I, HP, HP, P]
         L.qg_qk_norm_rope.restype = I
         L.qg_kv4_bytes.argtypes = [I64, I, I, I]
@@ -282,58 +283,77 @@ def qg_hbm_read(src, nbytes: int, out, stream=None) -> None:
     _ok(lib().qg_hbm_read(_ptr(src), int(nbytes), _ptr(out), _stream(stream)), "qg_hbm_read")
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+# The operators around the GEMVs are short (a few microseconds on the GPU), so what their wrappers do on the
+# host counts: torch is looked up once, views go to C as packed bytes, and the checks are a few attribute reads.
+_tc = None
+_pack_heads = struct.Struct("@Pqqqi4x").pack  # qg_heads
 
 
-def _on_device(what: str, *tensors) -> None:
-    """Every tensor (None apart) is on the current CUDA device, where the kernels run."""
-    import torch
-    dev = torch.cuda.current_device()
+class _Torch:
+    def __init__(self):
+        import torch
+        self.f32, self.f16, self.f64 = torch.float32, torch.float16, torch.float64
+        self.i32, self.i64, self.u8 = torch.int32, torch.int64, torch.uint8
+        self.empty, self.device = torch.empty, torch.cuda.current_device
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _torch() -> _Torch:
+    global _tc
+    if _tc is None:
+        _tc = _Torch()
+    return _tc
+
+
+def _where(tc, what: str, *tensors) -> int:
+    """The current device; every tensor (None apart) has to be on it, where the kernels run."""
+    dev = tc.device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"{what}: every tensor must be on the current CUDA device ({dev}), got {t.device}")
+    return dev
 
 
-def _heads(t, what: str) -> qg_heads:
-    import torch
-    if t.dtype is torch.float32:
-        kind = QG_TYPE_F32
-    elif t.dtype is torch.float16:
-        kind = QG_TYPE_F16
-    else:
-        raise ValueError(f"{what}: fp32 or fp16, got {t.dtype}")
-    _need(t.dim() == 3, f"{what}: [tokens, heads, dims]")
-    return qg_heads(t.data_ptr(), *t.stride(), kind)
+def _handle(tc, stream, dev: int) -> int:
+    if stream is None:
+        return tc.stream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _vector(t, dtype: str, n: int, what: str):
-    """A contiguous vector of n elements of the named type, or None."""
-    import torch
-    if t is not None:
-        _need(t.dtype is getattr(torch, dtype) and t.dim() == 1 and t.shape[0] == n and t.is_contiguous(),
-              f"{what}: contiguous {dtype} [{n}], got {t.dtype} {tuple(t.shape)}")
-        return t.data_ptr()
-    return None
+def _view(tc, t, what: str, name: str) -> bytes:
+    """A [tokens, heads, dims] tensor as a qg_heads."""
+    dt, st = t.dtype, t.stride()
+    if (dt is not tc.f32 and dt is not tc.f16) or len(st) != 3:
+        raise ValueError(f"{what}: {name} is fp32 or fp16 [tokens, heads, dims], got {dt} {tuple(t.shape)}")
+    return _pack_heads(t.data_ptr(), st[0], st[1], st[2], QG_TYPE_F32 if dt is tc.f32 else QG_TYPE_F16)
 
 
-def _cache_sizes(cache, page: int, what: str):
-    import torch
-    _need(cache.dtype is torch.uint8 and cache.dim() == 4 and cache.is_contiguous(),
-          f"{what}: the cache is contiguous uint8 [pages, heads, page / 16, 18 D]")
-    pages, H, blocks, width = cache.shape
-    _need(page >= 16 and blocks * 16 == page and width % 18 == 0,
-          f"{what}: a cache of shape {tuple(cache.shape)} does not hold pages of {page} tokens")
-    return pages, H, width // 18
+def _vec(t, dtype, n: int, what: str, name: str):
+    """The address of a contiguous vector of n elements of a type, or None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what}: {name} is a contiguous {dtype} [{n}], got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
-def _rope(pos, inv_freq, T: int, what: str):
-    R = 0 if inv_freq is None else 2 * inv_freq.shape[0]
-    if R:
-        _need(pos is not None, f"{what}: a rotation needs positions")
-        return _vector(pos, "int32", T, f"{what}: pos"), _vector(inv_freq, "float64", R // 2, f"{what}: inv_freq"), R
-    return None, None, 0
+def _cache_sizes(tc, cache, page: int, what: str):
+    if cache.dtype is tc.u8 and cache.dim() == 4 and cache.is_contiguous():
+        pages, H, blocks, width = cache.shape
+        if page >= 16 and blocks * 16 == page and width % 18 == 0:
+            return pages, H, width // 18
+    raise ValueError(f"{what}: the cache is contiguous uint8 [pages, heads, page / 16, 18 D] with pages of {page} "
+                     f"tokens, got {cache.dtype} {tuple(cache.shape)}")
+
+
+def _rope(tc, pos, inv_freq, T: int, what: str):
+    if inv_freq is None:
+        return None, None, 0
+    if pos is None:
+        raise ValueError(f"{what}: a rotation needs positions")
+    n = inv_freq.numel()
+    return _vec(pos, tc.i32, T, what, "pos"), _vec(inv_freq, tc.f64, n, what, "inv_freq"), 2 * n
 
 
 def qg_kv4_bytes(pages: int, page: int, H: int, D: int) -> int:
@@ -353,63 +373,75 @@ def qg_qk_norm_rope(q, k, wq, wk, eps: float, pos, inv_freq, pairing: int, q_out
     """Head norms (weights wq, wk fp32 [D]; None: no norm) and the rotation by pos * inv_freq (int32 [T],
     float64 [R / 2]; inv_freq None: no rotation) of q [T, Hq, D] and k [T, Hk, D] (either may be None)."""
     what = "qg_qk_norm_rope"
+    tc = _tc or _torch()
     some = q if q is not None else k
-    _need(some is not None, f"{what}: q or k")
-    _on_device(what, q, k, wq, wk, pos, inv_freq, q_out, k_out)
+    if some is None or some.dim() != 3:
+        raise ValueError(f"{what}: q or k, [tokens, heads, dims]")
+    dev = _where(tc, what, q, k, wq, wk, pos, inv_freq, q_out, k_out)
     T, _, D = some.shape
-    hv, H = [], []
-    for x, y, n in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            hv += [None, None]
-            H.append(0)
-            continue
-        _need(y is not None and x.shape == y.shape and x.shape[0] == T and x.shape[2] == D,
-              f"{what}: {n} and {n}_out are [{T}, heads, {D}]")
-        hv += [ctypes.byref(_heads(x, f"{what}: {n}")), ctypes.byref(_heads(y, f"{what}: {n}_out"))]
-        H.append(x.shape[1])
-    pp, pf, R = _rope(pos, inv_freq, T, what)
-    _ok(lib().qg_qk_norm_rope(hv[0], hv[2], T, H[0], H[1], D, _vector(wq, "float32", D, f"{what}: wq"),
-                              _vector(wk, "float32", D, f"{what}: wk"), float(eps), pp, pf, R, int(pairing),
-                              hv[1], hv[3], _stream(stream)), what)
+    vq = vk = oq = ok = None
+    Hq = Hk = 0
+    if q is not None:
+        Hq = q.shape[1]
+        if q_out is None or q_out.shape != q.shape:
+            raise ValueError(f"{what}: q and q_out are [{T}, heads, {D}]")
+        vq, oq = _view(tc, q, what, "q"), _view(tc, q_out, what, "q_out")
+    if k is not None:
+        Hk = k.shape[1]
+        if k_out is None or k_out.shape != k.shape or k.shape[0] != T or k.shape[2] != D:
+            raise ValueError(f"{what}: k and k_out are [{T}, heads, {D}]")
+        vk, ok = _view(tc, k, what, "k"), _view(tc, k_out, what, "k_out")
+    pp, pf, R = _rope(tc, pos, inv_freq, T, what)
+    rc = (_lib or lib()).qg_qk_norm_rope(vq, vk, T, Hq, Hk, D, _vec(wq, tc.f32, D, what, "wq"),
+                                         _vec(wk, tc.f32, D, what, "wk"), eps, pp, pf, R, pairing, oq, ok,
+                                         _handle(tc, stream, dev))
+    if rc:
+        raise QgError(rc, what)
 
 
 def qg_kv4_append(k, v, wk, eps: float, pos, inv_freq, pairing: int, slot, cache, page: int, stream=None) -> None:
     """Appends k, v [T, H, D] to the 4-bit cache at slot int64 [T] (-1: not written), the key with its head
     norm (wk None: none) and rotation (inv_freq None: none) applied on the way."""
     what = "qg_kv4_append"
-    _on_device(what, k, v, wk, pos, inv_freq, slot, cache)
-    pages, H, D = _cache_sizes(cache, page, what)
+    tc = _tc or _torch()
+    dev = _where(tc, what, k, v, wk, pos, inv_freq, slot, cache)
+    pages, H, D = _cache_sizes(tc, cache, page, what)
     T = k.shape[0]
-    _need(k.shape == v.shape and tuple(k.shape[1:]) == (H, D), f"{what}: k and v are [tokens, {H}, {D}]")
-    pp, pf, R = _rope(pos, inv_freq, T, what)
-    _ok(lib().qg_kv4_append(ctypes.byref(_heads(k, f"{what}: k")), ctypes.byref(_heads(v, f"{what}: v")), T, H, D,
-                            _vector(wk, "float32", D, f"{what}: wk"), float(eps), pp, pf, R, int(pairing),
-                            _vector(slot, "int64", T, f"{what}: slot"), cache.data_ptr(), pages, int(page),
-                            _stream(stream)), what)
+    if k.shape != v.shape or k.shape[1:] != (H, D):
+        raise ValueError(f"{what}: k and v are [tokens, {H}, {D}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    pp, pf, R = _rope(tc, pos, inv_freq, T, what)
+    rc = (_lib or lib()).qg_kv4_append(_view(tc, k, what, "k"), _view(tc, v, what, "v"), T, H, D,
+                                       _vec(wk, tc.f32, D, what, "wk"), eps, pp, pf, R, pairing,
+                                       _vec(slot, tc.i64, T, what, "slot"), cache.data_ptr(), pages, page,
+                                       _handle(tc, stream, dev))
+    if rc:
+        raise QgError(rc, what)
 
 
 def qg_kv4_read(cache, page: int, slot, k_out, v_out, stream=None) -> None:
     """The values that the slots (int64 [T]) of the cache hold, into k_out and v_out [T, H, D]."""
     what = "qg_kv4_read"
-    _on_device(what, cache, slot, k_out, v_out)
-    pages, H, D = _cache_sizes(cache, page, what)
-    T = slot.shape[0]
-    _need(tuple(k_out.shape) == (T, H, D) and k_out.shape == v_out.shape, f"{what}: k_out and v_out are [{T}, {H}, {D}]")
-    _ok(lib().qg_kv4_read(cache.data_ptr(), pages, int(page), H, D, _vector(slot, "int64", T, f"{what}: slot"), T,
-                          ctypes.byref(_heads(k_out, f"{what}: k_out")), ctypes.byref(_heads(v_out, f"{what}: v_out")),
-                          _stream(stream)), what)
+    tc = _tc or _torch()
+    dev = _where(tc, what, cache, slot, k_out, v_out)
+    pages, H, D = _cache_sizes(tc, cache, page, what)
+    T = slot.numel()
+    if k_out.shape != (T, H, D) or v_out.shape != (T, H, D):
+        raise ValueError(f"{what}: k_out and v_out are [{T}, {H}, {D}]")
+    rc = (_lib or lib()).qg_kv4_read(cache.data_ptr(), pages, page, H, D, _vec(slot, tc.i64, T, what, "slot"), T,
+                                     _view(tc, k_out, what, "k_out"), _view(tc, v_out, what, "v_out"),
+                                     _handle(tc, stream, dev))
+    if rc:
+        raise QgError(rc, what)
 
 
 _attn_ws: dict = {}
 
 
-def qg_attn_kv4_workspace(Hq: int, Hk: int, D: int, max_q: int) -> int:
-    """Workspace bytes of qg_attn_kv4 on the current device."""
-    import torch
-    key = (torch.cuda.current_device(), Hq, Hk, D, max_q)
+def _workspace_bytes(dev: int, Hq: int, Hk: int, D: int, max_q: int) -> int:
+    key = (dev, Hq, Hk, D, max_q)
     n = _attn_ws.get(key)
     if n is None:
-        n = int(lib().qg_attn_kv4_workspace(int(Hq), int(Hk), int(D), int(max_q)))
+        n = int(lib().qg_attn_kv4_workspace(Hq, Hk, D, max_q))
         if n == 0:
             raise QgError(QG_ERR_SHAPE, "qg_attn_kv4_workspace")
         if len(_attn_ws) >= 4096:
@@ -418,46 +450,61 @@ def qg_attn_kv4_workspace(Hq: int, Hk: int, D: int, max_q: int) -> int:
     return n
 
 
+def qg_attn_kv4_workspace(Hq: int, Hk: int, D: int, max_q: int) -> int:
+    """Workspace bytes of qg_attn_kv4 on the current device."""
+    return _workspace_bytes(_torch().device(), int(Hq), int(Hk), int(D), int(max_q))
+
+
 def qg_attn_kv4(q, q_start, max_q: int, cache, page: int, table, kv_len, scale: float, out, workspace=None,
                 stream=None) -> None:
     """Causal attention of the new tokens q [T, Hq, D] (fp16; sequence s: rows q_start[s] .. q_start[s + 1] - 1)
     over the 4-bit cache, sequence s having kv_len[s] places in the pages table[s], into out [T, Hq, D] (fp16).
-    workspace: uint8, qg_attn_kv4_workspace(Hq, Hk, D, max_q) bytes, not shared with a call that may overlap; None takes one
-    from torch's allocator for this call."""
-    import torch
+    workspace: uint8, qg_attn_kv4_workspace(Hq, Hk, D, max_q) bytes, not shared with a call that may overlap;
+    None takes one from torch's allocator for this call."""
     what = "qg_attn_kv4"
-    _on_device(what, q, q_start, cache, table, kv_len, out, workspace)
-    pages, Hk, D = _cache_sizes(cache, page, what)
-    _need(q.dtype is torch.float16 and out.dtype is torch.float16, f"{what}: q and out are fp16")
-    _need(q.dim() == 3 and q.shape == out.shape and q.shape[2] == D, f"{what}: q and out are [tokens, heads, {D}]")
+    tc = _tc or _torch()
+    dev = _where(tc, what, q, q_start, cache, table, kv_len, out, workspace)
+    pages, Hk, D = _cache_sizes(tc, cache, page, what)
+    if q.dtype is not tc.f16 or out.dtype is not tc.f16 or q.dim() != 3 or q.shape != out.shape or q.shape[2] != D:
+        raise ValueError(f"{what}: q and out are fp16 [tokens, heads, {D}]")
+    if table.dtype is not tc.i32 or table.dim() != 2 or not table.is_contiguous():
+        raise ValueError(f"{what}: table is contiguous int32 [sequences, pages]")
     T, Hq, _ = q.shape
-    _need(table.dtype is torch.int32 and table.dim() == 2 and table.is_contiguous(), f"{what}: table is contiguous int32 [sequences, pages]")
     nseq, width = table.shape
-    ps = _vector(q_start, "int32", nseq + 1, f"{what}: q_start")
-    pl = _vector(kv_len, "int32", nseq, f"{what}: kv_len")
-    st = _stream(stream)
+    st = _handle(tc, stream, dev)
     if workspace is None:
-        _need(st == torch.cuda.current_stream().cuda_stream, f"{what}: a call on a stream that is not torch's current one needs a workspace")
-        workspace = torch.empty(qg_attn_kv4_workspace(Hq, Hk, D, max_q), dtype=torch.uint8, device=q.device)
-    _ok(lib().qg_attn_kv4(ctypes.byref(_heads(q, what)), T, nseq, ps, int(max_q), Hq, Hk, D, cache.data_ptr(), pages,
-                          int(page), table.data_ptr(), width, pl, float(scale), ctypes.byref(_heads(out, what)),
-                          workspace.data_ptr(), workspace.numel() * workspace.element_size(), st), what)
+        if stream is not None and st != tc.stream(dev):
+            raise ValueError(f"{what}: a call on a stream that is not torch's current one needs a workspace")
+        n = _workspace_bytes(dev, Hq, Hk, D, max_q)
+        workspace = tc.empty(n, dtype=tc.u8, device=q.device)
+    else:
+        n = workspace.numel() * workspace.element_size()
+    rc = (_lib or lib()).qg_attn_kv4(_view(tc, q, what, "q"), T, nseq, _vec(q_start, tc.i32, nseq + 1, what, "q_start"),
+                                     max_q, Hq, Hk, D, cache.data_ptr(), pages, page, table.data_ptr(), width,
+                                     _vec(kv_len, tc.i32, nseq, what, "kv_len"), scale, _view(tc, out, what, "out"),
+                                     workspace.data_ptr(), n, st)
+    if rc:
+        raise QgError(rc, what)
 
 
 def qg_sample(logits, temperature, top_k, top_p, min_p, u, token, stream=None) -> None:
     """One token a row of logits [rows, V] (fp32, any strides: a GEMV's y.view(V, B).t()) with the row's
     temperature, top_k (int32), top_p and min_p (None: no such filter) from the random numbers u, into token
     (int32 [rows])."""
-    import torch
     what = "qg_sample"
-    _on_device(what, logits, temperature, top_k, top_p, min_p, u, token)
-    _need(logits.dtype is torch.float32 and logits.dim() == 2, f"{what}: logits are fp32 [rows, V]")
+    tc = _tc or _torch()
+    dev = _where(tc, what, logits, temperature, top_k, top_p, min_p, u, token)
+    if logits.dtype is not tc.f32 or logits.dim() != 2:
+        raise ValueError(f"{what}: logits are fp32 [rows, V]")
     R, V = logits.shape
     rs, es = logits.stride()
-    _ok(lib().qg_sample(logits.data_ptr(), R, V, rs, es, _vector(temperature, "float32", R, f"{what}: temperature"),
-                        _vector(top_k, "int32", R, f"{what}: top_k"), _vector(top_p, "float32", R, f"{what}: top_p"),
-                        _vector(min_p, "float32", R, f"{what}: min_p"), _vector(u, "float32", R, f"{what}: u"),
-                        _vector(token, "int32", R, f"{what}: token"), _stream(stream)), what)
+    f32 = tc.f32
+    rc = (_lib or lib()).qg_sample(logits.data_ptr(), R, V, rs, es, _vec(temperature, f32, R, what, "temperature"),
+                                   _vec(top_k, tc.i32, R, what, "top_k"), _vec(top_p, f32, R, what, "top_p"),
+                                   _vec(min_p, f32, R, what, "min_p"), _vec(u, f32, R, what, "u"),
+                                   _vec(token, tc.i32, R, what, "token"), _handle(tc, stream, dev))
+    if rc:
+        raise QgError(rc, what)
 
 
 def gemv(W, fmt: int, N: int, K: int, x, variant: int = QG_VARIANT_AUTO, stream=None):

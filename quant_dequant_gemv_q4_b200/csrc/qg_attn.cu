@@ -44,12 +44,6 @@
 #include "qg_ptx.cuh"
 #include "qg_tcgen05.cuh"
 
-#ifndef QG_VU
-#define QG_VU 1
-#endif
-#ifndef QG_KU
-#define QG_KU 1
-#endif
 namespace {
 
 using namespace qg;
@@ -58,7 +52,6 @@ constexpr int kTile = 128;                      // places of a tile
 constexpr int kTileBlocks = kTile / kKvBlock;
 constexpr float kMoveMax = 8.0f;                // a score this far above the reference moves it
 constexpr float kWeightShift = 7.0f;
-constexpr int kKeyUnroll = QG_KU, kValueUnroll = QG_VU;
 constexpr int kHoleBar = 10;                    // named barriers 10, 11: the value warpgroups
 constexpr int kMetas = 16;                      // tiles whose description is kept (more than any role lags)
 
@@ -625,11 +618,11 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
         const int scale_at = blk * F::kBlock + F::kCodes + tok * F::kGroups * 4;
         static_assert(F::kBlock % F::kCodeRow == 0 && C::kTileBytes % F::kCodeRow == 0, "rows of chunks are aligned");
         constexpr int kChunks = D / 32 / C::kSub;  // of a buffer
+        constexpr int kPer = N > 32 && kChunks > 1 ? 2 : 1;
         for (int i = 0; i < count; ++i) {
             const int st = i % C::kStages;
             wait(&sm.ring_full[st], (i / C::kStages) & 1, dead, a.err);
             const uint8_t *kb = smem + st * C::kTileBytes;
-            // short loops: three roles' instructions have to fit the instruction caches
 #pragma unroll 1
             for (int h = (wk + i * C::kSub) % C::kWork; h < C::kSub; h += C::kWork) {
                 const int u = i * C::kSub + h, b = u % C::kBufs;
@@ -638,24 +631,28 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                     tc_fence_after();
                 }
                 const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kK + b * C::kKCols;
-                uint4 next = *reinterpret_cast<const uint4 *>(kb + (code_at ^ (h * kChunks << 4)));
-#pragma unroll kKeyUnroll
-                for (int c = 0; c < kChunks; ++c) {
+                // Short loops: with few query rows four warps of a scheduler unpack, in two loops that ought to
+                // stay in its instruction cache (unrolled twice, 200001 places took 72 us instead of 69).
+#pragma unroll 1
+                for (int c = 0; c < kChunks; c += kPer) {
                     const int ch = h * kChunks + c;
-                    const uint32_t x[4] = {next.x, next.y, next.z, next.w};
                     const uint32_t sc = *reinterpret_cast<const uint32_t *>(kb + scale_at + (ch >> 1) * 4);
-                    if (c + 1 < kChunks) next = *reinterpret_cast<const uint4 *>(kb + (code_at ^ ((ch + 1) << 4)));
-                    const __half2 d = __low2half2(as_h2(sc)), m = __high2half2(as_h2(sc));
-                    uint32_t r[16];
+                    uint32_t x[4 * kPer], r[16 * kPer];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int y = 0; y < kPer; ++y) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(kb + (code_at ^ ((ch + y) << 4)));
+                        x[4 * y] = v.x, x[4 * y + 1] = v.y, x[4 * y + 2] = v.z, x[4 * y + 3] = v.w;
+                    }
+                    const __half2 d = __low2half2(as_h2(sc)), m = __high2half2(as_h2(sc));
+#pragma unroll
+                    for (int e = 0; e < 4 * kPer; ++e) {
                         const uint32_t x8 = x[e] >> 8;
                         r[4 * e] = dequant_lo(x[e], d, m);
                         r[4 * e + 1] = dequant_hi(x[e], d, m);
                         r[4 * e + 2] = dequant_lo(x8, d, m);
                         r[4 * e + 3] = dequant_hi(x8, d, m);
                     }
-                    tmem_st_32x32b(to + 16 * c, r);
+                    TmemWrite32<16 * kPer>::run(to + 16 * c, r);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -670,6 +667,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
         const int w = warp & 3;
         const int wv = C::kWork > 1 ? (warp >> 2) - 2 : 0;
         constexpr int kStep = D == 256 ? 16 : 32;  // places of one ldmatrix
+        constexpr int kBatch = N > 32 && C::kVTok >= 32 ? 32 : kStep;  // places written at once (a short loop, as for the keys)
         const bool idle = D == 64 && w >= 2;       // lanes 64 .. 127 of O^T hold nothing
         const int group = D == 256 ? w : D == 128 ? w >> 1 : 0;
         // where this lane reads within a step: the row it addresses (a 16-byte chunk of a place), and the
@@ -703,44 +701,47 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                     tc_fence_after();
                 }
                 if (!idle) {
-#pragma unroll kValueUnroll
-                    for (int p = 0; p < C::kVTok; p += kStep, vb += (kStep / kKvBlock) * F::kBlock) {
-                        uint32_t x[4];
-                        ldmatrix_x4_trans(smem_u32(vb + code_at), x);
-                        __half2 dd[kStep / 8], mm[kStep / 8];
-#pragma unroll
-                        for (int e = 0; e < kStep / 8; ++e) {
-                            const uint8_t *sp = vb + scale_at + (e >> 1) * F::kBlock + (e & 1) * 8 * F::kGroups * 4;
-                            const uint32_t s0 = *reinterpret_cast<const uint32_t *>(sp);
-                            const uint32_t s1 = *reinterpret_cast<const uint32_t *>(sp + F::kGroups * 4);
-                            dd[e] = as_h2(__byte_perm(s0, s1, 0x5410));
-                            mm[e] = as_h2(__byte_perm(s0, s1, 0x7632));
-                        }
+#pragma unroll 1
+                    for (int p = 0; p < C::kVTok; p += kBatch) {
                         // the operand's registers: D = 256, by nibble, (chunk 2w, 2w + 1) of each 8 places;
                         // else by pair of nibbles, (nibble 2q, 2q + 1) of each 8 places
-                        uint32_t r[D == 256 ? 4 : 2][kStep / 4];
+                        uint32_t r[D == 256 ? 4 : 2][kBatch / 4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int g = D == 256 ? e >> 1 : e;
-                            const uint32_t x8 = x[e] >> 8;
-                            const uint32_t v[4] = {dequant_lo(x[e], dd[g], mm[g]), dequant_hi(x[e], dd[g], mm[g]),
-                                                   dequant_lo(x8, dd[g], mm[g]), dequant_hi(x8, dd[g], mm[g])};
+                        for (int z = 0; z < kBatch / kStep; ++z, vb += (kStep / kKvBlock) * F::kBlock) {
+                            uint32_t x[4];
+                            ldmatrix_x4_trans(smem_u32(vb + code_at), x);
+                            __half2 dd[kStep / 8], mm[kStep / 8];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                if constexpr (D == 256)
-                                    r[j][e] = v[j];
-                                else
-                                    r[j >> 1][2 * e + (j & 1)] = v[j];
+                            for (int e = 0; e < kStep / 8; ++e) {
+                                const uint8_t *sp = vb + scale_at + (e >> 1) * F::kBlock + (e & 1) * 8 * F::kGroups * 4;
+                                const uint32_t s0 = *reinterpret_cast<const uint32_t *>(sp);
+                                const uint32_t s1 = *reinterpret_cast<const uint32_t *>(sp + F::kGroups * 4);
+                                dd[e] = as_h2(__byte_perm(s0, s1, 0x5410));
+                                mm[e] = as_h2(__byte_perm(s0, s1, 0x7632));
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int g = D == 256 ? e >> 1 : e;
+                                const uint32_t x8 = x[e] >> 8;
+                                const uint32_t v[4] = {dequant_lo(x[e], dd[g], mm[g]), dequant_hi(x[e], dd[g], mm[g]),
+                                                       dequant_lo(x8, dd[g], mm[g]), dequant_hi(x8, dd[g], mm[g])};
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    if constexpr (D == 256)
+                                        r[j][4 * z + e] = v[j];
+                                    else
+                                        r[j >> 1][8 * z + 2 * e + (j & 1)] = v[j];
+                                }
                             }
                         }
                         const uint32_t col = lanes + b * C::kMh * C::kVCols + p / 2;
                         if constexpr (D == 256) {
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                TmemWrite16<2>::run(col + ((uint32_t)(16 * (j & 1)) << 16) + (j >> 1) * C::kVCols, r[j]);
+                                TmemWrite16<kBatch / 8>::run(col + ((uint32_t)(16 * (j & 1)) << 16) + (j >> 1) * C::kVCols, r[j]);
                         } else {
 #pragma unroll
-                            for (int q = 0; q < 2; ++q) TmemWrite16<4>::run(col + ((uint32_t)(16 * q) << 16), r[q]);
+                            for (int q = 0; q < 2; ++q) TmemWrite16<kBatch / 8>::run(col + ((uint32_t)(16 * q) << 16), r[q]);
                         }
                     }
                     tmem_wait_st();
@@ -903,7 +904,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                         TmemRead<16>::run(at, o);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e] * sm.factor[n0 + y % NS + e]);
-                        tmem_st_32x32b(at, r);
+                        TmemWrite32<16>::run(at, r);
                     }
                     tmem_wait_st();
                 }
