@@ -425,10 +425,15 @@ int qg_attn_kv4(const qg_heads *q, int64_t T, int nseq, const int32_t *q_start, 
  *   rows, V      rows >= 0, 1 <= V < 2^31
  *   temperature, top_p, min_p (fp32), top_k (int32)  device, [rows]; NULL for 1, 1, 0 and 0
  *   u            device, fp32 [rows], 0 <= u < 1;  token  device, int32 [rows]
- * Weights are summed as 64-bit whole numbers: the token does not depend on timing. */
+ *   workspace    device, 4-byte aligned, qg_sample_workspace(rows, V, elem_stride) bytes (0 for rows that
+ *                stand one after another), not shared with a call that may overlap; NULL does without, more
+ *                slowly
+ * Weights are summed as 64-bit whole numbers: the token does not depend on timing.  Errors: QG_ERR_SHAPE,
+ * _NULL, _ALIGN, _SCRATCH (a workspace too small), _CUDA. */
+size_t qg_sample_workspace(int64_t rows, int64_t V, int64_t elem_stride);
 int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t row_stride, int64_t elem_stride,
               const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
-              const float *u, int32_t *token, void *stream);
+              const float *u, int32_t *token, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Static text for a status code. */
 const char *qg_status_string(int status);

@@ -124,7 +124,9 @@ def lib() -> ctypes.CDLL:
         L.qg_attn_kv4_workspace.restype = SZ
         L.qg_attn_kv4.argtypes = [HP, I64, I, P, I, I, I, I, P, I64, I, P, I, P, F, HP, P, SZ, P]
         L.qg_attn_kv4.restype = I
-        L.qg_sample.argtypes = [P, I64, I64, I64, I64, P, P, P, P, P, P, P]
+        L.qg_sample_workspace.argtypes = [I64, I64, I64]
+        L.qg_sample_workspace.restype = SZ
+        L.qg_sample.argtypes = [P, I64, I64, I64, I64, P, P, P, P, P, P, P, SZ, P]
         L.qg_sample.restype = I
         L.qg_status_string.argtypes = [I]
         L.qg_status_string.restype = ctypes.c_char_p
@@ -487,22 +489,37 @@ def qg_attn_kv4(q, q_start, max_q: int, cache, page: int, table, kv_len, scale: 
         raise QgError(rc, what)
 
 
-def qg_sample(logits, temperature, top_k, top_p, min_p, u, token, stream=None) -> None:
+def qg_sample_workspace(rows: int, V: int, elem_stride: int) -> int:
+    """Workspace bytes of qg_sample; 0 for rows that stand one after another."""
+    return int(lib().qg_sample_workspace(int(rows), int(V), int(elem_stride)))
+
+
+def qg_sample(logits, temperature, top_k, top_p, min_p, u, token, workspace=None, stream=None) -> None:
     """One token a row of logits [rows, V] (fp32, any strides: a GEMV's y.view(V, B).t()) with the row's
     temperature, top_k (int32), top_p and min_p (None: no such filter) from the random numbers u, into token
-    (int32 [rows])."""
+    (int32 [rows]).  workspace: uint8, qg_sample_workspace(rows, V, stride) bytes, not shared with a call that
+    may overlap; None takes one from torch's allocator for this call."""
     what = "qg_sample"
     tc = _tc or _torch()
-    dev = _where(tc, what, logits, temperature, top_k, top_p, min_p, u, token)
+    dev = _where(tc, what, logits, temperature, top_k, top_p, min_p, u, token, workspace)
     if logits.dtype is not tc.f32 or logits.dim() != 2:
         raise ValueError(f"{what}: logits are fp32 [rows, V]")
     R, V = logits.shape
     rs, es = logits.stride()
     f32 = tc.f32
+    st = _handle(tc, stream, dev)
+    wp, wn = None, 0
+    if workspace is not None:
+        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif es != 1 and R > 1:
+        if stream is not None and st != tc.stream(dev):
+            raise ValueError(f"{what}: a call on a stream that is not torch's current one needs a workspace")
+        workspace = tc.empty(R * V, dtype=f32, device=logits.device)
+        wp, wn = workspace.data_ptr(), R * V * 4
     rc = (_lib or lib()).qg_sample(logits.data_ptr(), R, V, rs, es, _vec(temperature, f32, R, what, "temperature"),
                                    _vec(top_k, tc.i32, R, what, "top_k"), _vec(top_p, f32, R, what, "top_p"),
                                    _vec(min_p, f32, R, what, "min_p"), _vec(u, f32, R, what, "u"),
-                                   _vec(token, tc.i32, R, what, "token"), _handle(tc, stream, dev))
+                                   _vec(token, tc.i32, R, what, "token"), wp, wn, st)
     if rc:
         raise QgError(rc, what)
 

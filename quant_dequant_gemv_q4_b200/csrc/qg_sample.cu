@@ -2,26 +2,29 @@
 // and contract: include/qg.h.
 //
 // With z = logit / temperature, in descending order (equal logits: the lower index first):
-//   top-k keeps the first k; top-p keeps, of those, the shortest prefix whose share of their weight
-//   w = exp(z - z_max) reaches p; min-p drops weights below min_p; the token is the first in the
-//   vocabulary's order whose running weight exceeds u times the kept weight.
+//   top-k keeps the first k; top-p keeps, of those, each token before which less than p of their weight
+//   w = exp(z - z_max) lies; min-p drops weights below min_p; the token is the first in the vocabulary's
+//   order whose running weight exceeds u times the kept weight.
+// Each filter keeps a prefix of the descending order, so the kept tokens are those above a logit and the
+// first few equal to it: a cut.
 //
-// One thread-block cluster takes a row and keeps it in its shared memory (up to eight CTAs, so 248,320
-// logits are read once from HBM), so the passes over the row run on chip.  The row is never sorted:
+// One thread-block cluster takes a row and keeps it in its shared memory (up to sixteen CTAs, so 248,320
+// logits are read once), and the passes over the row run on chip.  The row is never sorted:
 //   1. the largest logit;
-//   2. a histogram (counts, and weights where they are needed) over bins linear in the logit, which
-//      spread the bulk of a vocabulary over many bins; all CTAs add up the cluster's histograms over
-//      distributed shared memory and find the bin in which the k-th token or the p-th share falls;
-//   3. if the tokens down to that bin are few (kList), they are gathered in one CTA, where each
-//      thread compares one token with all others and so knows its rank, the weight before it and its
-//      running weight in index order: filters and choice follow at once;
-//   4. otherwise the cut (a logit and how many of the tokens equal to it stay) is found in that bin
-//      alone, by lists or finer histograms, and a pass in index order finds the token.
+//   2. a histogram of counts over bins linear in z, 128 a unit, and (for top-p) the exact sum of all weights;
+//   3. the bins in which the cut lies: exactly known for the k-th token; for top-p, since a bin's weights
+//      are within a factor e^(1/128) of each other, the weight below a bin is bounded on both sides by the
+//      counts, which leaves two or three bins.  If the tokens down to the last of these are at most kList,
+//      they are gathered in one CTA, sorted, filtered and chosen from;
+//   4. otherwise only the tokens of those bins are gathered and sorted (or, should they be too many, counted in
+//      finer and finer bins), together with the exact weight above them, which gives the cut; a pass over the
+//      row in index order then finds the token.
 //
-// Weights are whole multiples of 2^-44 of the largest (64-bit integers from 64-bit exponentials): their
-// sums do not depend on the order of the additions, atomic ones among them, so a call gives the same
-// token every time; and with errors of 2^-45 a weight the choice is that of the exact formula but for
-// u within about 1e-9 of a border.
+// Weights are whole multiples of 2^-44 of the largest (64-bit integers): their sums do not depend on the order
+// of the additions, so a call gives the same token every time.  A weight is off by about 2^-30 of itself
+// (Row::weight), in either direction, so running sums over many tokens are off by far less, and the choice is
+// that of the exact formula but for u (or a filter's border) within about 1e-9 of a border.  64-bit
+// exponentials instead (exact to 2^-45) took 113 cycles of a scheduler for 32 of them, this form a third.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -34,11 +37,15 @@ namespace {
 using namespace qg;
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 1024;
-constexpr int kBins = 2048;
-constexpr int kList = 1024;
-constexpr int kMaxCluster = 8;
-constexpr double kWeightOne = 17592186044416.0;  // 2^44
+constexpr int kThreads = 512;  // (with 1024 the scans and sorts, which every warp runs, cost more than they saved)
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 4096;
+constexpr int kPer = kBins / kThreads;  // bins of a thread
+constexpr float kBinsPerUnit = 128.0f;
+constexpr float kBinStep = 0.9922179382602435f;  // e^(-1/128)
+constexpr int kList = 512;
+constexpr int kMaxCluster = 16;  // (more than eight: not on every device of this kind, but on this one)
+constexpr double kOne = 17592186044416.0;  // the largest weight, 2^44
 typedef unsigned long long u64;
 
 struct SampleArgs {
@@ -52,60 +59,104 @@ struct SampleArgs {
 };
 
 struct Shared {
-    u64 weight[kBins];
-    unsigned count[kBins];
-    u64 lw[kList];
-    float lx[kList];
-    int64_t li[kList];
+    alignas(16) unsigned count[kBins];
+    alignas(16) unsigned total[kBins];  // of the cluster
+    u64 list[kList];  // key << 32 | ~index (the cluster's, in its first CTA)
+    u64 own[kList];   // the CTA's part of the list; weights of finer histograms
+    u64 t64[64];      // 2^(i / 64) in 2^-44
+    unsigned t32[64];  // and in 2^-30
     // exchanged over the cluster
     float top;
     int64_t best;
-    unsigned listed;
+    unsigned listed, klo, khi, cut_key, cut_ties, cta_ties;
     u64 cta_weight;
-    unsigned cta_ties;
-    unsigned klo, khi;
-    // results of the CTA's own searches
-    u64 scan_w[32];
-    unsigned scan_c[32];
-    int bin;
-    unsigned before_c, in_bin;
-    u64 before_w, total_w;
-    unsigned cut_key, cut_ties;
-    double cut_u;
-    int64_t pick;
+    // the CTA's own
+    unsigned own_listed, own_at;
+    u64 scan_w[kWarps];
+    unsigned scan_c[kWarps];
+    float scan_f[2][kWarps];
+    int bin[2];
+    unsigned before[2], in_bin;
+    u64 fine_before;
 };
 
-// logits in an order-preserving integer form; -inf (and NaN) lowest
+// logits in an order-preserving integer form
 __device__ __forceinline__ unsigned key_of(float x)
 {
     const unsigned b = __float_as_uint(x);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ float of_key(unsigned k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 
 __device__ __forceinline__ float clean(float x)
 {
-    x += 0.0f;                          // -0 and +0 are equal
-    return x != x ? -INFINITY : x;      // NaN is never chosen
+    x += 0.0f;                      // -0 and +0 are equal
+    return x != x ? -INFINITY : x;  // NaN is never chosen
 }
 
 struct Row {
     const SampleArgs &a;
     const float *slice;
+    const u64 *t64;
+    const unsigned *t32;
     int64_t row, base;
     int n;
-    double inv_t, zmax;
     float xmax;
+    double c, zc;  // log2(e) / temperature, and the largest logit times it
+    float ch, cl;  // c as the sum of two floats
 
     __device__ __forceinline__ float get(int i) const
     {
         return a.resident ? slice[i] : clean(a.x[row * a.rs + (base + i) * a.es]);
     }
-    __device__ __forceinline__ double ratio(float x) const
+    // f(i, x) for the CTA's logits, four a thread in flight
+    template <typename F> __device__ __forceinline__ void each(F f) const
     {
-        if (x == xmax) return 1.0;
-        return exp((double)x * inv_t - zmax);  // 0 for -inf, and below +inf
+        int i = threadIdx.x;
+        for (; i + 3 * kThreads < n; i += 4 * kThreads) {
+            float x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = get(i + j * kThreads);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f(i + j * kThreads, x[j]);
+        }
+        for (; i < n; i += kThreads) f(i, get(i));
     }
-    __device__ __forceinline__ u64 weight(float x) const { return __double2ull_rn(ratio(x) * kWeightOne); }
+    // The weight in whole 2^-44, without a branch (several are in flight).  t = (xmax - x) c is formed as a sum of
+    // two floats (the difference and the product with their rounding errors: about 2^-46 of t), and
+    // 2^-t = 2^-q 2^(j/64) e^y with t = n / 64 + r, y = -r ln 2, |r| <= 1/128: a table in 64 bits, and the Taylor
+    // series of e^y - 1 to the third power in fp32 (2^-24 of at most 0.0055; the fourth power is below 4e-11).
+    __device__ __forceinline__ u64 weight(float x) const
+    {
+        const float d = xmax - x;
+        const float v = d - xmax;
+        const float dl = (xmax - (d - v)) - (x + v);
+        const float t0 = d * ch;
+        const float t = fminf(t0, 60.0f);  // (also takes a NaN: two infinities)
+        const float tl = fmaf(d, ch, -t0) + fmaf(d, cl, dl * ch);
+        const float m = fmaf(t, 64.0f, 12582912.0f);  // 1.5 * 2^23: the sum's low bits are 64 t, rounded
+        const int n64 = __float_as_int(m) - 0x4b400000;
+        const float y = (fmaf(m - 12582912.0f, -1.0f / 64.0f, t) + tl) * -0.693147180559945f;
+        const float e = y * fmaf(y, fmaf(y, 1.0f / 6.0f, 0.5f), 1.0f);
+        const int q = (n64 + 63) >> 6, j = (q << 6) - n64;
+        const long long w = (long long)t64[j] + (((long long)t32[j] * __float2int_rn(e * 274877906944.0f)) >> 24);  // 2^38
+        const u64 r = (u64)(w + ((1ll << q) >> 1)) >> q;
+        return x == xmax ? 1ull << 44 : t < 46.0f ? r : 0;
+    }
+    // whether the weight is at least min_p (decided in 64 bits where it is close)
+    __device__ __forceinline__ bool at_least(float x, u64 w, double min_p) const
+    {
+        if (x == xmax) return true;
+        const double least = min_p * kOne;
+        if (fabs((double)w - least) > least * 1e-6 + 2.0) return (double)w > least;
+        return exp2(fma((double)x, c, -zc)) >= min_p;
+    }
+    // bin of the histogram: linear and monotone in x, the largest logit in bin 0
+    __device__ __forceinline__ int bin(float x, float scale) const
+    {
+        const float d = (xmax - x) * scale;
+        return x == xmax ? 0 : d < (float)(kBins - 1) ? (int)d : kBins - 1;
+    }
 };
 
 template <typename T> __device__ __forceinline__ T warp_incl(T v, int lane)
@@ -116,6 +167,24 @@ template <typename T> __device__ __forceinline__ T warp_incl(T v, int lane)
         if (lane >= o) v += w;
     }
     return v;
+}
+
+template <typename T> __device__ __forceinline__ T warp_total(T v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Sum of w over the block.
+__device__ __forceinline__ u64 block_sum(Shared &s, u64 w)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    w = warp_total(w);
+    __syncthreads();
+    if (lane == 0) s.scan_w[warp] = w;
+    __syncthreads();
+    return warp_total(lane < kWarps ? s.scan_w[lane] : 0ull);
 }
 
 // Exclusive prefix over the block's threads of (c, w), and the totals.
@@ -130,83 +199,167 @@ __device__ __forceinline__ void block_scan(Shared &s, unsigned c, u64 w, unsigne
         s.scan_w[warp] = wi;
     }
     __syncthreads();
-    if (warp == 0) {
-        const unsigned cw = warp_incl(s.scan_c[lane], lane);
-        const u64 ww = warp_incl(s.scan_w[lane], lane);
-        s.scan_c[lane] = cw;
-        s.scan_w[lane] = ww;
-    }
-    __syncthreads();
-    *c_before = ci - c + (warp ? s.scan_c[warp - 1] : 0);
-    *w_before = wi - w + (warp ? s.scan_w[warp - 1] : 0);
-    *c_all = s.scan_c[31];
-    *w_all = s.scan_w[31];
+    const unsigned cw = warp_incl(lane < kWarps ? s.scan_c[lane] : 0u, lane);
+    const u64 ww = warp_incl(lane < kWarps ? s.scan_w[lane] : 0ull, lane);
+    const unsigned cb = __shfl_sync(0xffffffffu, cw, warp > 0 ? warp - 1 : 0);
+    const u64 wb = __shfl_sync(0xffffffffu, ww, warp > 0 ? warp - 1 : 0);
+    *c_before = ci - c + (warp ? cb : 0);
+    *w_before = wi - w + (warp ? wb : 0);
+    *c_all = __shfl_sync(0xffffffffu, cw, 31);
+    *w_all = __shfl_sync(0xffffffffu, ww, 31);
 }
 
-// Adds up the cluster's histograms and finds the bin where the cumulative count reaches want_c (by
-// weight: where the cumulative weight first reaches want_w).  Every CTA finds the same.
-__device__ void find_bin(cg::cluster_group &cl, Shared &s, bool by_weight, unsigned want_c, double share, u64 want_w)
+// Sum of a CTA's value over the cluster: each warp fetches the CTAs' values with one load.
+template <typename T> __device__ __forceinline__ T over_cluster(cg::cluster_group &cl, Shared &s, T Shared::*field)
 {
-    cl.sync();  // all histograms are whole
-    constexpr int PB = kBins / kThreads;
-    unsigned c[PB];
-    u64 w[PB];
-    unsigned cs = 0;
-    u64 ws = 0;
-#pragma unroll
-    for (int b = 0; b < PB; ++b) {
-        c[b] = 0;
-        w[b] = 0;
-        for (unsigned r = 0; r < cl.num_blocks(); ++r) {
-            const Shared *o = cl.map_shared_rank(&s, r);
-            c[b] += o->count[threadIdx.x * PB + b];
-            w[b] += o->weight[threadIdx.x * PB + b];
-        }
-        cs += c[b];
-        ws += w[b];
+    const unsigned lane = threadIdx.x & 31;
+    return warp_total(lane < cl.num_blocks() ? cl.map_shared_rank(&s, lane)->*field : T(0));
+}
+
+// Descending sort of one 64-bit value a thread (bitonic: exchanges within a warp by shuffles, between warps
+// through shared memory); m values, the others 0.  Warps past the power of two that holds m take no part.
+__device__ __forceinline__ u64 block_sort(u64 v, u64 *buf, int m)
+{
+    const int t = threadIdx.x;
+    int size = 32;
+    while (size < m) size <<= 1;
+    if (t < size) {
+        for (int k = 2; k <= size; k <<= 1)
+            for (int j = k >> 1; j > 0; j >>= 1) {
+                u64 o;
+                if (j >= 32) {
+                    asm volatile("bar.sync 1, %0;" ::"r"(size) : "memory");
+                    buf[t] = v;
+                    asm volatile("bar.sync 1, %0;" ::"r"(size) : "memory");
+                    o = buf[t ^ j];
+                } else {
+                    o = __shfl_xor_sync(0xffffffffu, v, j);
+                }
+                const bool low = (t & j) == 0, down = (t & k) == 0;
+                v = (low == down) == (v > o) ? v : o;
+            }
     }
+    __syncthreads();
+    return v;
+}
+
+// The cluster's histogram, kPer bins a thread.  Each CTA adds up its share of the bins and hands the sums to
+// all (every CTA reading every histogram took four times as long with sixteen).
+__device__ __forceinline__ void cluster_counts(cg::cluster_group &cl, Shared &s, unsigned (&c)[kPer])
+{
+    const unsigned n = cl.num_blocks(), share = kBins / n;
+    cl.sync();  // all histograms are whole
+    if (n > 1) {
+        for (unsigned b = threadIdx.x; b < share; b += kThreads) {
+            const unsigned at = cl.block_rank() * share + b;
+            unsigned v[kMaxCluster], sum = 0;
+#pragma unroll
+            for (unsigned r = 0; r < kMaxCluster; ++r) v[r] = r < n ? cl.map_shared_rank(&s, r)->count[at] : 0;
+#pragma unroll
+            for (unsigned r = 0; r < kMaxCluster; ++r) sum += v[r];
+#pragma unroll
+            for (unsigned r = 0; r < kMaxCluster; ++r)
+                if (r < n) cl.map_shared_rank(&s, r)->total[at] = sum;
+        }
+        cl.sync();
+    }
+    const uint4 *from = reinterpret_cast<const uint4 *>(&(n > 1 ? s.total : s.count)[kPer * threadIdx.x]);
+#pragma unroll
+    for (int j = 0; j < kPer; j += 4) {
+        const uint4 v = from[j / 4];
+        c[j] = v.x, c[j + 1] = v.y, c[j + 2] = v.z, c[j + 3] = v.w;
+    }
+}
+
+// The bin in which the k-th token lies, with the tokens before it and in it.  Returns the number of all.
+__device__ unsigned find_count(Shared &s, const unsigned (&c)[kPer], unsigned k)
+{
+    unsigned sum = 0, cb, ca;
+    u64 wb, wa;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) sum += c[j];
+    block_scan(s, sum, 0, &cb, &wb, &ca, &wa);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        if (cb < k && cb + c[j] >= k) {
+            s.bin[0] = s.bin[1] = kPer * threadIdx.x + j;
+            s.before[0] = cb;
+            s.in_bin = c[j];
+        }
+        cb += c[j];
+    }
+    __syncthreads();
+    return ca;
+}
+
+// The bins between which the cut of top-p lies: the first whose lower bound, and the first whose upper bound,
+// of the weight after it is at most `tail`.  s.before[0]: tokens before the first, s.before[1]: down to the
+// last of them (of all tokens, `c`; the weights are those of `kept` of them).  The bounds' margin of 1e-4
+// covers the bins' borders and these sums, all in fp32.
+__device__ void find_share(Shared &s, const unsigned (&c)[kPer], const unsigned (&kept)[kPer], float tail)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b0 = kPer * threadIdx.x;
+    float edge = expf(-(float)b0 / kBinsPerUnit), h = 0.0f, l = 0.0f;
+    float hi[kPer], lo[kPer];  // weight of a bin, at most and at least
+    unsigned sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        hi[j] = (float)kept[j] * edge * 1.0001f;
+        edge *= kBinStep;
+        lo[j] = b0 + j == kBins - 1 ? 0.0f : (float)kept[j] * edge * 0.9999f;
+        h += hi[j];
+        l += lo[j];
+        sum += c[j];
+    }
+    // of the bins after the thread's
+    float hs = h, ls = l;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float x = __shfl_down_sync(0xffffffffu, hs, o), y = __shfl_down_sync(0xffffffffu, ls, o);
+        if (lane + o < 32) {
+            hs += x;
+            ls += y;
+        }
+    }
+    if (lane == 0) {
+        s.scan_f[0][warp] = hs;
+        s.scan_f[1][warp] = ls;
+    }
+    float after_h = __shfl_down_sync(0xffffffffu, hs, 1), after_l = __shfl_down_sync(0xffffffffu, ls, 1);
+    if (lane == 31) after_h = after_l = 0.0f;
     unsigned cb, ca;
     u64 wb, wa;
-    block_scan(s, cs, ws, &cb, &wb, &ca, &wa);
-    // `share` >= 0: the wanted weight is that share of all
-    const double target = share >= 0.0 ? share * (double)wa : (double)want_w;
-    if (threadIdx.x == 0) s.bin = -1;
+    block_scan(s, sum, 0, &cb, &wb, &ca, &wa);
+    if (threadIdx.x == 0) {  // (should rounding hide a border from both of its threads: all bins)
+        s.bin[0] = 0;
+        s.before[0] = 0;
+        s.bin[1] = kBins - 1;
+        s.before[1] = ca;
+    }
+    const bool later = lane > warp && lane < kWarps;
+    after_h += warp_total(later ? s.scan_f[0][lane] : 0.0f);
+    after_l += warp_total(later ? s.scan_f[1][lane] : 0.0f);
     __syncthreads();
+    // up through the thread's bins: the weight after bin j, and after the bin before it
+    cb += sum;
 #pragma unroll
-    for (int b = 0; b < PB; ++b) {
-        const bool here = by_weight ? ((double)wb < target && (double)(wb + w[b]) >= target)
-                                    : (cb < want_c && cb + c[b] >= want_c);
-        if (here) {
-            s.bin = threadIdx.x * PB + b;
-            s.before_c = cb;
-            s.before_w = wb;
-            s.in_bin = c[b];
+    for (int j = kPer - 1; j >= 0; --j) {
+        const bool first = b0 + j == 0;
+        if (after_l <= tail && (first || after_l + lo[j] > tail)) {
+            s.bin[0] = b0 + j;
+            s.before[0] = cb - c[j];
         }
-        cb += c[b];
-        wb += w[b];
+        if (after_h <= tail && (first || after_h + hi[j] > tail)) {
+            s.bin[1] = b0 + j;
+            s.before[1] = cb;
+        }
+        after_l += lo[j];
+        after_h += hi[j];
+        cb -= c[j];
     }
-    if (threadIdx.x == 0) s.total_w = wa;
-    cl.sync();  // the histograms may be cleared
+    __syncthreads();
 }
-
-__device__ __forceinline__ void clear_hist(Shared &s)
-{
-    for (int b = threadIdx.x; b < kBins; b += kThreads) {
-        s.count[b] = 0;
-        s.weight[b] = 0;
-    }
-}
-
-// Bins of the first histogram: linear in the logit, 64 a unit of z.
-struct LinearBins {
-    float xmax, scale;
-    __device__ __forceinline__ int operator()(float x) const
-    {
-        if (x == xmax) return 0;
-        const float d = (xmax - x) * scale;  // monotone in x
-        return d < (float)(kBins - 1) ? (int)d : kBins - 1;
-    }
-};
 
 __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
 {
@@ -216,78 +369,79 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
     cg::cluster_group cl = cg::this_cluster();
     const int rank = cl.block_rank(), C = cl.num_blocks();
     const int64_t row = blockIdx.x / C;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, tid = threadIdx.x;
+
+    for (int b = tid; b < kBins; b += kThreads) s.count[b] = 0;
+    if (tid < 64) {
+        const double v = exp2(tid / 64.0);
+        s.t64[tid] = __double2ull_rn(v * kOne);
+        s.t32[tid] = __double2uint_rn(v * 1073741824.0);
+    }
+    if (tid == 0) {
+        s.best = INT64_MAX;
+        s.listed = s.own_listed = 0;
+        s.klo = 0xffffffffu;
+        s.khi = 0;
+    }
     pdl_launch_dependents();
     pdl_wait();
 
+    // ---- the row into shared memory, and its largest logit
     const int64_t base = (int64_t)rank * a.per;
     const int n = (int)(base < a.V ? (a.V - base < a.per ? a.V - base : a.per) : 0);
-    Row r{a, slice, row, base, n, 0.0, 0.0, 0.0f};
-
-    // ---- the row into shared memory, and its largest logit
-    if (threadIdx.x == 0) {
-        s.top = -INFINITY;
-        s.best = INT64_MAX;
-        s.listed = 0;
-    }
-    clear_hist(s);
+    const float t = a.temperature ? a.temperature[row] : 1.0f;
+    const int64_t k_arg = a.top_k ? a.top_k[row] : 0;
+    const double p_arg = a.top_p ? (double)a.top_p[row] : 1.0;
+    const double mp = a.min_p ? (double)a.min_p[row] : 0.0;
+    const double u = (double)a.u[row];
     float top = -INFINITY;
     {
         const float *x = a.x + row * a.rs + base * a.es;
-        if (a.resident) {
-            const int full = n / (4 * kThreads) * (4 * kThreads);
-            for (int i = threadIdx.x; i < full; i += 4 * kThreads) {
-                float v[4];
+        int i = tid;
+        constexpr int U = 8;
+        for (; i + (U - 1) * kThreads < n; i += U * kThreads) {
+            float v[U];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = x[(i + (int64_t)j * kThreads) * a.es];
+            for (int j = 0; j < U; ++j) v[j] = x[(i + (int64_t)j * kThreads) * a.es];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float y = clean(v[j]);
-                    slice[i + j * kThreads] = y;
-                    top = fmaxf(top, y);
-                }
-            }
-            for (int i = full + threadIdx.x; i < n; i += kThreads) {
-                const float y = clean(x[i * a.es]);
-                slice[i] = y;
+            for (int j = 0; j < U; ++j) {
+                const float y = clean(v[j]);
+                if (a.resident) slice[i + j * kThreads] = y;
                 top = fmaxf(top, y);
             }
-        } else {
-            for (int i = threadIdx.x; i < n; i += kThreads) top = fmaxf(top, clean(x[i * a.es]));
+        }
+        for (; i < n; i += kThreads) {
+            const float y = clean(x[i * a.es]);
+            if (a.resident) slice[i] = y;
+            top = fmaxf(top, y);
         }
     }
+    auto warp_max = [](float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    __shared__ float warp_top[32];
-    if (lane == 0) warp_top[threadIdx.x >> 5] = top;
+        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        return v;
+    };
+    top = warp_max(top);
+    if (lane == 0) s.scan_f[0][tid >> 5] = top;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) top = fmaxf(top, warp_top[w]);
-        s.top = top;
-    }
+    top = warp_max(lane < kWarps ? s.scan_f[0][lane] : -INFINITY);
+    if (tid == 0) s.top = top;
     cl.sync();
-    top = -INFINITY;
-    for (int c = 0; c < C; ++c) top = fmaxf(top, cl.map_shared_rank(&s, c)->top);
-    r.xmax = top;
+    top = warp_max(lane < C ? cl.map_shared_rank(&s, lane)->top : -INFINITY);
     if (top == -INFINITY) {  // nothing to choose from
-        if (rank == 0 && threadIdx.x == 0) a.token[row] = -1;
+        if (rank == 0 && tid == 0) a.token[row] = -1;
         cl.sync();
         return;
     }
-    const float t = a.temperature ? a.temperature[row] : 1.0f;
-    const bool greedy = !(t > 0.0f);
-    const int64_t k_arg = a.top_k ? a.top_k[row] : 0;
     const unsigned k = k_arg > 0 && k_arg < a.V ? (unsigned)k_arg : 0;  // 0: all
-    const double p_arg = a.top_p ? (double)a.top_p[row] : 1.0;
     const bool by_p = p_arg < 1.0;
     const double p = p_arg > 0.0 ? p_arg : 0.0;
-    const double mp = a.min_p ? (double)a.min_p[row] : 0.0;
-    const double u = a.u ? (double)a.u[row] : 0.0;
+    Row r{a, slice, s.t64, s.t32, row, base, n, top, 0.0, 0.0, 0.0f, 0.0f};
 
-    if (greedy || k == 1) {
+    if (!(t > 0.0f) || k == 1) {
         // the lowest index of the largest logit
         int64_t best = INT64_MAX;
-        for (int i = threadIdx.x; i < n && best == INT64_MAX; i += kThreads)
+        for (int i = tid; i < n && best == INT64_MAX; i += kThreads)
             if (r.get(i) == top) best = base + i;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -296,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
         }
         if (lane == 0 && best != INT64_MAX) atomicMin(reinterpret_cast<long long *>(&s.best), (long long)best);
         cl.sync();
-        if (rank == 0 && threadIdx.x == 0) {
+        if (rank == 0 && tid == 0) {
             for (int c = 0; c < C; ++c) {
                 const int64_t b = cl.map_shared_rank(&s, c)->best;
                 best = b < best ? b : best;
@@ -306,178 +460,261 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
         cl.sync();
         return;
     }
-    r.inv_t = 1.0 / (double)t;
-    r.zmax = (double)top * r.inv_t;
+    r.c = 1.4426950408889634074 / (double)t;
+    r.zc = (double)top * r.c;
+    r.ch = (float)r.c;
+    r.cl = (float)(r.c - (double)r.ch);
 
-    unsigned cut_key = 0, cut_ties = 0xffffffffu;  // kept: above cut_key, and the first cut_ties equal to it
+    // kept: the tokens above cut_key, and the first cut_ties equal to it
+    constexpr unsigned kAll = 0xffffffffu;
+    unsigned cut_key = 0, cut_ties = kAll;
     if (k || by_p) {
-        // ---- histogram linear in the logit
-        const bool weigh = by_p;
-        const LinearBins bins{top, 64.0f / t};
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            const float x = r.get(i);
-            if (x == -INFINITY) continue;
-            const int b = bins(x);
-            atomicAdd(&s.count[b], 1u);
-            if (weigh) {
-                const u64 w = r.weight(x);
-                if (w) atomicAdd(&s.weight[b], w);
+        const float scale = kBinsPerUnit / t;
+        u64 all_w = 0;  // the share's total
+        r.each([&](int, float x) {
+            if (x != -INFINITY) atomicAdd(&s.count[r.bin(x, scale)], 1u);
+            if (!k) all_w += r.weight(x);
+        });
+        if (!k) {
+            all_w = block_sum(s, all_w);
+            if (tid == 0) s.cta_weight = all_w;
+        }
+        unsigned c[kPer], kept_c[kPer];  // tokens of a bin, and those of the first k
+        cluster_counts(cl, s, c);
+        if (!k) all_w = over_cluster(cl, s, &Shared::cta_weight);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) kept_c[j] = c[j];
+
+        // Two cuts at most: the k-th token, and then (unless the list of all that can be kept settles it) the
+        // share of the first k's weight.
+        for (int pass = k ? 0 : 1; pass < 2; ++pass) {
+            const bool share = pass == 1;
+            if (share && !by_p) break;
+            unsigned before, reach;  // tokens before the bins of the cut, and down to the last of them
+            if (share) {
+                find_share(s, c, kept_c, (float)((1.0 - p) * (double)all_w * (1.0 / kOne)));
+                before = s.before[0];
+                reach = s.before[1];
+            } else {
+                if (find_count(s, c, k) < k) {
+                    // fewer than k: no cut by the count
+                    if (by_p) {
+                        u64 w = 0;
+                        r.each([&](int, float x) { w += r.weight(x); });
+                        w = block_sum(s, w);
+                        if (tid == 0) s.cta_weight = w;
+                        cl.sync();
+                        all_w = over_cluster(cl, s, &Shared::cta_weight);
+                        cl.sync();
+                    }
+                    continue;
+                }
+                before = s.before[0];
+                reach = before + s.in_bin;
             }
-        }
-        // the deepest bin that can hold a kept token: of the k-th, or of the p-th share of everything
-        // (a share of the first k's weight is reached no later)
-        if (k)
-            find_bin(cl, s, false, k, -1.0, 0);
-        else
-            find_bin(cl, s, true, 0, p, 0);
-        // fewer than k tokens, or p = 0 (the first token alone): all of a row, or its first bin
-        const bool all = s.bin < 0 && k;
-        if (s.bin < 0 && !k && threadIdx.x == 0) {
-            s.bin = 0;
-            s.before_c = 0;
-            s.before_w = 0;
-            unsigned c0 = 0;
-            for (int c = 0; c < C; ++c) c0 += cl.map_shared_rank(&s, c)->count[0];
-            s.in_bin = c0;
-        }
-        cl.sync();
-        const int bin = s.bin;
-        const unsigned reach = s.before_c + s.in_bin;
-        if (!all && reach <= kList) {
-            // ---- everything that can be kept, in one list
+            const bool whole = reach <= kList;  // all that can be kept fits a list
+            const int b0 = whole ? 0 : min(s.bin[0], s.bin[1]), b1 = s.bin[1];
+            const bool listable = whole || reach - before <= kList;
             Shared *first = cl.map_shared_rank(&s, 0);
-            for (int i = threadIdx.x; i < n; i += kThreads) {
-                const float x = r.get(i);
-                if (x == -INFINITY || bins(x) > bin) continue;
-                const unsigned at = atomicAdd(&first->listed, 1u);
-                if (at < kList) {
-                    first->lx[at] = x;
-                    first->li[at] = base + i;
-                    first->lw[at] = r.weight(x);
+            // The tokens of those bins: into the list, or their least and largest key; and the weight of those above
+            // them, summed, or as all less the rest, whichever are fewer.  (After a cut by the count the tokens
+            // below it are not in the share's total.)
+            const bool sum = share && !whole, up = k || before < (unsigned)(a.V / 2);
+            u64 above = 0;
+            unsigned klo = 0xffffffffu, khi = 0;
+            r.each([&](int i, float x) {
+                const int b = r.bin(x, scale);
+                if (sum) above += (b < b0) == up ? r.weight(x) : 0;
+                if (b < b0 || b > b1 || x == -INFINITY) return;
+                const unsigned key = key_of(x);
+                klo = min(klo, key);
+                khi = max(khi, key);
+                if (listable) {
+                    const unsigned at = atomicAdd(&s.own_listed, 1u);
+                    if (at < kList) s.own[at] = (u64)key << 32 | (0xffffffffu - (unsigned)(base + i));
                 }
+            });
+            if (sum) {
+                above = block_sum(s, above);
+                if (tid == 0) s.cta_weight = above;
             }
-            cl.sync();
-            if (rank == 0) {
-                const int m = (int)(s.listed < kList ? s.listed : kList);
-                const int i = threadIdx.x;
-                const bool mine = i < m;
-                const float xi = mine ? s.lx[i] : 0.0f;
-                const int64_t ii = mine ? s.li[i] : 0;
-                const u64 wi = mine ? s.lw[i] : 0;
-                unsigned rk = 0;
-                u64 before = 0;
-                if (mine)
-                    for (int j = 0; j < m; ++j) {
-                        const float xj = s.lx[j];
-                        if (xj > xi || (xj == xi && s.li[j] < ii)) {
-                            ++rk;
-                            before += s.lw[j];
+            if (listable) {
+                __syncthreads();
+                // a CTA's tokens go to the list together: one remote addition, not one a token
+                const unsigned found = min(s.own_listed, (unsigned)kList);
+                if (tid == 0) s.own_at = found ? atomicAdd(&first->listed, found) : 0;
+                __syncthreads();
+                if (tid < found && s.own_at + tid < kList) first->list[s.own_at + tid] = s.own[tid];
+                cl.sync();
+                if (rank == 0) {
+                    if (sum) {
+                        above = over_cluster(cl, s, &Shared::cta_weight);
+                        if (!up) above = all_w - above;
+                    }
+                    const int m = (int)min(s.listed, (unsigned)kList);
+                    const bool mine = tid < m;
+                    const u64 e = block_sort(mine ? s.list[tid] : 0, s.list, m);
+                    const unsigned key = (unsigned)(e >> 32);
+                    const u64 w = mine ? r.weight(of_key(key)) : 0;
+                    unsigned cb, ca;
+                    u64 wb, wa;
+                    bool keep = mine;
+                    if (whole) {
+                        if (k) keep = keep && (unsigned)tid < k;
+                        if (by_p) {
+                            block_scan(s, 0, keep ? w : 0, &cb, &wb, &ca, &wa);
+                            keep = keep && (tid == 0 || (double)wb < p * (double)(share ? all_w : wa));
                         }
-                    }
-                bool keep = mine && (k == 0 || rk < k);
-                unsigned cb, ca;
-                u64 wb, wa;
-                if (by_p) {
-                    u64 total = s.total_w;
-                    if (k) {
-                        block_scan(s, 0, keep ? wi : 0, &cb, &wb, &ca, &wa);
-                        total = wa;
-                    }
-                    keep = keep && (rk == 0 || (double)before < p * (double)total);
-                }
-                if (mp > 0.0) keep = keep && (rk == 0 || r.ratio(xi) >= mp);
-                const u64 kw = keep ? wi : 0;
-                block_scan(s, 0, kw, &cb, &wb, &ca, &wa);
-                if (mine) s.lw[i] = kw;
-                if (threadIdx.x == 0) s.best = -1;
-                __syncthreads();
-                u64 upto = 0;  // running weight in index order, this token included
-                if (kw) {
-                    for (int j = 0; j < m; ++j)
-                        if (s.li[j] <= ii) upto += s.lw[j];
-                    const double target = u * (double)wa;
-                    // u of 1 or more (or NaN) takes the last kept token
-                    if (((double)upto > target && !((double)(upto - kw) > target)) || (upto == wa && !((double)wa > target)))
-                        a.token[row] = (int32_t)ii;
-                }
-            }
-            cl.sync();
-            return;
-        }
-        // ---- a cut within the row.  First by count, then by weight among those.
-        u64 kept_w = s.total_w;
-        for (int pass = 0; pass < 2; ++pass) {
-            const bool by_weight = pass == 1;
-            if (by_weight ? !by_p : (k == 0 || all)) continue;
-            if (by_weight && k && !all) {
-                // the weight of the first k tokens
-                u64 w = 0;
-                for (int i = threadIdx.x; i < n; i += kThreads) {
-                    const float x = r.get(i);
-                    if (x != -INFINITY && key_of(x) > cut_key) w += r.weight(x);
-                }
-                unsigned cb, ca;
-                u64 wb, wa;
-                block_scan(s, 0, w, &cb, &wb, &ca, &wa);
-                if (threadIdx.x == 0) s.cta_weight = wa;
-                cl.sync();
-                kept_w = 0;
-                for (int c = 0; c < C; ++c) kept_w += cl.map_shared_rank(&s, c)->cta_weight;
-                const unsigned kb = cut_key & 0x80000000u ? cut_key & 0x7fffffffu : ~cut_key;
-                kept_w += (u64)cut_ties * r.weight(__uint_as_float(kb));
-                cl.sync();
-            }
-            const double target = by_weight ? p * (double)kept_w : 0.0;
-            // finer and finer histograms over keys lo .. hi, the tokens above hi counted before
-            unsigned lo = key_of(-INFINITY) + 1, hi = key_of(top);
-            unsigned done_c = 0;
-            u64 done_w = 0;
-            for (;;) {
-                int shift = 0;
-                while (((hi - lo) >> shift) >= (unsigned)kBins) ++shift;
-                clear_hist(s);
-                __syncthreads();
-                for (int i = threadIdx.x; i < n; i += kThreads) {
-                    const unsigned ky = key_of(r.get(i));
-                    if (ky < lo || ky > hi) continue;
-                    const int b = (int)((hi - ky) >> shift);
-                    atomicAdd(&s.count[b], 1u);
-                    if (by_weight) {
-                        const u64 w = r.weight(r.get(i));
-                        if (w) atomicAdd(&s.weight[b], w);
-                    }
-                }
-                const u64 want_w = target > (double)done_w ? (u64)ceil(target - (double)done_w) : 0;
-                find_bin(cl, s, by_weight, k - done_c, -1.0, want_w);
-                const int b = s.bin;
-                if (b < 0) {
-                    // no weight is wanted: the first token alone (or rounding at the last): the largest key
-                    cut_key = want_w == 0 ? key_of(top) : lo;
-                    cut_ties = want_w == 0 ? 1 : 0xffffffffu;
-                    break;
-                }
-                done_c += s.before_c;
-                done_w += s.before_w;
-                const unsigned nhi = hi - ((unsigned)b << shift);
-                const unsigned width = (1u << shift) - 1;
-                const unsigned nlo = nhi - lo < width ? lo : nhi - width;
-                hi = nhi;
-                lo = nlo;
-                __syncthreads();
-                if (lo == hi) {
-                    cut_key = lo;
-                    if (by_weight) {
-                        const unsigned kb = cut_key & 0x80000000u ? cut_key & 0x7fffffffu : ~cut_key;
-                        const u64 w1 = r.weight(__uint_as_float(kb));
-                        // the fewest ties whose weight reaches the target
-                        u64 m = w1 ? (u64)ceil((target - (double)done_w) / (double)w1) : 1;
-                        if (m < 1) m = 1;
-                        cut_ties = (unsigned)(m < 0xffffffffu ? m : 0xffffffffu);
+                        if (mp > 0.0) keep = keep && r.at_least(of_key(key), w, mp);
+                        // the kept tokens by their index, lowest first
+                        const int kept = __syncthreads_count(keep);
+                        const u64 f = block_sort(keep ? e << 32 | key : 0, s.list, kept);
+                        const u64 fw = tid < kept ? r.weight(of_key((unsigned)f)) : 0;
+                        block_scan(s, 0, fw, &cb, &wb, &ca, &wa);
+                        const double target = u * (double)wa;
+                        const bool last = !((double)wa > target);  // u of 1 or more, or NaN: the last kept token
+                        if (fw && (last ? wb + fw == wa : (double)(wb + fw) > target && !((double)wb > target)))
+                            a.token[row] = (int32_t)(0xffffffffu - (unsigned)(f >> 32));
                     } else {
-                        cut_ties = k - done_c;
+                        if (share) {
+                            block_scan(s, 0, w, &cb, &wb, &ca, &wa);
+                            keep = keep && (double)(above + wb) < p * (double)all_w;
+                        } else {
+                            keep = keep && before + tid < k;
+                        }
+                        const int kept = __syncthreads_count(keep);
+                        // the last kept one and how many equal to it are kept (none: the cut is above the list)
+                        if (tid == (kept ? kept - 1 : 0)) s.cut_key = key;
+                        __syncthreads();
+                        const unsigned ties = __syncthreads_count(keep && key == s.cut_key);
+                        const unsigned equal = __syncthreads_count(mine && key == s.cut_key);
+                        if (tid == 0) s.cut_ties = ties == equal ? kAll : ties;  // (all: no need to count them)
                     }
-                    break;
                 }
+                cl.sync();
+                if (whole) return;
+                cut_key = first->cut_key;
+                cut_ties = first->cut_ties;
+            } else {
+                // too many tokens next to the cut: finer and finer histograms over the keys lo .. hi of those bins
+                klo = __reduce_min_sync(0xffffffffu, klo);
+                khi = __reduce_max_sync(0xffffffffu, khi);
+                if (lane == 0) {
+                    atomicMin(&s.klo, klo);
+                    atomicMax(&s.khi, khi);
+                }
+                cl.sync();
+                if (sum) {
+                    above = over_cluster(cl, s, &Shared::cta_weight);
+                    if (!up) above = all_w - above;
+                }
+                const double target = share ? p * (double)all_w : 0.0;
+                u64 done_w = above;
+                unsigned done_c = before;
+                unsigned lo = __reduce_min_sync(0xffffffffu, lane < C ? cl.map_shared_rank(&s, lane)->klo : 0xffffffffu);
+                unsigned hi = __reduce_max_sync(0xffffffffu, lane < C ? cl.map_shared_rank(&s, lane)->khi : 0u);
+                for (;;) {
+                    int shift = 0;
+                    while (((hi - lo) >> shift) >= (unsigned)kThreads) ++shift;
+                    cl.sync();
+                    s.count[tid] = 0;
+                    s.own[tid] = 0;
+                    __syncthreads();
+                    r.each([&](int, float x) {
+                        const unsigned ky = key_of(x);
+                        if (ky < lo || ky > hi) return;
+                        const int b = (int)((hi - ky) >> shift);
+                        atomicAdd(&s.count[b], 1u);
+                        if (share) {
+                            const u64 w = r.weight(x);
+                            if (w) atomicAdd(&s.own[b], w);
+                        }
+                    });
+                    if (tid == 0) s.bin[0] = -1;
+                    cl.sync();
+                    unsigned fc = 0;
+                    u64 fw = 0;
+#pragma unroll
+                    for (int q = 0; q < kMaxCluster; ++q)
+                        if (q < C) {
+                            const Shared *o = cl.map_shared_rank(&s, q);
+                            fc += o->count[tid];
+                            fw += o->own[tid];
+                        }
+                    unsigned cb, ca;
+                    u64 wb, wa;
+                    block_scan(s, fc, fw, &cb, &wb, &ca, &wa);
+                    const bool here = share ? fc && (double)(done_w + wb) < target && !((double)(done_w + wb + fw) < target)
+                                            : done_c + cb < k && done_c + cb + fc >= k;
+                    if (here) {
+                        s.bin[0] = tid;
+                        s.before[0] = cb;
+                        s.fine_before = wb;
+                    }
+                    __syncthreads();
+                    const int b = s.bin[0];
+                    if (b < 0) {
+                        // the cut is above these bins (or p is 0: the first token alone)
+                        cut_key = done_c ? hi : key_of(top);
+                        cut_ties = done_c ? 0 : 1;
+                        break;
+                    }
+                    done_c += s.before[0];
+                    done_w += s.fine_before;
+                    const unsigned nhi = hi - ((unsigned)b << shift);
+                    const unsigned width = (1u << shift) - 1;
+                    lo = nhi - lo < width ? lo : nhi - width;
+                    hi = nhi;
+                    if (lo == hi) {
+                        cut_key = lo;
+                        if (share) {
+                            // the fewest ties whose weight reaches the target
+                            const u64 w1 = r.weight(of_key(cut_key));
+                            const double need = w1 ? ceil((target - (double)done_w) / (double)w1) : 1.0;
+                            cut_ties = need < 1.0 ? 1u : need < 4294967295.0 ? (unsigned)need : kAll;
+                        } else {
+                            cut_ties = k - done_c;
+                        }
+                        break;
+                    }
+                }
+            }
+            cl.sync();  // the cut has been read everywhere: the list and the bounds may be used again
+            if (tid == 0) {
+                s.listed = s.own_listed = 0;
+                s.klo = 0xffffffffu;
+                s.khi = 0;
+            }
+            if (!share && by_p) {
+                // the weight of the first k, and their counts in the bins
+                const float xc = of_key(cut_key);
+                const int bc = r.bin(xc, scale);
+                u64 w = 0;
+                unsigned in = 0;  // of the cut's bin, above the cut (all the ties are kept: with them)
+                r.each([&](int, float x) {
+                    const unsigned ky = key_of(x);
+                    if (ky > cut_key || (ky == cut_key && cut_ties == kAll)) {
+                        w += r.weight(x);
+                        in += r.bin(x, scale) == bc;
+                    }
+                });
+                unsigned cb, ca;
+                u64 wb, wa;
+                block_scan(s, in, w, &cb, &wb, &ca, &wa);
+                if (tid == 0) {
+                    s.cta_weight = wa;
+                    s.cta_ties = ca;
+                }
+                cl.sync();
+                const unsigned extra = cut_ties == kAll ? 0 : cut_ties;
+                all_w = over_cluster(cl, s, &Shared::cta_weight) + (u64)extra * r.weight(xc);
+                const unsigned kept_in = over_cluster(cl, s, &Shared::cta_ties) + extra;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const int b = kPer * tid + j;
+                    kept_c[j] = b < bc ? c[j] : b == bc ? kept_in : 0;
+                }
+                cl.sync();
             }
         }
     }
@@ -485,80 +722,141 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
     // ---- the choice, in index order: each thread takes consecutive logits (an odd number of them, so
     // that the threads' reads fall in different banks)
     const int seg = ((n + kThreads - 1) / kThreads) | 1;
-    const int i0 = min(n, (int)threadIdx.x * seg), i1 = min(n, i0 + seg);
-    unsigned ties = 0;
-    for (int i = i0; i < i1; ++i) ties += key_of(r.get(i)) == cut_key;
-    unsigned ties_before, ca;
+    const int i0 = min(n, tid * seg), i1 = min(n, i0 + seg);
+    unsigned ties_before = 0, cb, ca;
     u64 wb, wa;
-    block_scan(s, ties, 0, &ties_before, &wb, &ca, &wa);
-    if (threadIdx.x == 0) s.cta_ties = ca;
-    cl.sync();
-    for (int c = 0; c < rank; ++c) ties_before += cl.map_shared_rank(&s, c)->cta_ties;
-    auto kept_weight = [&](float x, unsigned &seen) -> u64 {
+    if (cut_ties != kAll) {  // which of the tokens equal to the cut are kept depends on those before them
+        unsigned ties = 0;
+        for (int i = i0; i < i1; ++i) ties += key_of(r.get(i)) == cut_key;
+        block_scan(s, ties, 0, &ties_before, &wb, &ca, &wa);
+        if (tid == 0) s.cta_ties = ca;
+        cl.sync();
+        for (int q = 0; q < rank; ++q) ties_before += cl.map_shared_rank(&s, q)->cta_ties;
+    }
+    // its weight, 0 if it is not kept; `earlier`: tokens equal to the cut before it
+    auto kept_weight = [&](float x, unsigned earlier) -> u64 {
         const unsigned ky = key_of(x);
-        if (x == -INFINITY || ky < cut_key) return 0;
-        if (ky == cut_key && seen++ >= cut_ties) return 0;
-        const double q = r.ratio(x);
-        if (mp > 0.0 && q < mp && x != top) return 0;
-        return __double2ull_rn(q * kWeightOne);
+        const u64 w = r.weight(x);
+        const bool in = x != -INFINITY && (ky > cut_key || (ky == cut_key && earlier < cut_ties)) && (!(mp > 0.0) || r.at_least(x, w, mp));
+        return in ? w : 0;
     };
     u64 mine = 0;
     unsigned seen = ties_before;
-    for (int i = i0; i < i1; ++i) mine += kept_weight(r.get(i), seen);
-    unsigned cb;
-    block_scan(s, 0, mine, &cb, &wb, &ca, &wa);
-    if (threadIdx.x == 0) s.cta_weight = wa;
-    cl.sync();
-    u64 before = wb, all_w = 0;
-    for (int c = 0; c < C; ++c) {
-        const u64 w = cl.map_shared_rank(&s, c)->cta_weight;
-        if (c < rank) before += w;
-        all_w += w;
+#pragma unroll 4
+    for (int i = i0; i < i1; ++i) {
+        const float x = r.get(i);
+        mine += kept_weight(x, seen);
+        seen += key_of(x) == cut_key;
     }
+    block_scan(s, 0, mine, &cb, &wb, &ca, &wa);
+    if (tid == 0) s.cta_weight = wa;
+    cl.sync();
+    const u64 theirs = lane < C ? cl.map_shared_rank(&s, lane)->cta_weight : 0;
+    const u64 before = wb + warp_total(lane < rank ? theirs : 0), all_w = warp_total(theirs);
     const double target = u * (double)all_w;
     const bool last = !((double)all_w > target);  // u of 1 or more, or NaN: the last kept token
-    const bool here = last ? mine && before + mine == all_w
-                           : (double)(before + mine) > target && !((double)before > target);
-    if (mine && here) {
-        u64 run = before;
-        seen = ties_before;
-        for (int i = i0; i < i1; ++i) {
-            const u64 w = kept_weight(r.get(i), seen);
-            run += w;
-            if (w && (last ? run == all_w : (double)run > target)) {
-                a.token[row] = (int32_t)(base + i);
+    const bool here = mine && (last ? before + mine == all_w : (double)(before + mine) > target && !((double)before > target));
+    // the thread whose logits hold the token hands them to its warp, a logit a lane
+    const unsigned who = __ballot_sync(0xffffffffu, here);
+    if (who) {
+        const int from = __ffs(who) - 1;
+        u64 run = __shfl_sync(0xffffffffu, before, from);
+        seen = __shfl_sync(0xffffffffu, ties_before, from);
+        const int e0 = __shfl_sync(0xffffffffu, i0, from), e1 = __shfl_sync(0xffffffffu, i1, from);
+        for (int e = e0; e < e1; e += 32) {
+            const int i = e + lane;
+            const float x = i < e1 ? r.get(i) : -INFINITY;
+            const unsigned equal = __ballot_sync(0xffffffffu, i < e1 && key_of(x) == cut_key);
+            const u64 w = i < e1 ? kept_weight(x, seen + __popc(equal & ((1u << lane) - 1))) : 0;
+            const u64 upto = run + warp_incl(w, lane);
+            const unsigned hit = __ballot_sync(0xffffffffu, w && (last ? upto == all_w : (double)upto > target));
+            if (hit) {
+                if (lane == __ffs(hit) - 1) a.token[row] = (int32_t)(base + i);
                 break;
             }
+            run = __shfl_sync(0xffffffffu, upto, 31);
+            seen += __popc(equal);
         }
     }
     cl.sync();  // no CTA leaves while another reads its shared memory
 }
 
+// Rows side by side (a GEMV's [V][B]) to rows one after another: 64 x 16 tiles through shared memory.
+__global__ void __launch_bounds__(256) rows_kernel(const float *x, float *y, int64_t rows, int64_t V, int64_t rs, int64_t es)
+{
+    __shared__ float tile[16][65];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t v0 = (int64_t)blockIdx.x * 64, r0 = (int64_t)blockIdx.y * 16;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int e = threadIdx.x + 256 * j;
+        const int64_t r = r0 + (e & 15), v = v0 + (e >> 4);
+        if (r < rows && v < V) tile[e & 15][e >> 4] = x[r * rs + v * es];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int e = threadIdx.x + 256 * j;
+        const int64_t r = r0 + (e >> 6), v = v0 + (e & 63);
+        if (r < rows && v < V) y[r * V + v] = tile[e >> 6][e & 63];
+    }
+}
+
 }  // namespace
 
-extern "C" int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t row_stride, int64_t elem_stride,
-                         const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
-                         const float *u, int32_t *token, void *stream)
+extern "C" {
+
+size_t qg_sample_workspace(int64_t rows, int64_t V, int64_t elem_stride)
 {
-    if (rows < 0 || V < 1 || V > 0x7fffffff || rows > 0x7fffffff / kMaxCluster) return QG_ERR_SHAPE;
+    // rows that do not stand one after another are set out so first: a cluster reads its row alone, and of
+    // rows side by side it would fetch a whole sector for each logit
+    if (rows < 2 || V < 1 || elem_stride == 1 || rows > 0xfffff || V > 0x7fffffff) return 0;
+    return (size_t)rows * (size_t)V * sizeof(float);
+}
+
+int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t row_stride, int64_t elem_stride,
+              const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+              const float *u, int32_t *token, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (rows < 0 || V < 1 || V > 0x7fffffff || rows > 0xfffff) return QG_ERR_SHAPE;
     if (rows == 0) return QG_OK;
     if (!logits || !token || !u) return QG_ERR_NULL;
     const uintptr_t bits = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(temperature) |
                            reinterpret_cast<uintptr_t>(top_k) | reinterpret_cast<uintptr_t>(top_p) |
-                           reinterpret_cast<uintptr_t>(min_p) | reinterpret_cast<uintptr_t>(u) | reinterpret_cast<uintptr_t>(token);
+                           reinterpret_cast<uintptr_t>(min_p) | reinterpret_cast<uintptr_t>(u) |
+                           reinterpret_cast<uintptr_t>(token) | reinterpret_cast<uintptr_t>(workspace);
     if (bits % 4) return QG_ERR_ALIGN;
+    const size_t need = qg_sample_workspace(rows, V, elem_stride);
+    if (workspace && workspace_bytes < need) return QG_ERR_SCRATCH;
+    static std::atomic<int> optins[64];
     int dev = 0, optin = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
-        return QG_ERR_CUDA;
-    const int64_t room = (optin - (int)sizeof(Shared) - 1024) / 4;  // logits of a CTA
-    int C = 1;
-    while (C < kMaxCluster && V > (int64_t)C * 8192) C *= 2;
+    if (cudaGetDevice(&dev) != cudaSuccess) return QG_ERR_CUDA;
+    if (dev < 64) optin = optins[dev].load(std::memory_order_relaxed);
+    if (optin == 0) {
+        if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
+            cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin) != cudaSuccess ||
+            cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return QG_ERR_CUDA;
+        if (dev < 64) optins[dev].store(optin, std::memory_order_relaxed);
+    }
     SampleArgs a = {};
     a.x = logits;
-    a.V = V;
     a.rs = row_stride;
     a.es = elem_stride;
+    if (need && workspace) {
+        const int rc = launch_pdl(rows_kernel, dim3((unsigned)((V + 63) / 64), (unsigned)((rows + 15) / 16)), dim3(256), 0, stream,
+                                  logits, static_cast<float *>(workspace), rows, V, row_stride, elem_stride);
+        if (rc != QG_OK) return rc;
+        a.x = static_cast<const float *>(workspace);
+        a.rs = V;
+        a.es = 1;
+    }
+    // Eight CTAs a row; sixteen for so few rows that their clusters find room side by side; fewer for short rows.
+    const int most = rows <= 8 ? kMaxCluster : 8;
+    int C = 1;
+    while (C < most && V > (int64_t)C * 8192) C *= 2;
+    a.V = V;
     a.temperature = temperature;
     a.top_k = top_k;
     a.top_p = top_p;
@@ -566,18 +864,11 @@ extern "C" int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t r
     a.u = u;
     a.token = token;
     a.per = (V + C - 1) / C;
-    a.resident = a.per <= room;
-    const size_t smem = sizeof(Shared) + (a.resident ? (size_t)a.per * 4 : 0);
-    static std::atomic<uint64_t> raised{0};
-    if (dev >= 64 || !(raised.load() >> dev & 1)) {
-        if (cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - 1024) != cudaSuccess)
-            return QG_ERR_CUDA;
-        if (dev < 64) raised.fetch_or(uint64_t(1) << dev);
-    }
+    a.resident = a.per <= (optin - (int)sizeof(Shared)) / 4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * C));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = sizeof(Shared) + (a.resident ? (size_t)a.per * 4 : 0);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -590,3 +881,5 @@ extern "C" int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t r
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, sample_kernel, a) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
+
+}  // extern "C"

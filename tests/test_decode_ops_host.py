@@ -100,11 +100,18 @@ def test_attention_refusals(L, kw, want):
 @pytest.mark.parametrize("kw,want", [
     (dict(rows=-1), qg.QG_ERR_SHAPE), (dict(V=0), qg.QG_ERR_SHAPE), (dict(V=1 << 31), qg.QG_ERR_SHAPE),
     (dict(logits=None), qg.QG_ERR_NULL), (dict(token=None), qg.QG_ERR_NULL), (dict(u=None), qg.QG_ERR_NULL),
-    (dict(logits=A + 2), qg.QG_ERR_ALIGN), (dict(top_k=A + 1), qg.QG_ERR_ALIGN), (dict(rows=0), qg.QG_OK)])
+    (dict(logits=A + 2), qg.QG_ERR_ALIGN), (dict(top_k=A + 1), qg.QG_ERR_ALIGN), (dict(ws=A + 2), qg.QG_ERR_ALIGN),
+    (dict(es=2, ws=A, wb=799), qg.QG_ERR_SCRATCH), (dict(rows=0), qg.QG_OK)])
 def test_sample_refusals(L, kw, want):
-    a = dict(logits=A, rows=2, V=100, t=A, top_k=A, p=A, mp=A, u=A, token=A)
+    a = dict(logits=A, rows=2, V=100, es=1, t=A, top_k=A, p=A, mp=A, u=A, token=A, ws=None, wb=0)
     a.update(kw)
-    assert L.qg_sample(a["logits"], a["rows"], a["V"], a["V"], 1, a["t"], a["top_k"], a["p"], a["mp"], a["u"], a["token"], None) == want
+    assert L.qg_sample(a["logits"], a["rows"], a["V"], a["V"], a["es"], a["t"], a["top_k"], a["p"], a["mp"], a["u"], a["token"], a["ws"],
+                       a["wb"], None) == want
+
+
+def test_sample_workspace(L):
+    assert qg.qg_sample_workspace(16, 1000, 16) == 64000
+    assert qg.qg_sample_workspace(16, 1000, 1) == 0 and qg.qg_sample_workspace(1, 1000, 16) == 0
 
 
 def test_wrappers_refuse_host_tensors(L):
