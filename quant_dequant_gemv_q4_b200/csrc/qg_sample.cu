@@ -11,9 +11,9 @@
 // One thread-block cluster takes a row and keeps it in its shared memory (up to sixteen CTAs, so 248,320
 // logits are read once), and the passes over the row run on chip.  The row is never sorted:
 //   1. the largest logit;
-//   2. a histogram of counts over bins linear in z, 128 a unit, and (for top-p) the exact sum of all weights;
+//   2. a histogram of counts over bins linear in z, 64 a factor of two, and (for top-p) the exact sum of all weights;
 //   3. the bins in which the cut lies: exactly known for the k-th token; for top-p, since a bin's weights
-//      are within a factor e^(1/128) of each other, the weight below a bin is bounded on both sides by the
+//      are within a factor 2^(1/64) of each other, the weight below a bin is bounded on both sides by the
 //      counts, which leaves two or three bins.  If the tokens down to the last of these are at most kList,
 //      they are gathered in one CTA, sorted, filtered and chosen from;
 //   4. otherwise only the tokens of those bins are gathered and sorted (or, should they be too many, counted in
@@ -24,7 +24,7 @@
 // of the additions, so a call gives the same token every time.  A weight is off by about 2^-30 of itself
 // (Row::weight), in either direction, so running sums over many tokens are off by far less, and the choice is
 // that of the exact formula but for u (or a filter's border) within about 1e-9 of a border.  64-bit
-// exponentials instead (exact to 2^-45) took 113 cycles of a scheduler for 32 of them, this form a third.
+// exponentials instead (exact to 2^-45) took 113 cycles of a scheduler for 32 of them.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -41,8 +41,8 @@ constexpr int kThreads = 512;  // (with 1024 the scans and sorts, which every wa
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 4096;
 constexpr int kPer = kBins / kThreads;  // bins of a thread
-constexpr float kBinsPerUnit = 128.0f;
-constexpr float kBinStep = 0.9922179382602435f;  // e^(-1/128)
+constexpr float kBinStep = 0.98922801319397548f;  // 2^(-1/64)
+constexpr float kDeepest = 45.9f;  // below 2^-45.9 of the largest a weight is 0
 constexpr int kList = 512;
 constexpr int kMaxCluster = 16;  // (more than eight: not on every device of this kind, but on this one)
 constexpr double kOne = 17592186044416.0;  // the largest weight, 2^44
@@ -54,8 +54,7 @@ struct SampleArgs {
     const float *temperature, *top_p, *min_p, *u;
     const int32_t *top_k;
     int32_t *token;
-    int64_t per;   // logits of a CTA
-    int resident;  // the CTA's logits stand in shared memory
+    int64_t per;  // logits of a CTA
 };
 
 struct Shared {
@@ -63,8 +62,7 @@ struct Shared {
     alignas(16) unsigned total[kBins];  // of the cluster
     u64 list[kList];  // key << 32 | ~index (the cluster's, in its first CTA)
     u64 own[kList];   // the CTA's part of the list; weights of finer histograms
-    u64 t64[64];      // 2^(i / 64) in 2^-44
-    unsigned t32[64];  // and in 2^-30
+    unsigned table[64];  // 2^(i / 64) in 2^-30
     // exchanged over the cluster
     float top;
     int64_t best;
@@ -94,12 +92,16 @@ __device__ __forceinline__ float clean(float x)
     return x != x ? -INFINITY : x;  // NaN is never chosen
 }
 
-struct Row {
-    const SampleArgs &a;
+// (kept out of line: code that is seldom run costs those passes that would have to be fetched around it)
+__device__ __noinline__ bool at_least_exact(double t, double min_p) { return exp2(t) >= min_p; }
+
+// A CTA's part of a row; RESIDENT: in shared memory.
+template <bool RESIDENT> struct Row {
+    const float *x;  // in global memory otherwise
+    int64_t es;
     const float *slice;
-    const u64 *t64;
-    const unsigned *t32;
-    int64_t row, base;
+    const unsigned *table;
+    bool infinite;  // the largest logit is +inf: those count as 0, all others as -inf
     int n;
     float xmax;
     double c, zc;  // log2(e) / temperature, and the largest logit times it
@@ -107,7 +109,12 @@ struct Row {
 
     __device__ __forceinline__ float get(int i) const
     {
-        return a.resident ? slice[i] : clean(a.x[row * a.rs + (base + i) * a.es]);
+        float v;
+        if constexpr (RESIDENT)
+            v = slice[i];
+        else
+            v = clean(x[i * es]);
+        return !infinite ? v : v == INFINITY ? 0.0f : -INFINITY;
     }
     // f(i, x) for the CTA's logits, four a thread in flight
     template <typename F> __device__ __forceinline__ void each(F f) const
@@ -122,26 +129,36 @@ struct Row {
         }
         for (; i < n; i += kThreads) f(i, get(i));
     }
-    // The weight in whole 2^-44, without a branch (several are in flight).  t = (xmax - x) c is formed as a sum of
-    // two floats (the difference and the product with their rounding errors: about 2^-46 of t), and
-    // 2^-t = 2^-q 2^(j/64) e^y with t = n / 64 + r, y = -r ln 2, |r| <= 1/128: a table in 64 bits, and the Taylor
-    // series of e^y - 1 to the third power in fp32 (2^-24 of at most 0.0055; the fourth power is below 4e-11).
-    __device__ __forceinline__ u64 weight(float x) const
+    // The weight in whole 2^-44, without a branch (several are in flight), and the bin of the histogram.
+    // t = (xmax - x) c is formed as a sum of two floats (the difference and the product with their rounding
+    // errors: about 2^-46 of t).  With n = 64 t rounded, which is the bin (monotone in x), t = n / 64 + r and
+    // |r| <= 1/128: 2^-t = 2^-q 2^(j/64) e^y, y = -r ln 2; a table, and the Taylor series of e^y - 1 to the third
+    // power in fp32 (2^-24 of at most 0.0055; the fourth power is below 4e-11), multiplied in 62 bits.
+    __device__ __forceinline__ u64 weight(float x, int *bin) const
     {
         const float d = xmax - x;
         const float v = d - xmax;
         const float dl = (xmax - (d - v)) - (x + v);
         const float t0 = d * ch;
-        const float t = fminf(t0, 60.0f);  // (also takes a NaN: two infinities)
-        const float tl = fmaf(d, ch, -t0) + fmaf(d, cl, dl * ch);
+        const float t = fminf(t0, kDeepest);
+        const float tl = fmaf(d, ch, -t0) + fmaf(d, cl, dl * ch);  // (NaN at -inf: y is then of no matter)
         const float m = fmaf(t, 64.0f, 12582912.0f);  // 1.5 * 2^23: the sum's low bits are 64 t, rounded
         const int n64 = __float_as_int(m) - 0x4b400000;
         const float y = (fmaf(m - 12582912.0f, -1.0f / 64.0f, t) + tl) * -0.693147180559945f;
         const float e = y * fmaf(y, fmaf(y, 1.0f / 6.0f, 0.5f), 1.0f);
-        const int q = (n64 + 63) >> 6, j = (q << 6) - n64;
-        const long long w = (long long)t64[j] + (((long long)t32[j] * __float2int_rn(e * 274877906944.0f)) >> 24);  // 2^38
-        const u64 r = (u64)(w + ((1ll << q) >> 1)) >> q;
-        return x == xmax ? 1ull << 44 : t < 46.0f ? r : 0;
+        const int q = (n64 + 63) >> 6;
+        const unsigned factor = 0x80000000u + (unsigned)__float2int_rn(e * 2147483648.0f);
+        *bin = n64;
+        return ((u64)table[(q << 6) - n64] * factor) >> (17 + q);
+    }
+    __device__ __forceinline__ u64 weight(float x) const
+    {
+        int b;
+        return weight(x, &b);
+    }
+    __device__ __forceinline__ int bin(float x) const
+    {
+        return __float_as_int(fmaf(fminf((xmax - x) * ch, kDeepest), 64.0f, 12582912.0f)) - 0x4b400000;
     }
     // whether the weight is at least min_p (decided in 64 bits where it is close)
     __device__ __forceinline__ bool at_least(float x, u64 w, double min_p) const
@@ -149,13 +166,7 @@ struct Row {
         if (x == xmax) return true;
         const double least = min_p * kOne;
         if (fabs((double)w - least) > least * 1e-6 + 2.0) return (double)w > least;
-        return exp2(fma((double)x, c, -zc)) >= min_p;
-    }
-    // bin of the histogram: linear and monotone in x, the largest logit in bin 0
-    __device__ __forceinline__ int bin(float x, float scale) const
-    {
-        const float d = (xmax - x) * scale;
-        return x == xmax ? 0 : d < (float)(kBins - 1) ? (int)d : kBins - 1;
+        return at_least_exact(fma((double)x, c, -zc), min_p);
     }
 };
 
@@ -300,14 +311,15 @@ __device__ void find_share(Shared &s, const unsigned (&c)[kPer], const unsigned 
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b0 = kPer * threadIdx.x;
-    float edge = expf(-(float)b0 / kBinsPerUnit), h = 0.0f, l = 0.0f;
+    // a bin holds t within half a bin of b / 64; the last one that is used everything deeper
+    float edge = exp2f(-((float)b0 - 0.5f) / 64.0f), h = 0.0f, l = 0.0f;
     float hi[kPer], lo[kPer];  // weight of a bin, at most and at least
     unsigned sum = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         hi[j] = (float)kept[j] * edge * 1.0001f;
         edge *= kBinStep;
-        lo[j] = b0 + j == kBins - 1 ? 0.0f : (float)kept[j] * edge * 0.9999f;
+        lo[j] = b0 + j >= 2937 ? 0.0f : (float)kept[j] * edge * 0.9999f;
         h += hi[j];
         l += lo[j];
         sum += c[j];
@@ -361,7 +373,7 @@ __device__ void find_share(Shared &s, const unsigned (&c)[kPer], const unsigned 
     __syncthreads();
 }
 
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
+template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
 {
     extern __shared__ __align__(16) uint8_t dyn[];
     Shared &s = *reinterpret_cast<Shared *>(dyn);
@@ -372,11 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
     const int lane = threadIdx.x & 31, tid = threadIdx.x;
 
     for (int b = tid; b < kBins; b += kThreads) s.count[b] = 0;
-    if (tid < 64) {
-        const double v = exp2(tid / 64.0);
-        s.t64[tid] = __double2ull_rn(v * kOne);
-        s.t32[tid] = __double2uint_rn(v * 1073741824.0);
-    }
+    if (tid < 64) s.table[tid] = __double2uint_rn(exp2(tid / 64.0) * 1073741824.0);
     if (tid == 0) {
         s.best = INT64_MAX;
         s.listed = s.own_listed = 0;
@@ -394,9 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
     const double p_arg = a.top_p ? (double)a.top_p[row] : 1.0;
     const double mp = a.min_p ? (double)a.min_p[row] : 0.0;
     const double u = (double)a.u[row];
+    const float *x = a.x + row * a.rs + base * a.es;
     float top = -INFINITY;
     {
-        const float *x = a.x + row * a.rs + base * a.es;
         int i = tid;
         constexpr int U = 8;
         for (; i + (U - 1) * kThreads < n; i += U * kThreads) {
@@ -406,13 +414,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
 #pragma unroll
             for (int j = 0; j < U; ++j) {
                 const float y = clean(v[j]);
-                if (a.resident) slice[i + j * kThreads] = y;
+                if (RESIDENT) slice[i + j * kThreads] = y;
                 top = fmaxf(top, y);
             }
         }
         for (; i < n; i += kThreads) {
             const float y = clean(x[i * a.es]);
-            if (a.resident) slice[i] = y;
+            if (RESIDENT) slice[i] = y;
             top = fmaxf(top, y);
         }
     }
@@ -436,7 +444,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
     const unsigned k = k_arg > 0 && k_arg < a.V ? (unsigned)k_arg : 0;  // 0: all
     const bool by_p = p_arg < 1.0;
     const double p = p_arg > 0.0 ? p_arg : 0.0;
-    Row r{a, slice, s.t64, s.t32, row, base, n, top, 0.0, 0.0, 0.0f, 0.0f};
+    const bool infinite = top == INFINITY;
+    if (infinite) top = 0.0f;
+    Row<RESIDENT> r{x, a.es, slice, s.table, infinite, n, top, 0.0, 0.0, 0.0f, 0.0f};
 
     if (!(t > 0.0f) || k == 1) {
         // the lowest index of the largest logit
@@ -469,11 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
     constexpr unsigned kAll = 0xffffffffu;
     unsigned cut_key = 0, cut_ties = kAll;
     if (k || by_p) {
-        const float scale = kBinsPerUnit / t;
         u64 all_w = 0;  // the share's total
         r.each([&](int, float x) {
-            if (x != -INFINITY) atomicAdd(&s.count[r.bin(x, scale)], 1u);
-            if (!k) all_w += r.weight(x);
+            int b;
+            if (k)
+                b = r.bin(x);
+            else
+                all_w += r.weight(x, &b);
+            if (x != -INFINITY) atomicAdd(&s.count[b], 1u);
         });
         if (!k) {
             all_w = block_sum(s, all_w);
@@ -523,8 +536,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
             u64 above = 0;
             unsigned klo = 0xffffffffu, khi = 0;
             r.each([&](int i, float x) {
-                const int b = r.bin(x, scale);
-                if (sum) above += (b < b0) == up ? r.weight(x) : 0;
+                int b;
+                if (sum) {
+                    const u64 w = r.weight(x, &b);
+                    above += (b < b0) == up ? w : 0;
+                } else {
+                    b = r.bin(x);
+                }
                 if (b < b0 || b > b1 || x == -INFINITY) return;
                 const unsigned key = key_of(x);
                 klo = min(klo, key);
@@ -688,14 +706,14 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
             if (!share && by_p) {
                 // the weight of the first k, and their counts in the bins
                 const float xc = of_key(cut_key);
-                const int bc = r.bin(xc, scale);
+                const int bc = r.bin(xc);
                 u64 w = 0;
                 unsigned in = 0;  // of the cut's bin, above the cut (all the ties are kept: with them)
                 r.each([&](int, float x) {
                     const unsigned ky = key_of(x);
                     if (ky > cut_key || (ky == cut_key && cut_ties == kAll)) {
                         w += r.weight(x);
-                        in += r.bin(x, scale) == bc;
+                        in += r.bin(x) == bc;
                     }
                 });
                 unsigned cb, ca;
@@ -835,8 +853,10 @@ int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t row_stride, 
     if (dev < 64) optin = optins[dev].load(std::memory_order_relaxed);
     if (optin == 0) {
         if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-            cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin) != cudaSuccess ||
-            cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            cudaFuncSetAttribute(sample_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin) != cudaSuccess ||
+            cudaFuncSetAttribute(sample_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin) != cudaSuccess ||
+            cudaFuncSetAttribute(sample_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+            cudaFuncSetAttribute(sample_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
             return QG_ERR_CUDA;
         if (dev < 64) optins[dev].store(optin, std::memory_order_relaxed);
     }
@@ -864,11 +884,11 @@ int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t row_stride, 
     a.u = u;
     a.token = token;
     a.per = (V + C - 1) / C;
-    a.resident = a.per <= (optin - (int)sizeof(Shared)) / 4;
+    const bool resident = a.per <= (optin - (int)sizeof(Shared)) / 4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * C));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(Shared) + (a.resident ? (size_t)a.per * 4 : 0);
+    cfg.dynamicSmemBytes = sizeof(Shared) + (resident ? (size_t)a.per * 4 : 0);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -879,7 +899,7 @@ int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t row_stride, 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, sample_kernel, a) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, resident ? sample_kernel<true> : sample_kernel<false>, a) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
 
 }  // extern "C"
