@@ -37,13 +37,13 @@ namespace {
 using namespace qg;
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;  // (with 1024 the scans and sorts, which every warp runs, cost more than they saved)
+constexpr int kThreads = 1024;  // (16 x 248320: 57 us, with 512 threads 70 us)
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 4096;
 constexpr int kPer = kBins / kThreads;  // bins of a thread
 constexpr float kBinStep = 0.98922801319397548f;  // 2^(-1/64)
 constexpr float kDeepest = 45.9f;  // below 2^-45.9 of the largest a weight is 0
-constexpr int kList = 512;
+constexpr int kList = kThreads;
 constexpr int kMaxCluster = 16;  // (more than eight: not on every device of this kind, but on this one)
 constexpr double kOne = 17592186044416.0;  // the largest weight, 2^44
 typedef unsigned long long u64;
@@ -116,20 +116,13 @@ template <bool RESIDENT> struct Row {
             v = clean(x[i * es]);
         return !infinite ? v : v == INFINITY ? 0.0f : -INFINITY;
     }
-    // f(i, x) for the CTA's logits, four a thread in flight
+    // f(i, x) for the CTA's logits
     template <typename F> __device__ __forceinline__ void each(F f) const
     {
-        int i = threadIdx.x;
-        for (; i + 3 * kThreads < n; i += 4 * kThreads) {
-            float x[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = get(i + j * kThreads);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f(i + j * kThreads, x[j]);
-        }
-        for (; i < n; i += kThreads) f(i, get(i));
+#pragma unroll 1
+        for (int i = threadIdx.x; i < n; i += kThreads) f(i, get(i));
     }
-    // The weight in whole 2^-44, without a branch (several are in flight), and the bin of the histogram.
+    // The weight in whole 2^-44, without a branch, and the bin of the histogram.
     // t = (xmax - x) c is formed as a sum of two floats (the difference and the product with their rounding
     // errors: about 2^-46 of t).  With n = 64 t rounded, which is the bin (monotone in x), t = n / 64 + r and
     // |r| <= 1/128: 2^-t = 2^-q 2^(j/64) e^y, y = -r ln 2; a table, and the Taylor series of e^y - 1 to the third
@@ -172,7 +165,7 @@ template <bool RESIDENT> struct Row {
 
 template <typename T> __device__ __forceinline__ T warp_incl(T v, int lane)
 {
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const T w = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += w;
@@ -188,7 +181,7 @@ template <typename T> __device__ __forceinline__ T warp_total(T v)
 }
 
 // Sum of w over the block.
-__device__ __forceinline__ u64 block_sum(Shared &s, u64 w)
+__device__ __noinline__ u64 block_sum(Shared &s, u64 w)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     w = warp_total(w);
@@ -199,7 +192,11 @@ __device__ __forceinline__ u64 block_sum(Shared &s, u64 w)
 }
 
 // Exclusive prefix over the block's threads of (c, w), and the totals.
-__device__ __forceinline__ void block_scan(Shared &s, unsigned c, u64 w, unsigned *c_before, u64 *w_before, unsigned *c_all, u64 *w_all)
+struct Scan {
+    u64 w_before, w_all;
+    unsigned c_before, c_all;
+};
+__device__ __noinline__ Scan block_scan(Shared &s, unsigned c, u64 w)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned ci = warp_incl(c, lane);
@@ -214,10 +211,7 @@ __device__ __forceinline__ void block_scan(Shared &s, unsigned c, u64 w, unsigne
     const u64 ww = warp_incl(lane < kWarps ? s.scan_w[lane] : 0ull, lane);
     const unsigned cb = __shfl_sync(0xffffffffu, cw, warp > 0 ? warp - 1 : 0);
     const u64 wb = __shfl_sync(0xffffffffu, ww, warp > 0 ? warp - 1 : 0);
-    *c_before = ci - c + (warp ? cb : 0);
-    *w_before = wi - w + (warp ? wb : 0);
-    *c_all = __shfl_sync(0xffffffffu, cw, 31);
-    *w_all = __shfl_sync(0xffffffffu, ww, 31);
+    return {wi - w + (warp ? wb : 0), __shfl_sync(0xffffffffu, ww, 31), ci - c + (warp ? cb : 0), __shfl_sync(0xffffffffu, cw, 31)};
 }
 
 // Sum of a CTA's value over the cluster: each warp fetches the CTAs' values with one load.
@@ -229,13 +223,15 @@ template <typename T> __device__ __forceinline__ T over_cluster(cg::cluster_grou
 
 // Descending sort of one 64-bit value a thread (bitonic: exchanges within a warp by shuffles, between warps
 // through shared memory); m values, the others 0.  Warps past the power of two that holds m take no part.
-__device__ __forceinline__ u64 block_sort(u64 v, u64 *buf, int m)
+__device__ __noinline__ u64 block_sort(u64 v, u64 *buf, int m)
 {
     const int t = threadIdx.x;
     int size = 32;
     while (size < m) size <<= 1;
     if (t < size) {
+#pragma unroll 1
         for (int k = 2; k <= size; k <<= 1)
+#pragma unroll 1
             for (int j = k >> 1; j > 0; j >>= 1) {
                 u64 o;
                 if (j >= 32) {
@@ -263,14 +259,11 @@ __device__ __forceinline__ void cluster_counts(cg::cluster_group &cl, Shared &s,
     if (n > 1) {
         for (unsigned b = threadIdx.x; b < share; b += kThreads) {
             const unsigned at = cl.block_rank() * share + b;
-            unsigned v[kMaxCluster], sum = 0;
-#pragma unroll
-            for (unsigned r = 0; r < kMaxCluster; ++r) v[r] = r < n ? cl.map_shared_rank(&s, r)->count[at] : 0;
-#pragma unroll
-            for (unsigned r = 0; r < kMaxCluster; ++r) sum += v[r];
-#pragma unroll
-            for (unsigned r = 0; r < kMaxCluster; ++r)
-                if (r < n) cl.map_shared_rank(&s, r)->total[at] = sum;
+            unsigned sum = 0;
+#pragma unroll 4
+            for (unsigned r = 0; r < n; ++r) sum += cl.map_shared_rank(&s, r)->count[at];
+#pragma unroll 4
+            for (unsigned r = 0; r < n; ++r) cl.map_shared_rank(&s, r)->total[at] = sum;
         }
         cl.sync();
     }
@@ -285,11 +278,11 @@ __device__ __forceinline__ void cluster_counts(cg::cluster_group &cl, Shared &s,
 // The bin in which the k-th token lies, with the tokens before it and in it.  Returns the number of all.
 __device__ unsigned find_count(Shared &s, const unsigned (&c)[kPer], unsigned k)
 {
-    unsigned sum = 0, cb, ca;
-    u64 wb, wa;
+    unsigned sum = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) sum += c[j];
-    block_scan(s, sum, 0, &cb, &wb, &ca, &wa);
+    const Scan z = block_scan(s, sum, 0);
+    unsigned cb = z.c_before;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         if (cb < k && cb + c[j] >= k) {
@@ -300,7 +293,7 @@ __device__ unsigned find_count(Shared &s, const unsigned (&c)[kPer], unsigned k)
         cb += c[j];
     }
     __syncthreads();
-    return ca;
+    return z.c_all;
 }
 
 // The bins between which the cut of top-p lies: the first whose lower bound, and the first whose upper bound,
@@ -340,14 +333,13 @@ __device__ void find_share(Shared &s, const unsigned (&c)[kPer], const unsigned 
     }
     float after_h = __shfl_down_sync(0xffffffffu, hs, 1), after_l = __shfl_down_sync(0xffffffffu, ls, 1);
     if (lane == 31) after_h = after_l = 0.0f;
-    unsigned cb, ca;
-    u64 wb, wa;
-    block_scan(s, sum, 0, &cb, &wb, &ca, &wa);
+    const Scan z = block_scan(s, sum, 0);
+    unsigned cb = z.c_before;
     if (threadIdx.x == 0) {  // (should rounding hide a border from both of its threads: all bins)
         s.bin[0] = 0;
         s.before[0] = 0;
         s.bin[1] = kBins - 1;
-        s.before[1] = ca;
+        s.before[1] = z.c_all;
     }
     const bool later = lane > warp && lane < kWarps;
     after_h += warp_total(later ? s.scan_f[0][lane] : 0.0f);
@@ -574,29 +566,28 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                     const u64 e = block_sort(mine ? s.list[tid] : 0, s.list, m);
                     const unsigned key = (unsigned)(e >> 32);
                     const u64 w = mine ? r.weight(of_key(key)) : 0;
-                    unsigned cb, ca;
-                    u64 wb, wa;
                     bool keep = mine;
                     if (whole) {
                         if (k) keep = keep && (unsigned)tid < k;
                         if (by_p) {
-                            block_scan(s, 0, keep ? w : 0, &cb, &wb, &ca, &wa);
-                            keep = keep && (tid == 0 || (double)wb < p * (double)(share ? all_w : wa));
+                            const Scan z = block_scan(s, 0, keep ? w : 0);
+                            keep = keep && (tid == 0 || (double)z.w_before < p * (double)(share ? all_w : z.w_all));
                         }
                         if (mp > 0.0) keep = keep && r.at_least(of_key(key), w, mp);
                         // the kept tokens by their index, lowest first
                         const int kept = __syncthreads_count(keep);
                         const u64 f = block_sort(keep ? e << 32 | key : 0, s.list, kept);
                         const u64 fw = tid < kept ? r.weight(of_key((unsigned)f)) : 0;
-                        block_scan(s, 0, fw, &cb, &wb, &ca, &wa);
-                        const double target = u * (double)wa;
-                        const bool last = !((double)wa > target);  // u of 1 or more, or NaN: the last kept token
-                        if (fw && (last ? wb + fw == wa : (double)(wb + fw) > target && !((double)wb > target)))
+                        const Scan z = block_scan(s, 0, fw);
+                        const double target = u * (double)z.w_all;
+                        const u64 upto = z.w_before + fw;
+                        const bool last = !((double)z.w_all > target);  // u of 1 or more, or NaN: the last kept token
+                        if (fw && (last ? upto == z.w_all : (double)upto > target && !((double)z.w_before > target)))
                             a.token[row] = (int32_t)(0xffffffffu - (unsigned)(f >> 32));
                     } else {
                         if (share) {
-                            block_scan(s, 0, w, &cb, &wb, &ca, &wa);
-                            keep = keep && (double)(above + wb) < p * (double)all_w;
+                            const Scan z = block_scan(s, 0, w);
+                            keep = keep && (double)(above + z.w_before) < p * (double)all_w;
                         } else {
                             keep = keep && before + tid < k;
                         }
@@ -652,16 +643,15 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                     cl.sync();
                     unsigned fc = 0;
                     u64 fw = 0;
-#pragma unroll
-                    for (int q = 0; q < kMaxCluster; ++q)
-                        if (q < C) {
-                            const Shared *o = cl.map_shared_rank(&s, q);
-                            fc += o->count[tid];
-                            fw += o->own[tid];
-                        }
-                    unsigned cb, ca;
-                    u64 wb, wa;
-                    block_scan(s, fc, fw, &cb, &wb, &ca, &wa);
+#pragma unroll 4
+                    for (int q = 0; q < C; ++q) {
+                        const Shared *o = cl.map_shared_rank(&s, q);
+                        fc += o->count[tid];
+                        fw += o->own[tid];
+                    }
+                    const Scan z = block_scan(s, fc, fw);
+                    const unsigned cb = z.c_before;
+                    const u64 wb = z.w_before;
                     const bool here = share ? fc && (double)(done_w + wb) < target && !((double)(done_w + wb + fw) < target)
                                             : done_c + cb < k && done_c + cb + fc >= k;
                     if (here) {
@@ -716,12 +706,10 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                         in += r.bin(x) == bc;
                     }
                 });
-                unsigned cb, ca;
-                u64 wb, wa;
-                block_scan(s, in, w, &cb, &wb, &ca, &wa);
+                const Scan z = block_scan(s, in, w);
                 if (tid == 0) {
-                    s.cta_weight = wa;
-                    s.cta_ties = ca;
+                    s.cta_weight = z.w_all;
+                    s.cta_ties = z.c_all;
                 }
                 cl.sync();
                 const unsigned extra = cut_ties == kAll ? 0 : cut_ties;
@@ -741,13 +729,13 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
     // that the threads' reads fall in different banks)
     const int seg = ((n + kThreads - 1) / kThreads) | 1;
     const int i0 = min(n, tid * seg), i1 = min(n, i0 + seg);
-    unsigned ties_before = 0, cb, ca;
-    u64 wb, wa;
+    unsigned ties_before = 0;
     if (cut_ties != kAll) {  // which of the tokens equal to the cut are kept depends on those before them
         unsigned ties = 0;
         for (int i = i0; i < i1; ++i) ties += key_of(r.get(i)) == cut_key;
-        block_scan(s, ties, 0, &ties_before, &wb, &ca, &wa);
-        if (tid == 0) s.cta_ties = ca;
+        const Scan z = block_scan(s, ties, 0);
+        ties_before = z.c_before;
+        if (tid == 0) s.cta_ties = z.c_all;
         cl.sync();
         for (int q = 0; q < rank; ++q) ties_before += cl.map_shared_rank(&s, q)->cta_ties;
     }
@@ -760,17 +748,17 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
     };
     u64 mine = 0;
     unsigned seen = ties_before;
-#pragma unroll 4
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) {
         const float x = r.get(i);
         mine += kept_weight(x, seen);
         seen += key_of(x) == cut_key;
     }
-    block_scan(s, 0, mine, &cb, &wb, &ca, &wa);
-    if (tid == 0) s.cta_weight = wa;
+    const Scan z = block_scan(s, 0, mine);
+    if (tid == 0) s.cta_weight = z.w_all;
     cl.sync();
     const u64 theirs = lane < C ? cl.map_shared_rank(&s, lane)->cta_weight : 0;
-    const u64 before = wb + warp_total(lane < rank ? theirs : 0), all_w = warp_total(theirs);
+    const u64 before = z.w_before + warp_total(lane < rank ? theirs : 0), all_w = warp_total(theirs);
     const double target = u * (double)all_w;
     const bool last = !((double)all_w > target);  // u of 1 or more, or NaN: the last kept token
     const bool here = mine && (last ? before + mine == all_w : (double)(before + mine) > target && !((double)before > target));
