@@ -4,10 +4,13 @@
 //
 // A row is one head of one token.  A lane holds eight consecutive dimensions of it, so D / 8 lanes take a
 // row and a warp 32 * 8 / D rows: fp16 rows move in 16-byte accesses whatever D is, and the sums over a row
-// are shuffles among its lanes.  The sines and cosines of a token depend on the token alone: a block takes
-// one token, fills a table of them in shared memory once, and its warps take the token's heads, the next
-// rows' loads in flight while a row is worked on.  The kernels are bound by memory traffic for long inputs
-// and by launch and load latency for a few tokens.
+// are shuffles among its lanes.
+//
+// Norm weights and rotation together are y_i = r (x_i A_i + x_j B_i) with j the dimension's rotation partner,
+// A_i = w_i cos a, B_i = -+ w_j sin a and r the norm's factor.  A and B depend on the token alone: a block
+// takes one token, makes them once in shared memory, and its warps take the token's heads with a lane's eight
+// of each in registers, the next rows' loads in flight while a row is worked on.  The kernels are bound by
+// instructions and memory traffic for long inputs and by launch and load latency for a few tokens.
 #include <algorithm>
 
 #include "qg_kv4.cuh"
@@ -54,9 +57,9 @@ struct ReadArgs {
 
 constexpr int kV = 8;  // dimensions of a lane
 
-// The rotation partners of a lane's dimensions dim .. dim + 7 < R.  Dimension i < R is the pair (i, i + R/2)
+// The rotation partners of a lane's dimensions dim .. dim + 7.  Dimension i < R is the pair (i, i + R/2)
 // (halves) or (2j, 2j + 1) (adjacent) of angle index j.  For halves the partners are another lane's eight
-// when R/2 is a multiple of eight (`far`: lanes between), and go through shared memory otherwise.
+// when R/2 is a multiple of eight, and go through shared memory otherwise.
 template <typename T>
 __device__ __forceinline__ void rope_partners(const T (&x)[kV], T *row, int dim, int R, int pairing, T (&partner)[kV])
 {
@@ -82,32 +85,81 @@ __device__ __forceinline__ void rope_partners(const T (&x)[kV], T *row, int dim,
     }
 }
 
-__device__ __forceinline__ int rope_index(int d, int R, int pairing)
+// The tables of a token: ab[d] = (A, B) of dimension d, one for each of W weight vectors (null: ones);
+// cs(f, &c, &s) gives the angles' cosine and sine.  A thread has at most one angle, and asks for everything it
+// reads before it computes.
+template <int D, int W, typename T2, typename F> __device__ __forceinline__ void make_tables(T2 (*ab)[D], const float *const (&w)[W], const RopeArgs &r, F cs)
 {
-    return pairing == QG_ROPE_ADJACENT ? d >> 1 : (d < (R >> 1) ? d : d - (R >> 1));
-}
-
-__device__ __forceinline__ bool rope_first(int d, int R, int pairing)
-{
-    return pairing == QG_ROPE_ADJACENT ? (d & 1) == 0 : d < (R >> 1);
-}
-
-// x_i cos a - x_j sin a, x_j cos a + x_i sin a of the lane's rotated dimensions; cs: (cos, sin) by angle index.
-template <typename T, typename T2>
-__device__ __forceinline__ void rotate(T (&x)[kV], T *row, const T2 *cs, int dim, const RopeArgs &r)
-{
-    T p[kV];
-    rope_partners(x, row, dim, r.R, r.pairing, p);
-    if (dim >= r.R) return;
+    static_assert(D <= kHeadWarps * 32, "a thread a dimension");
+    const int n = threadIdx.x, half = r.R / 2;
+    if (n < half) {
+        const int i = r.pairing == QG_ROPE_ADJACENT ? 2 * n : n, j = r.pairing == QG_ROPE_ADJACENT ? 2 * n + 1 : n + half;
+        float wi[W], wj[W];
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int d = dim + i;
-        if (d < r.R) {
-            const T2 c = cs[rope_index(d, r.R, r.pairing)];
-            x[i] = rope_first(d, r.R, r.pairing) ? x[i] * c.x - p[i] * c.y : x[i] * c.x + p[i] * c.y;
+        for (int y = 0; y < W; ++y) {
+            wi[y] = w[y] ? w[y][i] : 1.0f;
+            wj[y] = w[y] ? w[y][j] : 1.0f;
+        }
+        decltype(ab[0][0].x) c, s;
+        cs(n, &c, &s);
+#pragma unroll
+        for (int y = 0; y < W; ++y) {
+            ab[y][i] = T2{wi[y] * c, -(wj[y] * s)};
+            ab[y][j] = T2{wj[y] * c, wi[y] * s};
         }
     }
+    if (n >= r.R && n < D)
+#pragma unroll
+        for (int y = 0; y < W; ++y) ab[y][n] = T2{w[y] ? w[y][n] : 1.0f, 0.0f};
 }
+
+// The rows of a token in a view, from a lane's dimensions on.  KIND: 1 fp16 in 16-byte accesses, 2 fp32 so, 0 any.
+struct RowsAt {
+    const HeadsView &v;
+    int64_t base;  // elements to this token's head 0, this lane's dimensions
+    __device__ __forceinline__ RowsAt(const HeadsView &view, int64_t t, int dim) : v(view), base(t * view.st + dim * view.sd) {}
+    // eight dimensions as they come: what is converted at once is waited for at once
+    template <int KIND> __device__ __forceinline__ void load(int head, uint4 (&raw)[2]) const
+    {
+        const int64_t at = base + head * v.sh;
+        if constexpr (KIND == 1) {
+            raw[0] = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(v.p) + at);
+        } else if constexpr (KIND == 2) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(v.p) + at);
+            raw[0] = p[0], raw[1] = p[1];
+        } else {
+            float x[kV];
+            HeadsView w = v;
+            w.p = v.type == QG_TYPE_F32 ? static_cast<void *>(static_cast<float *>(v.p) + at) : static_cast<void *>(static_cast<__half *>(v.p) + at);
+            load_dims<kV>(w, 0, 0, 0, x);
+            raw[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+            raw[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+        }
+    }
+    template <int KIND> static __device__ __forceinline__ void values(const uint4 (&raw)[2], float (&x)[kV])
+    {
+        if constexpr (KIND == 1) {
+            const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                x[2 * i] = f.x, x[2 * i + 1] = f.y;
+            }
+        } else {
+            x[0] = __uint_as_float(raw[0].x), x[1] = __uint_as_float(raw[0].y), x[2] = __uint_as_float(raw[0].z), x[3] = __uint_as_float(raw[0].w);
+            x[4] = __uint_as_float(raw[1].x), x[5] = __uint_as_float(raw[1].y), x[6] = __uint_as_float(raw[1].z), x[7] = __uint_as_float(raw[1].w);
+        }
+    }
+    __device__ __forceinline__ void store(int head, const float (&x)[kV]) const
+    {
+        const int64_t at = base + head * v.sh;
+        HeadsView w = v;
+        w.p = v.type == QG_TYPE_F32 ? static_cast<void *>(static_cast<float *>(v.p) + at) : static_cast<void *>(static_cast<__half *>(v.p) + at);
+        store_dims<kV>(w, 0, 0, 0, x);
+    }
+};
+
+inline int view_kind(const HeadsView &v) { return v.vec == 1 ? 0 : v.type == QG_TYPE_F16 ? 1 : 2; }
 
 template <int LR, typename T> __device__ __forceinline__ T row_sum(T v)
 {
@@ -119,10 +171,10 @@ template <int LR, typename T> __device__ __forceinline__ T row_sum(T v)
 // y = x * rsqrt(mean(x^2) + eps) * w, then the rotation.  The sum of squares and the products are in
 // fp32.  The angle is reduced to a fraction of a turn in 64 bits, so far positions keep their sine and
 // cosine to fp32 (the reduced fraction is off by at most 2^-25 turns).
-template <int D> __global__ void __launch_bounds__(kHeadWarps * 32) norm_rope_kernel(const NormRopeArgs a)
+template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32, 4) norm_rope_kernel(const NormRopeArgs a)
 {
     constexpr int LR = D / kV, RW = 32 / LR;  // lanes of a row, rows of a warp
-    __shared__ float2 cs[D / 2];
+    __shared__ __align__(16) float2 ab[2][D];
     __shared__ float rows[kHeadWarps][RW][D];
     const int64_t t = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -130,48 +182,66 @@ template <int D> __global__ void __launch_bounds__(kHeadWarps * 32) norm_rope_ke
     pdl_launch_dependents();
     pdl_wait();
     const int R = a.rope.R;
-    const int H = a.Hq + a.Hk;
-    const int step = gridDim.y * kHeadWarps * RW;
-    int h0 = (blockIdx.y * kHeadWarps + warp) * RW;  // the warp's rows: heads h0 .. h0 + RW - 1
-    auto load = [&](int h, float (&v)[kV]) {
-        if (h < H) load_dims<kV>(h < a.Hq ? a.q : a.k, t, h < a.Hq ? h : h - a.Hq, dim, v);
+    const bool norm = a.wq || a.wk;
+    // the warp's rows in turn: groups of RW heads, those of q first (no group holds heads of both)
+    const int gq = (a.Hq + RW - 1) / RW, groups = gq + (a.Hk + RW - 1) / RW;
+    const int step = gridDim.y * kHeadWarps;
+    int g = blockIdx.y * kHeadWarps + warp;
+    const RowsAt q(a.q, t, dim), k(a.k, t, dim), qo(a.qo, t, dim), ko(a.ko, t, dim);
+    auto load = [&](int group, uint4 (&v)[2]) {
+        const int h = (group < gq ? group : group - gq) * RW + sub;
+        if (group < gq) {
+            if (h < a.Hq) q.load<KIND>(h, v);
+        } else if (group < groups) {
+            if (h < a.Hk) k.load<KIND>(h, v);
+        }
     };
-    float x[kV] = {};
-    load(h0 + sub, x);
-    for (int i = threadIdx.x; i < (R >> 1); i += blockDim.x) {
-        double turns = (double)a.rope.pos[t] * a.rope.freq[i] * 0.15915494309189533577;  // 1 / (2 pi)
+    uint4 raw[2] = {};
+    load(g, raw);
+    auto angle = [&](int f, float *c, float *s) {
+        double turns = (double)a.rope.pos[t] * a.rope.freq[f] * 0.15915494309189533577;  // 1 / (2 pi)
         turns -= rint(turns);
-        float s, c;
-        sincospif(2.0f * (float)turns, &s, &c);
-        cs[i] = make_float2(c, s);
-    }
+        sincospif(2.0f * (float)turns, s, c);
+    };
+    const float *const weights[2] = {a.wq, a.wk};
+    make_tables<D, 2>(ab, weights, a.rope, angle);
     __syncthreads();
-    while (h0 < H) {
-        const int h = h0 + sub, hn = h0 + step;
-        const bool isq = h < a.Hq;
-        float xn[kV] = {};
-        load(hn + sub, xn);
-        const float *w = isq ? a.wq : a.wk;
-        if (a.wq || a.wk) {
+    float A[kV], B[kV];
+    int which = -1;
+    for (; g < groups; g += step) {
+        float x[kV];
+        RowsAt::values<KIND>(raw, x);
+        load(g + step, raw);
+        const bool isq = g < gq;
+        if (which != (isq ? 0 : 1)) {
+            which = isq ? 0 : 1;
+#pragma unroll
+            for (int i = 0; i < kV; i += 2) {
+                const float4 v = *reinterpret_cast<const float4 *>(&ab[which][dim + i]);
+                A[i] = v.x, B[i] = v.y, A[i + 1] = v.z, B[i + 1] = v.w;
+            }
+        }
+        float r = 1.0f, p[kV];
+        if (R) rope_partners(x, rows[warp][sub], dim, R, a.rope.pairing, p);
+        if (norm) {
             float ss = 0.0f;
 #pragma unroll
             for (int i = 0; i < kV; ++i) ss = fmaf(x[i], x[i], ss);
             ss = row_sum<LR>(ss);
-            if (w) {
-                const float r = 1.0f / sqrtf(ss * (1.0f / D) + (float)a.eps);
-#pragma unroll
-                for (int i = 0; i < kV; ++i) x[i] = x[i] * r * __ldg(w + dim + i);
-            }
+            if (isq ? a.wq != nullptr : a.wk != nullptr) r = 1.0f / sqrtf(ss * (1.0f / D) + (float)a.eps);
         }
-        if (R) rotate(x, rows[warp][sub], cs, dim, a.rope);
-        if (h < H) store_dims<kV>(isq ? a.qo : a.ko, t, isq ? h : h - a.Hq, dim, x);
 #pragma unroll
-        for (int i = 0; i < kV; ++i) x[i] = xn[i];
-        h0 = hn;
+        for (int i = 0; i < kV; ++i) x[i] = r * (R ? fmaf(p[i], B[i], x[i] * A[i]) : x[i] * A[i]);
+        const int h = (isq ? g : g - gq) * RW + sub;
+        if (isq) {
+            if (h < a.Hq) qo.store(h, x);
+        } else if (h < a.Hk) {
+            ko.store(h, x);
+        }
     }
 }
 
-// Appending: rows 0 .. H-1 of a token are its keys, H .. 2H-1 its values.
+// Appending.
 //
 // A code is the nearest of sixteen levels, and a value next to the border of two would go to one or the
 // other by the rounding of the sums before it.  So that the stored bytes are those of the formula, the norm,
@@ -179,12 +249,12 @@ template <int D> __global__ void __launch_bounds__(kHeadWarps * 32) norm_rope_ke
 // own error of a border, where it is formed again in 64 bits (for about one value in ten thousand).  d and m
 // are rounded to fp16 first and the codes are found against the rounded pair, which is what a reader
 // multiplies by.
-template <int D> __global__ void __launch_bounds__(kHeadWarps * 32) kv4_append_kernel(const AppendArgs a)
+template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32) kv4_append_kernel(const AppendArgs a)
 {
     constexpr int LR = D / kV, RW = 32 / LR;
     constexpr int LG = kKvGroup / kV;  // lanes of a group of 64
     using F = Kv4<D>;
-    __shared__ double2 cs[D / 2];
+    __shared__ __align__(16) double2 ab[1][D];
     __shared__ double rows[kHeadWarps][RW][D];
     const int64_t t = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -194,51 +264,57 @@ template <int D> __global__ void __launch_bounds__(kHeadWarps * 32) kv4_append_k
     const int64_t slot = a.slot[t];
     if (slot < 0 || slot >= a.slots) return;  // not to be written
     const int R = a.rope.R;
-    const int step = gridDim.y * kHeadWarps * RW;
-    int h0 = (blockIdx.y * kHeadWarps + warp) * RW;
-    auto load = [&](int h, float (&v)[kV]) {
-        if (h < 2 * a.H) load_dims<kV>(h < a.H ? a.k : a.v, t, h < a.H ? h : h - a.H, dim, v);
+    const bool changed = a.wk || R;  // keys are stored as something other than they come
+    // groups of RW heads: those of k first
+    const int gk = (a.H + RW - 1) / RW;
+    const int step = gridDim.y * kHeadWarps;
+    int g = blockIdx.y * kHeadWarps + warp;
+    const RowsAt k(a.k, t, dim), v(a.v, t, dim);
+    auto load = [&](int group, uint4 (&x)[2]) {
+        const int h = (group < gk ? group : group - gk) * RW + sub;
+        if (h >= a.H || group >= 2 * gk) return;
+        if (group < gk)
+            k.load<KIND>(h, x);
+        else
+            v.load<KIND>(h, x);
     };
-    float xf[kV] = {};
-    load(h0 + sub, xf);
-    for (int i = threadIdx.x; i < (R >> 1); i += blockDim.x) {
-        double s, c;
-        sincos((double)a.rope.pos[t] * a.rope.freq[i], &s, &c);
-        cs[i] = make_double2(c, s);
+    uint4 raw[2] = {};
+    load(g, raw);
+    if (changed) {
+        const float *const weights[1] = {a.wk};
+        make_tables<D, 1>(ab, weights, a.rope, [&](int f, double *c, double *s) { sincos((double)a.rope.pos[t] * a.rope.freq[f], s, c); });
+        __syncthreads();
     }
-    __syncthreads();
     const int64_t pg = slot / a.page;
     const int in_page = (int)(slot - pg * a.page);
     const int blk = in_page / kKvBlock, tok = in_page % kKvBlock;
-    while (h0 < 2 * a.H) {
-        const int h = h0 + sub, hn = h0 + step;
-        const bool isk = h < a.H;
-        float xn[kV] = {};
-        load(hn + sub, xn);
-        double lo, hi;
-        double x[kV];
-        const bool exact = (a.wk != nullptr || R) && h0 < a.H;  // some row of the warp is a key that is changed
+    for (; g < 2 * gk; g += step) {
+        float xf[kV];
+        RowsAt::values<KIND>(raw, xf);
+        load(g + step, raw);
+        const bool isk = g < gk, exact = changed && isk;
+        double x[kV], lo, hi;
         if (exact) {
+            double r = 1.0, p[kV];
 #pragma unroll
             for (int i = 0; i < kV; ++i) x[i] = xf[i];
+            if (R) {
+                // partners are exchanged as they came, in fp32
+                float pf[kV];
+                rope_partners(xf, reinterpret_cast<float *>(rows[warp][sub]), dim, R, a.rope.pairing, pf);
+#pragma unroll
+                for (int i = 0; i < kV; ++i) p[i] = pf[i];
+            }
             if (a.wk) {
                 double ss = 0.0;
 #pragma unroll
                 for (int i = 0; i < kV; ++i) ss = fma(x[i], x[i], ss);
-                ss = row_sum<LR>(ss);
-                if (isk) {
-                    const double r = 1.0 / sqrt(ss * (1.0 / D) + a.eps);
-#pragma unroll
-                    for (int i = 0; i < kV; ++i) x[i] = x[i] * r * (double)__ldg(a.wk + dim + i);
-                }
+                r = 1.0 / sqrt(row_sum<LR>(ss) * (1.0 / D) + a.eps);
             }
-            if (R) {
-                double y[kV];
 #pragma unroll
-                for (int i = 0; i < kV; ++i) y[i] = x[i];
-                rotate(y, rows[warp][sub], cs, dim, a.rope);
-#pragma unroll
-                for (int i = 0; i < kV; ++i) x[i] = isk ? y[i] : x[i];
+            for (int i = 0; i < kV; ++i) {
+                const double2 c = ab[0][dim + i];
+                x[i] = r * (R ? fma(p[i], c.y, x[i] * c.x) : x[i] * c.x);
             }
             lo = x[0], hi = x[0];
 #pragma unroll
@@ -273,30 +349,30 @@ template <int D> __global__ void __launch_bounds__(kHeadWarps * 32) kv4_append_k
         const __half mh = __float2half_rn(fminf(fmaxf((float)lo, -65504.0f), 65504.0f));
         const float d = __half2float(dh), m = __half2float(mh);
         const float rd = d > 0.0f ? 1.0f / d : 0.0f;
-        uint32_t codes = 0;
+        uint32_t codes = 0, close = 0;
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
             // off by at most 2^-23 of the quotient and 2^-24 (|x| + |m|) / d, twice that with x rounded to fp32
-            const float y = (xf[i] - m) * rd;
-            const float c = fminf(fmaxf(rintf(y), 0.0f), 15.0f);  // (also takes a NaN to 0)
-            uint32_t code = (uint32_t)(int)c;
+            const float y = (xf[i] - m) * rd, n = rintf(y);
+            codes |= (uint32_t)(int)fminf(fmaxf(n, 0.0f), 15.0f) << (4 * i);  // (also takes a NaN to 0)
             const float margin = fmaf(fabsf(xf[i]) + fabsf(m), 3e-7f * rd, 1e-5f);
-            if (d > 0.0f && 0.5f - fabsf(y - rintf(y)) < margin) {
-                const double z = ((exact ? x[i] : (double)xf[i]) - (double)m) / (double)d;
-                code = (uint32_t)__double2int_rn(fmin(fmax(z, 0.0), 15.0));
-            }
-            codes |= code << (4 * i);
+            if (0.5f - fabsf(y - n) < margin) close |= 1u << i;
         }
-        if (h < 2 * a.H) {
-            const int head = isk ? h : h - a.H;
+        if (close && d > 0.0f) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+                if (close >> i & 1) {
+                    const double z = ((exact ? x[i] : (double)xf[i]) - (double)m) / (double)d;
+                    codes = (codes & ~(15u << (4 * i))) | (uint32_t)__double2int_rn(fmin(fmax(z, 0.0), 15.0)) << (4 * i);
+                }
+        }
+        const int head = (isk ? g : g - gk) * RW + sub;
+        if (head < a.H) {
             uint8_t *part = a.cache + ((pg * a.H + head) * (a.page / kKvBlock) + blk) * F::kBlock + (isk ? 0 : F::kPart);
             *reinterpret_cast<uint32_t *>(part + kv4_code_offset<D>(tok, dim)) = codes;
             if (lane % LG == 0)
                 *reinterpret_cast<__half2 *>(part + F::kCodes + (tok * F::kGroups + dim / kKvGroup) * 4) = __halves2half2(dh, mh);
         }
-#pragma unroll
-        for (int i = 0; i < kV; ++i) xf[i] = xn[i];
-        h0 = hn;
     }
 }
 
@@ -357,6 +433,23 @@ int head_blocks(int64_t T, int rows, int D, int sms)
     return (int)std::min<int64_t>(most, std::max<int64_t>(1, want));
 }
 
+template <int D> int launch_norm_rope(int kind, dim3 grid, dim3 block, void *stream, const NormRopeArgs &a)
+{
+    switch (kind) {
+    case 1: return launch_pdl(norm_rope_kernel<D, 1>, grid, block, 0, stream, a);
+    case 2: return launch_pdl(norm_rope_kernel<D, 2>, grid, block, 0, stream, a);
+    default: return launch_pdl(norm_rope_kernel<D, 0>, grid, block, 0, stream, a);
+    }
+}
+template <int D> int launch_append(int kind, dim3 grid, dim3 block, void *stream, const AppendArgs &a)
+{
+    switch (kind) {
+    case 1: return launch_pdl(kv4_append_kernel<D, 1>, grid, block, 0, stream, a);
+    case 2: return launch_pdl(kv4_append_kernel<D, 2>, grid, block, 0, stream, a);
+    default: return launch_pdl(kv4_append_kernel<D, 0>, grid, block, 0, stream, a);
+    }
+}
+
 constexpr int64_t kMostTokens = 0x7fffffff;  // grid limit
 
 int check_cache(const void *cache, int64_t pages, int page, int H, int D)
@@ -406,11 +499,12 @@ int qg_qk_norm_rope(const qg_heads *q, const qg_heads *k, int64_t T, int Hq, int
     a.Hk = Hk;
     int sms = 0;
     if ((rc = current_sms(&sms)) != QG_OK) return rc;
-    const dim3 grid((unsigned)T, head_blocks(T, Hq + Hk, D, sms)), block(kHeadWarps * 32);
+    const dim3 grid((unsigned)T, head_blocks(T, Hq + Hk + 32 * kV / D - 1, D, sms)), block(kHeadWarps * 32);
+    const int kq = Hq ? view_kind(a.q) : view_kind(a.k), kk = Hk ? view_kind(a.k) : kq;
     switch (D) {
-    case 64: return launch_pdl(norm_rope_kernel<64>, grid, block, 0, stream, a);
-    case 128: return launch_pdl(norm_rope_kernel<128>, grid, block, 0, stream, a);
-    default: return launch_pdl(norm_rope_kernel<256>, grid, block, 0, stream, a);
+    case 64: return launch_norm_rope<64>(kq == kk ? kq : 0, grid, block, stream, a);
+    case 128: return launch_norm_rope<128>(kq == kk ? kq : 0, grid, block, stream, a);
+    default: return launch_norm_rope<256>(kq == kk ? kq : 0, grid, block, stream, a);
     }
 }
 
@@ -438,11 +532,12 @@ int qg_kv4_append(const qg_heads *k, const qg_heads *v, int64_t T, int H, int D,
     a.H = H;
     int sms = 0;
     if ((rc = current_sms(&sms)) != QG_OK) return rc;
-    const dim3 grid((unsigned)T, head_blocks(T, 2 * H, D, sms)), block(kHeadWarps * 32);
+    const dim3 grid((unsigned)T, head_blocks(T, 2 * (H + 32 * kV / D - 1), D, sms)), block(kHeadWarps * 32);
+    const int kind = view_kind(a.k) == view_kind(a.v) ? view_kind(a.k) : 0;
     switch (D) {
-    case 64: return launch_pdl(kv4_append_kernel<64>, grid, block, 0, stream, a);
-    case 128: return launch_pdl(kv4_append_kernel<128>, grid, block, 0, stream, a);
-    default: return launch_pdl(kv4_append_kernel<256>, grid, block, 0, stream, a);
+    case 64: return launch_append<64>(kind, grid, block, stream, a);
+    case 128: return launch_append<128>(kind, grid, block, stream, a);
+    default: return launch_append<256>(kind, grid, block, stream, a);
     }
 }
 
