@@ -8,8 +8,9 @@
 //
 // Norm weights and rotation together are y_i = r (x_i A_i + x_j B_i) with j the dimension's rotation partner,
 // A_i = w_i cos a, B_i = -+ w_j sin a and r the norm's factor.  A and B depend on the token alone: a block
-// takes one token, makes them once in shared memory, and its warps take the token's heads with a lane's eight
-// of each in registers, the next rows' loads in flight while a row is worked on.  The kernels are bound by
+// makes them once in shared memory, and its warps take the token's heads with a lane's eight of each in
+// registers, the next rows' loads in flight while a row is worked on.  With many tokens a block takes
+// four: their tables are made side by side, and what a block waits for before its first row is shared.  The kernels are bound by
 // instructions and memory traffic for long inputs and by launch and load latency for a few tokens.
 #include <algorithm>
 
@@ -20,6 +21,7 @@ namespace {
 using namespace qg;
 
 constexpr int kHeadWarps = 8;
+constexpr int kMostTogether = 4;  // tokens of a block
 
 struct RopeArgs {
     const int32_t *pos;
@@ -33,7 +35,8 @@ struct NormRopeArgs {
     const float *wq, *wk;
     double eps;
     RopeArgs rope;
-    int Hq, Hk;
+    int64_t T;
+    int Hq, Hk, together;  // together: tokens of a block
 };
 
 struct AppendArgs {
@@ -44,7 +47,8 @@ struct AppendArgs {
     const int64_t *slot;
     uint8_t *cache;
     int64_t slots;  // pages * page
-    int page, H;
+    int64_t T;
+    int page, H, together;
 };
 
 struct ReadArgs {
@@ -85,43 +89,47 @@ __device__ __forceinline__ void rope_partners(const T (&x)[kV], T *row, int dim,
     }
 }
 
-// The tables of a token: ab[d] = (A, B) of dimension d, one for each of W weight vectors (null: ones);
-// cs(f, &c, &s) gives the angles' cosine and sine.  A thread has at most one angle, and asks for everything it
-// reads before it computes.
-template <int D, int W, typename T2, typename F> __device__ __forceinline__ void make_tables(T2 (*ab)[D], const float *const (&w)[W], const RopeArgs &r, F cs)
+// The tables of a block's tokens t0 .. t0 + n - 1: ab[j][y][d] = (A, B) of dimension d of token t0 + j, one for
+// each of W weight vectors (null: ones); cs(angle, &c, &s) gives cosine and sine.
+template <int D, int W, typename T2, typename F>
+__device__ __forceinline__ void make_tables(T2 (*ab)[W][D], const float *const (&w)[W], const RopeArgs &r, int64_t t0, int n, F cs)
 {
-    static_assert(D <= kHeadWarps * 32, "a thread a dimension");
-    const int n = threadIdx.x, half = r.R / 2;
-    if (n < half) {
-        const int i = r.pairing == QG_ROPE_ADJACENT ? 2 * n : n, j = r.pairing == QG_ROPE_ADJACENT ? 2 * n + 1 : n + half;
+    const int half = r.R / 2;
+    for (int x = threadIdx.x; x < n * half; x += kHeadWarps * 32) {
+        const int tok = x / half, f = x - tok * half;
+        const int i = r.pairing == QG_ROPE_ADJACENT ? 2 * f : f, j = r.pairing == QG_ROPE_ADJACENT ? 2 * f + 1 : f + half;
+        const double angle = (double)r.pos[t0 + tok] * r.freq[f];
         float wi[W], wj[W];
 #pragma unroll
         for (int y = 0; y < W; ++y) {
             wi[y] = w[y] ? w[y][i] : 1.0f;
             wj[y] = w[y] ? w[y][j] : 1.0f;
         }
-        decltype(ab[0][0].x) c, s;
-        cs(n, &c, &s);
+        decltype(ab[0][0][0].x) c, s;
+        cs(angle, &c, &s);
 #pragma unroll
         for (int y = 0; y < W; ++y) {
-            ab[y][i] = T2{wi[y] * c, -(wj[y] * s)};
-            ab[y][j] = T2{wj[y] * c, wi[y] * s};
+            ab[tok][y][i] = T2{wi[y] * c, -(wj[y] * s)};
+            ab[tok][y][j] = T2{wj[y] * c, wi[y] * s};
         }
     }
-    if (n >= r.R && n < D)
+    const int rest = D - r.R;
+    for (int x = threadIdx.x; x < n * rest; x += kHeadWarps * 32) {
+        const int tok = x / rest, d = r.R + x - tok * rest;
 #pragma unroll
-        for (int y = 0; y < W; ++y) ab[y][n] = T2{w[y] ? w[y][n] : 1.0f, 0.0f};
+        for (int y = 0; y < W; ++y) ab[tok][y][d] = T2{w[y] ? w[y][d] : 1.0f, 0.0f};
+    }
 }
 
 // The rows of a token in a view, from a lane's dimensions on.  KIND: 1 fp16 in 16-byte accesses, 2 fp32 so, 0 any.
 struct RowsAt {
     const HeadsView &v;
-    int64_t base;  // elements to this token's head 0, this lane's dimensions
-    __device__ __forceinline__ RowsAt(const HeadsView &view, int64_t t, int dim) : v(view), base(t * view.st + dim * view.sd) {}
+    int64_t base;  // elements to the block's first token, head 0, this lane's dimensions
+    __device__ __forceinline__ RowsAt(const HeadsView &view, int64_t t0, int dim) : v(view), base(t0 * view.st + dim * view.sd) {}
     // eight dimensions as they come: what is converted at once is waited for at once
-    template <int KIND> __device__ __forceinline__ void load(int head, uint4 (&raw)[2]) const
+    template <int KIND> __device__ __forceinline__ void load(int tok, int head, uint4 (&raw)[2]) const
     {
-        const int64_t at = base + head * v.sh;
+        const int64_t at = base + tok * v.st + head * v.sh;
         if constexpr (KIND == 1) {
             raw[0] = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(v.p) + at);
         } else if constexpr (KIND == 2) {
@@ -150,9 +158,9 @@ struct RowsAt {
             x[4] = __uint_as_float(raw[1].x), x[5] = __uint_as_float(raw[1].y), x[6] = __uint_as_float(raw[1].z), x[7] = __uint_as_float(raw[1].w);
         }
     }
-    __device__ __forceinline__ void store(int head, const float (&x)[kV]) const
+    __device__ __forceinline__ void store(int tok, int head, const float (&x)[kV]) const
     {
-        const int64_t at = base + head * v.sh;
+        const int64_t at = base + tok * v.st + head * v.sh;
         HeadsView w = v;
         w.p = v.type == QG_TYPE_F32 ? static_cast<void *>(static_cast<float *>(v.p) + at) : static_cast<void *>(static_cast<__half *>(v.p) + at);
         store_dims<kV>(w, 0, 0, 0, x);
@@ -174,50 +182,60 @@ template <int LR, typename T> __device__ __forceinline__ T row_sum(T v)
 template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32, 4) norm_rope_kernel(const NormRopeArgs a)
 {
     constexpr int LR = D / kV, RW = 32 / LR;  // lanes of a row, rows of a warp
-    __shared__ __align__(16) float2 ab[2][D];
+    __shared__ __align__(16) float2 ab[kMostTogether][2][D];
     __shared__ float rows[kHeadWarps][RW][D];
-    const int64_t t = blockIdx.x;
+    const int64_t t0 = (int64_t)blockIdx.x * a.together;
+    const int n = (int)(a.T - t0 < a.together ? a.T - t0 : a.together);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int dim = kV * (lane % LR), sub = lane / LR;
     pdl_launch_dependents();
     pdl_wait();
     const int R = a.rope.R;
     const bool norm = a.wq || a.wk;
-    // the warp's rows in turn: groups of RW heads, those of q first (no group holds heads of both)
+    // a token's rows in groups of RW heads, those of q first (no group holds heads of both)
     const int gq = (a.Hq + RW - 1) / RW, groups = gq + (a.Hk + RW - 1) / RW;
     const int step = gridDim.y * kHeadWarps;
-    int g = blockIdx.y * kHeadWarps + warp;
-    const RowsAt q(a.q, t, dim), k(a.k, t, dim), qo(a.qo, t, dim), ko(a.ko, t, dim);
-    auto load = [&](int group, uint4 (&v)[2]) {
-        const int h = (group < gq ? group : group - gq) * RW + sub;
-        if (group < gq) {
-            if (h < a.Hq) q.load<KIND>(h, v);
-        } else if (group < groups) {
-            if (h < a.Hk) k.load<KIND>(h, v);
+    const RowsAt q(a.q, t0, dim), k(a.k, t0, dim), qo(a.qo, t0, dim), ko(a.ko, t0, dim);
+    int g = blockIdx.y * kHeadWarps + warp, tok = 0;  // the group, and the token it is of
+    while (g >= groups) {
+        g -= groups;
+        ++tok;
+    }
+    auto load = [&](int tok, int g, uint4 (&v)[2]) {
+        const int h = (g < gq ? g : g - gq) * RW + sub;
+        if (tok >= n) return;
+        if (g < gq) {
+            if (h < a.Hq) q.load<KIND>(tok, h, v);
+        } else if (h < a.Hk) {
+            k.load<KIND>(tok, h, v);
         }
     };
     uint4 raw[2] = {};
-    load(g, raw);
-    auto angle = [&](int f, float *c, float *s) {
-        double turns = (double)a.rope.pos[t] * a.rope.freq[f] * 0.15915494309189533577;  // 1 / (2 pi)
+    load(tok, g, raw);
+    const float *const weights[2] = {a.wq, a.wk};
+    make_tables<D, 2>(ab, weights, a.rope, t0, n, [](double angle, float *c, float *s) {
+        double turns = angle * 0.15915494309189533577;  // 1 / (2 pi)
         turns -= rint(turns);
         sincospif(2.0f * (float)turns, s, c);
-    };
-    const float *const weights[2] = {a.wq, a.wk};
-    make_tables<D, 2>(ab, weights, a.rope, angle);
+    });
     __syncthreads();
     float A[kV], B[kV];
     int which = -1;
-    for (; g < groups; g += step) {
+    while (tok < n) {
         float x[kV];
         RowsAt::values<KIND>(raw, x);
-        load(g + step, raw);
+        int gn = g + step, tn = tok;
+        while (gn >= groups) {
+            gn -= groups;
+            ++tn;
+        }
+        load(tn, gn, raw);
         const bool isq = g < gq;
-        if (which != (isq ? 0 : 1)) {
-            which = isq ? 0 : 1;
+        if (which != 2 * tok + !isq) {
+            which = 2 * tok + !isq;
 #pragma unroll
             for (int i = 0; i < kV; i += 2) {
-                const float4 v = *reinterpret_cast<const float4 *>(&ab[which][dim + i]);
+                const float4 v = *reinterpret_cast<const float4 *>(&ab[tok][!isq][dim + i]);
                 A[i] = v.x, B[i] = v.y, A[i + 1] = v.z, B[i + 1] = v.w;
             }
         }
@@ -228,16 +246,18 @@ template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32, 4)
 #pragma unroll
             for (int i = 0; i < kV; ++i) ss = fmaf(x[i], x[i], ss);
             ss = row_sum<LR>(ss);
-            if (isq ? a.wq != nullptr : a.wk != nullptr) r = 1.0f / sqrtf(ss * (1.0f / D) + (float)a.eps);
+            if (isq ? a.wq != nullptr : a.wk != nullptr) r = rsqrtf(ss * (1.0f / D) + (float)a.eps);  // (2 ulp)
         }
 #pragma unroll
         for (int i = 0; i < kV; ++i) x[i] = r * (R ? fmaf(p[i], B[i], x[i] * A[i]) : x[i] * A[i]);
         const int h = (isq ? g : g - gq) * RW + sub;
         if (isq) {
-            if (h < a.Hq) qo.store(h, x);
+            if (h < a.Hq) qo.store(tok, h, x);
         } else if (h < a.Hk) {
-            ko.store(h, x);
+            ko.store(tok, h, x);
         }
+        g = gn;
+        tok = tn;
     }
 }
 
@@ -254,45 +274,56 @@ template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32) kv
     constexpr int LR = D / kV, RW = 32 / LR;
     constexpr int LG = kKvGroup / kV;  // lanes of a group of 64
     using F = Kv4<D>;
-    __shared__ __align__(16) double2 ab[1][D];
-    __shared__ double rows[kHeadWarps][RW][D];
-    const int64_t t = blockIdx.x;
+    __shared__ __align__(16) double2 ab[kMostTogether][1][D];
+    __shared__ float rows[kHeadWarps][RW][D];
+    const int64_t t0 = (int64_t)blockIdx.x * a.together;
+    const int n = (int)(a.T - t0 < a.together ? a.T - t0 : a.together);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int dim = kV * (lane % LR), sub = lane / LR;
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t slot = a.slot[t];
-    if (slot < 0 || slot >= a.slots) return;  // not to be written
     const int R = a.rope.R;
     const bool changed = a.wk || R;  // keys are stored as something other than they come
-    // groups of RW heads: those of k first
-    const int gk = (a.H + RW - 1) / RW;
+    // a token's rows in groups of RW heads: those of k first
+    const int gk = (a.H + RW - 1) / RW, groups = 2 * gk;
     const int step = gridDim.y * kHeadWarps;
-    int g = blockIdx.y * kHeadWarps + warp;
-    const RowsAt k(a.k, t, dim), v(a.v, t, dim);
-    auto load = [&](int group, uint4 (&x)[2]) {
-        const int h = (group < gk ? group : group - gk) * RW + sub;
-        if (h >= a.H || group >= 2 * gk) return;
-        if (group < gk)
-            k.load<KIND>(h, x);
+    const RowsAt k(a.k, t0, dim), v(a.v, t0, dim);
+    int g = blockIdx.y * kHeadWarps + warp, tok = 0;
+    while (g >= groups) {
+        g -= groups;
+        ++tok;
+    }
+    auto load = [&](int tok, int g, uint4 (&x)[2], int64_t &slot) {
+        const int h = (g < gk ? g : g - gk) * RW + sub;
+        if (tok >= n) return;
+        slot = a.slot[t0 + tok];
+        if (h >= a.H) return;
+        if (g < gk)
+            k.load<KIND>(tok, h, x);
         else
-            v.load<KIND>(h, x);
+            v.load<KIND>(tok, h, x);
     };
     uint4 raw[2] = {};
-    load(g, raw);
+    int64_t next_slot = -1;
+    load(tok, g, raw, next_slot);
     if (changed) {
         const float *const weights[1] = {a.wk};
-        make_tables<D, 1>(ab, weights, a.rope, [&](int f, double *c, double *s) { sincos((double)a.rope.pos[t] * a.rope.freq[f], s, c); });
+        make_tables<D, 1>(ab, weights, a.rope, t0, n, [](double angle, double *c, double *s) { sincos(angle, s, c); });
         __syncthreads();
     }
-    const int64_t pg = slot / a.page;
-    const int in_page = (int)(slot - pg * a.page);
-    const int blk = in_page / kKvBlock, tok = in_page % kKvBlock;
-    for (; g < 2 * gk; g += step) {
+    while (tok < n) {
         float xf[kV];
         RowsAt::values<KIND>(raw, xf);
-        load(g + step, raw);
-        const bool isk = g < gk, exact = changed && isk;
+        const int64_t slot = next_slot;
+        const int gt = g, tt = tok;
+        g += step;
+        while (g >= groups) {
+            g -= groups;
+            ++tok;
+        }
+        load(tok, g, raw, next_slot);
+        if (slot < 0 || slot >= a.slots) continue;  // not to be written
+        const bool isk = gt < gk, exact = changed && isk;
         double x[kV], lo, hi;
         if (exact) {
             double r = 1.0, p[kV];
@@ -301,7 +332,7 @@ template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32) kv
             if (R) {
                 // partners are exchanged as they came, in fp32
                 float pf[kV];
-                rope_partners(xf, reinterpret_cast<float *>(rows[warp][sub]), dim, R, a.rope.pairing, pf);
+                rope_partners(xf, rows[warp][sub], dim, R, a.rope.pairing, pf);
 #pragma unroll
                 for (int i = 0; i < kV; ++i) p[i] = pf[i];
             }
@@ -313,7 +344,7 @@ template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32) kv
             }
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                const double2 c = ab[0][dim + i];
+                const double2 c = ab[tt][0][dim + i];
                 x[i] = r * (R ? fma(p[i], c.y, x[i] * c.x) : x[i] * c.x);
             }
             lo = x[0], hi = x[0];
@@ -366,12 +397,15 @@ template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32) kv
                     codes = (codes & ~(15u << (4 * i))) | (uint32_t)__double2int_rn(fmin(fmax(z, 0.0), 15.0)) << (4 * i);
                 }
         }
-        const int head = (isk ? g : g - gk) * RW + sub;
+        const int head = (isk ? gt : gt - gk) * RW + sub;
         if (head < a.H) {
+            const int64_t pg = slot / a.page;
+            const int in_page = (int)(slot - pg * a.page);
+            const int blk = in_page / kKvBlock, place = in_page % kKvBlock;
             uint8_t *part = a.cache + ((pg * a.H + head) * (a.page / kKvBlock) + blk) * F::kBlock + (isk ? 0 : F::kPart);
-            *reinterpret_cast<uint32_t *>(part + kv4_code_offset<D>(tok, dim)) = codes;
+            *reinterpret_cast<uint32_t *>(part + kv4_code_offset<D>(place, dim)) = codes;
             if (lane % LG == 0)
-                *reinterpret_cast<__half2 *>(part + F::kCodes + (tok * F::kGroups + dim / kKvGroup) * 4) = __halves2half2(dh, mh);
+                *reinterpret_cast<__half2 *>(part + F::kCodes + (place * F::kGroups + dim / kKvGroup) * 4) = __halves2half2(dh, mh);
         }
     }
 }
@@ -423,14 +457,17 @@ int check_rope(const int32_t *pos, const double *freq, int R, int pairing, int D
     return QG_OK;
 }
 
-// Blocks along a token's heads: a warp's rows once each while that leaves the card room, else the whole token
-// in one block, so that its sines and cosines are made once.
-int head_blocks(int64_t T, int rows, int D, int sms)
+// Tokens of a block, and blocks along a token's heads: four tokens while that leaves several blocks for each
+// multiprocessor (4099 tokens of 40 heads of 128 took 33 us with one), else one, cut along its heads
+// while the card has room.
+void head_blocks(int64_t T, int rows, int D, int sms, int *together, dim3 *grid)
 {
+    *together = T >= (int64_t)8 * sms ? kMostTogether : 1;
     const int each = kHeadWarps * 32 * kV / D;
     const int most = (rows + each - 1) / each;
-    const int64_t want = (4 * (int64_t)sms + T - 1) / T;
-    return (int)std::min<int64_t>(most, std::max<int64_t>(1, want));
+    const int64_t blocks = (T + *together - 1) / *together;
+    const int64_t want = (4 * (int64_t)sms + blocks - 1) / blocks;
+    *grid = dim3((unsigned)blocks, (unsigned)std::min<int64_t>(most, std::max<int64_t>(1, want)));
 }
 
 template <int D> int launch_norm_rope(int kind, dim3 grid, dim3 block, void *stream, const NormRopeArgs &a)
@@ -499,7 +536,10 @@ int qg_qk_norm_rope(const qg_heads *q, const qg_heads *k, int64_t T, int Hq, int
     a.Hk = Hk;
     int sms = 0;
     if ((rc = current_sms(&sms)) != QG_OK) return rc;
-    const dim3 grid((unsigned)T, head_blocks(T, Hq + Hk + 32 * kV / D - 1, D, sms)), block(kHeadWarps * 32);
+    dim3 grid;
+    const dim3 block(kHeadWarps * 32);
+    a.T = T;
+    head_blocks(T, Hq + Hk + 32 * kV / D - 1, D, sms, &a.together, &grid);
     const int kq = Hq ? view_kind(a.q) : view_kind(a.k), kk = Hk ? view_kind(a.k) : kq;
     switch (D) {
     case 64: return launch_norm_rope<64>(kq == kk ? kq : 0, grid, block, stream, a);
@@ -532,7 +572,10 @@ int qg_kv4_append(const qg_heads *k, const qg_heads *v, int64_t T, int H, int D,
     a.H = H;
     int sms = 0;
     if ((rc = current_sms(&sms)) != QG_OK) return rc;
-    const dim3 grid((unsigned)T, head_blocks(T, 2 * (H + 32 * kV / D - 1), D, sms)), block(kHeadWarps * 32);
+    dim3 grid;
+    const dim3 block(kHeadWarps * 32);
+    a.T = T;
+    head_blocks(T, 2 * (H + 32 * kV / D - 1), D, sms, &a.together, &grid);
     const int kind = view_kind(a.k) == view_kind(a.v) ? view_kind(a.k) : 0;
     switch (D) {
     case 64: return launch_append<64>(kind, grid, block, stream, a);
