@@ -89,8 +89,12 @@ __device__ __forceinline__ void rope_partners(const T (&x)[kV], T *row, int dim,
     }
 }
 
-// The tables of a block's tokens t0 .. t0 + n - 1: ab[j][y][d] = (A, B) of dimension d of token t0 + j, one for
-// each of W weight vectors (null: ones); cs(angle, &c, &s) gives cosine and sine.
+// Where dimension d stands in a table: a lane's first dimension next to the neighbouring lane's first, and so
+// on.  In their own order the lanes' reads would all start in the same banks of shared memory.
+template <int D> __device__ __forceinline__ int place(int d) { return (d % kV) * (D / kV) + d / kV; }
+
+// The tables of a block's tokens t0 .. t0 + n - 1: ab[j][y][place(d)] = (A, B) of dimension d of token t0 + j, one
+// for each of W weight vectors (null: ones); cs(angle, &c, &s) gives cosine and sine.
 template <int D, int W, typename T2, typename F>
 __device__ __forceinline__ void make_tables(T2 (*ab)[W][D], const float *const (&w)[W], const RopeArgs &r, int64_t t0, int n, F cs)
 {
@@ -109,15 +113,15 @@ __device__ __forceinline__ void make_tables(T2 (*ab)[W][D], const float *const (
         cs(angle, &c, &s);
 #pragma unroll
         for (int y = 0; y < W; ++y) {
-            ab[tok][y][i] = T2{wi[y] * c, -(wj[y] * s)};
-            ab[tok][y][j] = T2{wj[y] * c, wi[y] * s};
+            ab[tok][y][place<D>(i)] = T2{wi[y] * c, -(wj[y] * s)};
+            ab[tok][y][place<D>(j)] = T2{wj[y] * c, wi[y] * s};
         }
     }
     const int rest = D - r.R;
     for (int x = threadIdx.x; x < n * rest; x += kHeadWarps * 32) {
         const int tok = x / rest, d = r.R + x - tok * rest;
 #pragma unroll
-        for (int y = 0; y < W; ++y) ab[tok][y][d] = T2{w[y] ? w[y][d] : 1.0f, 0.0f};
+        for (int y = 0; y < W; ++y) ab[tok][y][place<D>(d)] = T2{w[y] ? w[y][d] : 1.0f, 0.0f};
     }
 }
 
@@ -234,9 +238,9 @@ template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32, 4)
         if (which != 2 * tok + !isq) {
             which = 2 * tok + !isq;
 #pragma unroll
-            for (int i = 0; i < kV; i += 2) {
-                const float4 v = *reinterpret_cast<const float4 *>(&ab[tok][!isq][dim + i]);
-                A[i] = v.x, B[i] = v.y, A[i + 1] = v.z, B[i + 1] = v.w;
+            for (int i = 0; i < kV; ++i) {
+                const float2 v = ab[tok][!isq][place<D>(dim + i)];
+                A[i] = v.x, B[i] = v.y;
             }
         }
         float r = 1.0f, p[kV];
@@ -269,7 +273,7 @@ template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32, 4)
 // own error of a border, where it is formed again in 64 bits (for about one value in ten thousand).  d and m
 // are rounded to fp16 first and the codes are found against the rounded pair, which is what a reader
 // multiplies by.
-template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32) kv4_append_kernel(const AppendArgs a)
+template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32, 3) kv4_append_kernel(const AppendArgs a)
 {
     constexpr int LR = D / kV, RW = 32 / LR;
     constexpr int LG = kKvGroup / kV;  // lanes of a group of 64
@@ -340,11 +344,11 @@ template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32) kv
                 double ss = 0.0;
 #pragma unroll
                 for (int i = 0; i < kV; ++i) ss = fma(x[i], x[i], ss);
-                r = 1.0 / sqrt(row_sum<LR>(ss) * (1.0 / D) + a.eps);
+                r = rsqrt(row_sum<LR>(ss) * (1.0 / D) + a.eps);
             }
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
-                const double2 c = ab[tt][0][dim + i];
+                const double2 c = ab[tt][0][place<D>(dim + i)];
                 x[i] = r * (R ? fma(p[i], c.y, x[i] * c.x) : x[i] * c.x);
             }
             lo = x[0], hi = x[0];
@@ -376,7 +380,7 @@ template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32) kv
             lo = l, hi = u;
         }
         // a range past fp16 saturates, so that what is read back stays finite
-        const __half dh = __float2half_rn(fminf((float)((hi - lo) / 15.0), 65504.0f));
+        const __half dh = __float2half_rn(fminf((float)((hi - lo) * (1.0 / 15.0)), 65504.0f));
         const __half mh = __float2half_rn(fminf(fmaxf((float)lo, -65504.0f), 65504.0f));
         const float d = __half2float(dh), m = __half2float(mh);
         const float rd = d > 0.0f ? 1.0f / d : 0.0f;
