@@ -399,11 +399,12 @@ int qg_kv4_read(const void *cache, int64_t pages, int page, int H, int D, const 
  *              0 .. pages - 1 is skipped as if its places were masked
  *   kv_len     device, int32 [nseq]; taken as at least 0 and at most width * page
  *   workspace  device, at least qg_attn_kv4_workspace(Hq, Hk, D, max_q) bytes (0 for arguments out of
- *              range, or without a device), 256-byte aligned, contents of no matter.  Calls that may overlap on the GPU (two streams, two graphs) need one each.  Its
- *              first word is nonzero afterwards only if a copy did not arrive within two seconds (the
- *              results are then void).
+ *              range, or without a device), 256-byte aligned, contents of no matter.  Calls that may overlap on the GPU
+ *              (two streams, two graphs) need one each.  Its first word is nonzero afterwards only if
+ *              a wait inside the kernel ran out after two seconds (the results are then void).
  * Scores, softmax statistics and sums are fp32; cache values and softmax weights enter the products as
- * fp16, rounded once.  Errors as above, plus QG_ERR_SCRATCH. */
+ * fp16, rounded once.  Errors as above (QG_ERR_SHAPE also where T * (Hq/Hk) exceeds 2^31 - 257), plus
+ * QG_ERR_SCRATCH. */
 size_t qg_attn_kv4_workspace(int Hq, int Hk, int D, int max_q);
 int qg_attn_kv4(const qg_heads *q, int64_t T, int nseq, const int32_t *q_start, int max_q, int Hq, int Hk,
                 int D, const void *cache, int64_t pages, int page, const int32_t *table, int width,
@@ -418,13 +419,14 @@ int qg_attn_kv4(const qg_heads *q, int64_t T, int nseq, const int32_t *q_start, 
  *   min-p drops tokens with w < min_p (never the first);
  *   the token is the first, in index order, whose running kept weight exceeds u times all kept weight
  *   (the last kept token for u >= 1).
- * A temperature that is not above 0 takes the largest logit, the lowest index of equal ones.  A logit of
+ * A temperature that is not above 0 takes the largest logit, the lowest index of equal ones; one above 0
+ * counts as at least 2^-126.  A logit of
  * -inf or NaN is never chosen; a row of nothing else gets -1.
  *   logits       device, fp32: row r, token v at logits[r * row_stride + v * elem_stride] (a GEMV's
  *                y[v*B + b]: strides 1 and B)
- *   rows, V      rows >= 0, 1 <= V < 2^31
+ *   rows, V      0 <= rows <= 1048560, 1 <= V < 2^20 (so that the sum of a row's weights fits 64 bits)
  *   temperature, top_p, min_p (fp32), top_k (int32)  device, [rows]; NULL for 1, 1, 0 and 0
- *   u            device, fp32 [rows], 0 <= u < 1;  token  device, int32 [rows]
+ *   u            device, fp32 [rows], 0 <= u < 1 (below 0 it counts as 0);  token  device, int32 [rows]
  *   workspace    device, 4-byte aligned, qg_sample_workspace(rows, V, elem_stride) bytes (0 for rows that
  *                stand one after another), not shared with a call that may overlap; NULL does without, more
  *                slowly

@@ -93,16 +93,6 @@ __device__ __forceinline__ void bulk_g2s_plain(uint32_t dst, const void *src, ui
                  : "memory");
 }
 
-// The same from a converged warp: one elected lane issues it (all lanes hold the same operands).
-__device__ __forceinline__ void bulk_g2s_elect(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile(
-        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-        "@q cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar)
-        : "memory");
-}
-
 __device__ __forceinline__ uint64_t evict_first_policy()
 {
     uint64_t p;

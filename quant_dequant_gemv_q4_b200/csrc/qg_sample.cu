@@ -29,6 +29,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 
 #include "qg_kv4.cuh"
 
@@ -47,6 +48,8 @@ constexpr int kList = kThreads;
 constexpr int kMaxCluster = 16;  // (more than eight: not on every device of this kind, but on this one)
 constexpr double kOne = 17592186044416.0;  // the largest weight, 2^44
 typedef unsigned long long u64;
+constexpr int64_t kMostLogits = (1 << 20) - 1;  // so many weights of 2^44 fit 64 bits
+constexpr int64_t kMostRows = 16 * 65535;       // rows_kernel's grid
 
 struct SampleArgs {
     const float *x;
@@ -393,7 +396,7 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
     const int64_t k_arg = a.top_k ? a.top_k[row] : 0;
     const double p_arg = a.top_p ? (double)a.top_p[row] : 1.0;
     const double mp = a.min_p ? (double)a.min_p[row] : 0.0;
-    const double u = (double)a.u[row];
+    const double u = a.u[row] < 0.0f ? 0.0 : (double)a.u[row];
     const float *x = a.x + row * a.rs + base * a.es;
     float top = -INFINITY;
     {
@@ -462,7 +465,7 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
         cl.sync();
         return;
     }
-    r.c = 1.4426950408889634074 / (double)t;
+    r.c = 1.4426950408889634074 / (double)fmaxf(t, FLT_MIN);  // (finite in fp32)
     r.zc = (double)top * r.c;
     r.ch = (float)r.c;
     r.cl = (float)(r.c - (double)r.ch);
@@ -817,7 +820,7 @@ size_t qg_sample_workspace(int64_t rows, int64_t V, int64_t elem_stride)
 {
     // rows that do not stand one after another are set out so first: a cluster reads its row alone, and of
     // rows side by side it would fetch a whole sector for each logit
-    if (rows < 2 || V < 1 || elem_stride == 1 || rows > 0xfffff || V > 0x7fffffff) return 0;
+    if (rows < 2 || V < 1 || elem_stride == 1 || rows > kMostRows || V > kMostLogits) return 0;
     return (size_t)rows * (size_t)V * sizeof(float);
 }
 
@@ -825,7 +828,7 @@ int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t row_stride, 
               const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
               const float *u, int32_t *token, void *workspace, size_t workspace_bytes, void *stream)
 {
-    if (rows < 0 || V < 1 || V > 0x7fffffff || rows > 0xfffff) return QG_ERR_SHAPE;
+    if (rows < 0 || V < 1 || V > kMostLogits || rows > kMostRows) return QG_ERR_SHAPE;
     if (rows == 0) return QG_OK;
     if (!logits || !token || !u) return QG_ERR_NULL;
     const uintptr_t bits = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(temperature) |

@@ -154,3 +154,12 @@ def test_reference_samples_by_hand():
     assert ref.sample(x, 0.0, None, None, None, 0.99) == 1
     assert ref.sample(np.full(3, -np.inf), 1.0, None, None, None, 0.5) == -1
     assert ref.sample(np.zeros(4), 1.0, 2, None, None, 0.75) == 1  # ties: the lower indices stay
+
+
+@pytest.mark.parametrize("kw", [dict(V=1 << 20), dict(rows=16 * 65535 + 1)])
+def test_sample_sizes_past_the_sums_and_the_grid(L, kw):
+    """2^20 weights of 2^44 would not fit 64 bits; a grid has 65535 rows of blocks."""
+    a = dict(rows=2, V=100)
+    a.update(kw)
+    assert L.qg_sample(A, a["rows"], a["V"], a["V"], 1, A, A, A, A, A, A, None, 0, None) == qg.QG_ERR_SHAPE
+    assert qg.qg_sample_workspace(a["rows"], a["V"], 2) == 0

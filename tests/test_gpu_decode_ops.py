@@ -459,6 +459,80 @@ def test_sample_large_vocabulary_and_many_rows(qg):
     check_sample(qg, x, u=rng.random(300), p=rng.uniform(0, 1, 300))
 
 
+def test_sample_rows_that_no_cluster_holds(qg):
+    """Rows too long for the shared memory of eight processors, of more rows than sixteen are taken for; and the longest."""
+    rng = np.random.default_rng(3)
+    x = (rng.normal(size=(9, 420_001)) * 2).astype("f4")
+    x[2] = rng.integers(-3, 3, x.shape[1])  # ties past any list
+    u = rng.random(9)
+    check_sample(qg, x, u=u, p=rng.uniform(0.1, 1, 9), k=rng.integers(0, 3000, 9))
+    check_sample(qg, x, u=u, p=rng.uniform(0.1, 1, 9), mp=rng.uniform(0, 0.1, 9), major="vocabulary")
+    x = np.zeros((2, (1 << 20) - 1), "f4")
+    x[1] = rng.normal(size=x.shape[1])
+    check_sample(qg, x, u=[0.999, 0.25])
+
+
+def test_sample_tiny_temperatures_and_random_numbers_below_zero(qg):
+    x = np.array([[0, 1, 3, 3, 2], [-1, 0, 0, 0, -2]], "f4").repeat(3, 0)
+    for t in (1.2e-38, 1e-40, 1.5e-45):
+        check_sample(qg, x, t=np.full(6, t, "f4"), u=[0.1, 0.6, 0.9, 0.1, 0.5, 0.9], p=[1, 0.9, 0.4, 1, 0.9, 0.2])
+    assert run_sample(qg, x[:2], u=[-1.0, -np.inf]).tolist() == [0, 0]
+
+
+def test_sample_side_by_side_without_a_workspace(qg):
+    """The C entry takes rows side by side as they are where it gets no workspace."""
+    import torch
+    rng = np.random.default_rng(9)
+    x = (rng.normal(size=(5, 30_011)) * 2).astype("f4")
+    u, p = rng.random(5).astype("f4"), rng.uniform(0.3, 0.99, 5).astype("f4")
+    lx, du, dp = dev(x.T), dev(u), dev(p)
+    tok = torch.full((7,), -9, dtype=torch.int32, device="cuda")
+    st = torch.cuda.current_stream().cuda_stream
+    assert qg.lib().qg_sample(lx.data_ptr(), 5, 30_011, 1, 5, None, None, dp.data_ptr(), None, du.data_ptr(), tok.data_ptr(), None, 0,
+                              st) == qg.QG_OK
+    assert tok.cpu().tolist() == [ref.sample(x[i], None, None, p[i], None, u[i]) for i in range(5)] + [-9, -9]
+
+
+def test_calls_on_two_streams_at_once(qg):
+    """Attention and sampling on two streams, launched so that they may overlap, give what they give alone."""
+    import torch
+    rng = np.random.default_rng(11)
+    cache = qg.kv4_cache(40, 64, 2, 128)
+    kv = torch.randn(40 * 64, 2, 128, device="cuda")
+    qg.qg_kv4_append(kv, kv, None, 0.0, None, None, 0, torch.arange(40 * 64, device="cuda"), cache, 64)
+    sets = []
+    for i in range(2):
+        q = torch.randn(3, 8, 128, device="cuda", dtype=torch.float16)
+        table = dev(np.stack([rng.permutation(40) for _ in range(3)]).astype(np.int32))
+        lens = dev(rng.integers(1, 2560, 3).astype(np.int32))
+        x = torch.randn(4, 60_000, device="cuda").t().contiguous().t()
+        u = torch.rand(4, device="cuda")
+        sets.append((q, table, lens, x, u))
+    start = dev(np.arange(4, dtype=np.int32))
+
+    def go(s, out, tok):
+        q, table, lens, x, u = s
+        qg.qg_attn_kv4(q, start, 1, cache, 64, table, lens, 0.1, out)
+        qg.qg_sample(x, None, None, None, None, u, tok)
+
+    fresh = lambda: (torch.zeros(3, 8, 128, device="cuda", dtype=torch.float16), torch.zeros(4, device="cuda", dtype=torch.int32))  # noqa: E731
+    want = [fresh() for _ in sets]
+    for s, w in zip(sets, want):
+        go(s, *w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[fresh() for _ in range(20)] for _ in sets]
+    torch.cuda.synchronize()
+    for r in range(20):
+        for s, g, st in zip(sets, got, streams):
+            with torch.cuda.stream(st):
+                go(s, *g[r])
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for out, tok in g:
+            assert torch.equal(out, w[0]) and torch.equal(tok, w[1])
+
+
 def test_sample_follows_the_weights(qg):
     """Evenly spread random numbers reach every token in proportion to its weight."""
     import torch
