@@ -461,12 +461,13 @@ int check_rope(const int32_t *pos, const double *freq, int R, int pairing, int D
     return QG_OK;
 }
 
-// Tokens of a block, and blocks along a token's heads: four tokens while that leaves several blocks for each
-// multiprocessor (4099 tokens of 40 heads of 128 took 33 us with one), else one, cut along its heads
-// while the card has room.
+// Tokens of a block, and blocks along a token's heads: four tokens where that leaves several blocks for each
+// multiprocessor, else one, cut along its heads while the card has room.  With one and with four, 40 heads of 128
+// took 11.8 and 12.8 us for 1300 tokens, 15.9 and 16.2 for 2000, 30.5 and 26.3 for 4099; the append of eight
+// heads 14.4 and 15.0 us for 2000, 27.4 and 24.8 for 4099.
 void head_blocks(int64_t T, int rows, int D, int sms, int *together, dim3 *grid)
 {
-    *together = T >= (int64_t)8 * sms ? kMostTogether : 1;
+    *together = T >= (int64_t)16 * sms ? kMostTogether : 1;
     const int each = kHeadWarps * 32 * kV / D;
     const int most = (rows + each - 1) / each;
     const int64_t blocks = (T + *together - 1) / *together;

@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
+#include <mutex>
 
 #include "qg_kv4.cuh"
 
@@ -45,10 +46,10 @@ constexpr int kPer = kBins / kThreads;  // bins of a thread
 constexpr float kBinStep = 0.98922801319397548f;  // 2^(-1/64)
 constexpr float kDeepest = 45.9f;  // below 2^-45.9 of the largest a weight is 0
 constexpr int kList = kThreads;
-constexpr int kMaxCluster = 16;  // (more than eight: not on every device of this kind, but on this one)
 constexpr double kOne = 17592186044416.0;  // the largest weight, 2^44
 typedef unsigned long long u64;
 constexpr int64_t kMostLogits = (1 << 20) - 1;  // so many weights of 2^44 fit 64 bits
+constexpr int kMostCtas = 16;
 constexpr int64_t kMostRows = 16 * 65535;       // rows_kernel's grid
 
 struct SampleArgs {
@@ -257,11 +258,11 @@ __device__ __noinline__ u64 block_sort(u64 v, u64 *buf, int m)
 // all (every CTA reading every histogram took four times as long with sixteen).
 __device__ __forceinline__ void cluster_counts(cg::cluster_group &cl, Shared &s, unsigned (&c)[kPer])
 {
-    const unsigned n = cl.num_blocks(), share = kBins / n;
+    const unsigned n = cl.num_blocks();
     cl.sync();  // all histograms are whole
     if (n > 1) {
-        for (unsigned b = threadIdx.x; b < share; b += kThreads) {
-            const unsigned at = cl.block_rank() * share + b;
+        const unsigned share = (kBins + n - 1) / n, end = min((cl.block_rank() + 1) * share, (unsigned)kBins);
+        for (unsigned at = cl.block_rank() * share + threadIdx.x; at < end; at += kThreads) {
             unsigned sum = 0;
 #pragma unroll 4
             for (unsigned r = 0; r < n; ++r) sum += cl.map_shared_rank(&s, r)->count[at];
@@ -812,6 +813,75 @@ __global__ void __launch_bounds__(256) rows_kernel(const float *x, float *y, int
     }
 }
 
+// Clusters of 1 to 16 CTAs that the current device holds side by side (a CTA takes a multiprocessor; the
+// multiprocessors of a cluster lie in one of the chip's partitions, so fewer than their number suggests), and its
+// shared memory for a block.
+struct Card {
+    int optin;
+    int side_by_side[kMostCtas + 1];  // 0: a size that it does not take
+};
+
+int look_at_card(Card *out)
+{
+    static std::atomic<int> known[64];
+    static Card cards[64];
+    static std::mutex lock;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return QG_ERR_CUDA;
+    if (!known[dev].load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> hold(lock);
+        Card c = {};
+        if (cudaDeviceGetAttribute(&c.optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) return QG_ERR_CUDA;
+        for (auto kernel : {sample_kernel<true>, sample_kernel<false>})
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, c.optin) != cudaSuccess ||
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+                return QG_ERR_CUDA;
+        for (int C = 1; C <= kMostCtas; ++C) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(C);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = c.optin;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = C;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&c.side_by_side[C], sample_kernel<true>, &cfg) != cudaSuccess) {
+                c.side_by_side[C] = 0;
+                (void)cudaGetLastError();
+            }
+        }
+        if (c.side_by_side[1] < 1) return QG_ERR_CUDA;
+        cards[dev] = c;
+        known[dev].store(1, std::memory_order_release);
+    }
+    *out = cards[dev];
+    return QG_OK;
+}
+
+// CTAs of a row's cluster.  A row takes about as long as 35000 logits of a CTA and then its CTAs' share (of a share
+// that does not fit the shared memory 2.4 times as long); rows that find no room side by side wait.  Shares are not cut
+// below 8192 logits.  Top-p of one row of 151936: 45 us with 8 CTAs, 37 with 16; of 8 rows, 46 with 8 and 74 with 16, of
+// which seven find room; of 16 rows 228, 130, 64, 52 and 83 us with 1, 2, 4, 6 and 8; of 64 rows of 50257 90, 46, 68 and
+// 139 us with 1, 2, 4 and 8; of 16 rows of 248320 156, 82 and 115 us with 4 (not resident), 6 and 8.
+int cluster_of(const Card &card, int64_t rows, int64_t V)
+{
+    int best = 1;
+    double least = 0;
+    for (int C = 1; C <= kMostCtas && (C == 1 || V > (int64_t)(C - 1) * 8192); ++C) {
+        const int64_t side = card.side_by_side[C], per = (V + C - 1) / C;
+        if (side < 1) continue;
+        const bool resident = per <= (card.optin - (int)sizeof(Shared)) / 4;
+        const double cost = (double)((rows + side - 1) / side) * (35000.0 + (double)per * (resident ? 1.0 : 2.4));
+        if (C == 1 || cost < least) {
+            best = C;
+            least = cost;
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
 extern "C" {
@@ -838,19 +908,8 @@ int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t row_stride, 
     if (bits % 4) return QG_ERR_ALIGN;
     const size_t need = qg_sample_workspace(rows, V, elem_stride);
     if (workspace && workspace_bytes < need) return QG_ERR_SCRATCH;
-    static std::atomic<int> optins[64];
-    int dev = 0, optin = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return QG_ERR_CUDA;
-    if (dev < 64) optin = optins[dev].load(std::memory_order_relaxed);
-    if (optin == 0) {
-        if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-            cudaFuncSetAttribute(sample_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin) != cudaSuccess ||
-            cudaFuncSetAttribute(sample_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin) != cudaSuccess ||
-            cudaFuncSetAttribute(sample_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-            cudaFuncSetAttribute(sample_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-            return QG_ERR_CUDA;
-        if (dev < 64) optins[dev].store(optin, std::memory_order_relaxed);
-    }
+    Card card;
+    if (const int rc = look_at_card(&card); rc != QG_OK) return rc;
     SampleArgs a = {};
     a.x = logits;
     a.rs = row_stride;
@@ -863,10 +922,7 @@ int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t row_stride, 
         a.rs = V;
         a.es = 1;
     }
-    // Eight CTAs a row; sixteen for so few rows that their clusters find room side by side; fewer for short rows.
-    const int most = rows <= 8 ? kMaxCluster : 8;
-    int C = 1;
-    while (C < most && V > (int64_t)C * 8192) C *= 2;
+    const int C = cluster_of(card, rows, V);
     a.V = V;
     a.temperature = temperature;
     a.top_k = top_k;
@@ -875,7 +931,7 @@ int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t row_stride, 
     a.u = u;
     a.token = token;
     a.per = (V + C - 1) / C;
-    const bool resident = a.per <= (optin - (int)sizeof(Shared)) / 4;
+    const bool resident = a.per <= (card.optin - (int)sizeof(Shared)) / 4;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * C));
     cfg.blockDim = dim3(kThreads);
