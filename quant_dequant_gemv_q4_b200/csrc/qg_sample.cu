@@ -11,14 +11,15 @@
 // One thread-block cluster takes a row and keeps it in its shared memory (up to sixteen CTAs, so 248,320
 // logits are read once), and the passes over the row run on chip.  The row is never sorted:
 //   1. the largest logit;
-//   2. a histogram of counts over bins linear in z, 64 a factor of two, and (for top-p) the exact sum of all weights;
+//   2. a histogram of counts over bins linear in z, 64 a factor of two, and (for top-p) the weights' sum in fp32;
 //   3. the bins in which the cut lies: exactly known for the k-th token; for top-p, since a bin's weights
 //      are within a factor 2^(1/64) of each other, the weight below a bin is bounded on both sides by the
 //      counts, which leaves two or three bins.  If the tokens down to the last of these are at most kList,
 //      they are gathered in one CTA, sorted, filtered and chosen from;
 //   4. otherwise only the tokens of those bins are gathered and sorted (or, should they be too many, counted in
-//      finer and finer bins), together with the exact weight above them, which gives the cut; a pass over the
-//      row in index order then finds the token.
+//      finer and finer bins), together with the exact weight above them, which gives the cut;
+//   5. the token is found from the running sums in index order: from those of 4, a thread's consecutive logits each,
+//      and the listed tokens above the cut, or by another pass where that does not do (min-p, ties at the cut).
 //
 // Weights are whole multiples of 2^-44 of the largest (64-bit integers): their sums do not depend on the order
 // of the additions, so a call gives the same token every time.  A weight is off by about 2^-30 of itself
@@ -39,7 +40,7 @@ namespace {
 using namespace qg;
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 1024;  // (16 x 248320: 57 us, with 512 threads 70 us)
+constexpr int kThreads = 1024;  // (with 512, 16 x 248320 took a quarter longer)
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 4096;
 constexpr int kPer = kBins / kThreads;  // bins of a thread
@@ -50,6 +51,7 @@ constexpr double kOne = 17592186044416.0;  // the largest weight, 2^44
 typedef unsigned long long u64;
 constexpr int64_t kMostLogits = (1 << 20) - 1;  // so many weights of 2^44 fit 64 bits
 constexpr int kMostCtas = 16;
+constexpr double kRough = 4294967296.0;  // the largest weight in the rough sum
 constexpr int64_t kMostRows = 16 * 65535;       // rows_kernel's grid
 
 struct SampleArgs {
@@ -71,7 +73,7 @@ struct Shared {
     float top;
     int64_t best;
     unsigned listed, klo, khi, cut_key, cut_ties, cta_ties;
-    u64 cta_weight;
+    u64 cta_weight, cta_total, cta_rough;
     // the CTA's own
     unsigned own_listed, own_at;
     u64 scan_w[kWarps];
@@ -157,6 +159,7 @@ template <bool RESIDENT> struct Row {
     {
         return __float_as_int(fmaf(fminf((xmax - x) * ch, kDeepest), 64.0f, 12582912.0f)) - 0x4b400000;
     }
+    __device__ __forceinline__ float rough(float x) const { return exp2f(-fminf((xmax - x) * ch, kDeepest)); }
     // whether the weight is at least min_p (decided in 64 bits where it is close)
     __device__ __forceinline__ bool at_least(float x, u64 w, double min_p) const
     {
@@ -302,8 +305,8 @@ __device__ unsigned find_count(Shared &s, const unsigned (&c)[kPer], unsigned k)
 
 // The bins between which the cut of top-p lies: the first whose lower bound, and the first whose upper bound,
 // of the weight after it is at most `tail`.  s.before[0]: tokens before the first, s.before[1]: down to the
-// last of them (of all tokens, `c`; the weights are those of `kept` of them).  The bounds' margin of 1e-4
-// covers the bins' borders and these sums, all in fp32.
+// last of them (of all tokens, `c`; the weights are those of `kept` of them).  The bounds' margin of 2e-4
+// covers the bins' borders, these sums and the one in `tail`, all in fp32 (of at most 2^10 logits a thread).
 __device__ void find_share(Shared &s, const unsigned (&c)[kPer], const unsigned (&kept)[kPer], float tail)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -314,9 +317,9 @@ __device__ void find_share(Shared &s, const unsigned (&c)[kPer], const unsigned 
     unsigned sum = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        hi[j] = (float)kept[j] * edge * 1.0001f;
+        hi[j] = (float)kept[j] * edge * 1.0002f;
         edge *= kBinStep;
-        lo[j] = b0 + j >= 2937 ? 0.0f : (float)kept[j] * edge * 0.9999f;
+        lo[j] = b0 + j >= 2937 ? 0.0f : (float)kept[j] * edge * 0.9998f;
         h += hi[j];
         l += lo[j];
         sum += c[j];
@@ -473,24 +476,30 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
 
     // kept: the tokens above cut_key, and the first cut_ties equal to it
     constexpr unsigned kAll = 0xffffffffu;
+    // the logits of a thread where order counts: consecutive, an odd number of them, so that the threads' reads fall
+    // in different banks
+    const int seg = ((n + kThreads - 1) / kThreads) | 1;
+    const int i0 = min(n, tid * seg), i1 = min(n, i0 + seg);
+    u64 above_mine = 0;   // weight of the thread's logits in the bins above the cut's
+    bool listed = false;  // ... and the kept tokens of the cut's bins are those of the list from cut_key up
     unsigned cut_key = 0, cut_ties = kAll;
     if (k || by_p) {
-        u64 all_w = 0;  // the share's total
+        u64 all_w = 0;      // the share's total
+        float rough = 0.0f;  // of all weights, in fp32 (all that finding the bins takes)
         r.each([&](int, float x) {
-            int b;
-            if (k)
-                b = r.bin(x);
-            else
-                all_w += r.weight(x, &b);
-            if (x != -INFINITY) atomicAdd(&s.count[b], 1u);
+            if (x != -INFINITY) {
+                atomicAdd(&s.count[r.bin(x)], 1u);
+                rough += r.rough(x);
+            }
         });
         if (!k) {
-            all_w = block_sum(s, all_w);
-            if (tid == 0) s.cta_weight = all_w;
+            const u64 w = block_sum(s, (u64)(rough * kRough));
+            if (tid == 0) s.cta_rough = w;
         }
         unsigned c[kPer], kept_c[kPer];  // tokens of a bin, and those of the first k
         cluster_counts(cl, s, c);
-        if (!k) all_w = over_cluster(cl, s, &Shared::cta_weight);
+        float tail = 0.0f;
+        if (!k) tail = (float)((1.0 - p) * (double)over_cluster(cl, s, &Shared::cta_rough) * (1.0 / kRough));
 #pragma unroll
         for (int j = 0; j < kPer; ++j) kept_c[j] = c[j];
 
@@ -501,7 +510,7 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
             if (share && !by_p) break;
             unsigned before, reach;  // tokens before the bins of the cut, and down to the last of them
             if (share) {
-                find_share(s, c, kept_c, (float)((1.0 - p) * (double)all_w * (1.0 / kOne)));
+                find_share(s, c, kept_c, k ? (float)((1.0 - p) * (double)all_w * (1.0 / kOne)) : tail);
                 before = s.before[0];
                 reach = s.before[1];
             } else {
@@ -525,21 +534,24 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
             const int b0 = whole ? 0 : min(s.bin[0], s.bin[1]), b1 = s.bin[1];
             const bool listable = whole || reach - before <= kList;
             Shared *first = cl.map_shared_rank(&s, 0);
-            // The tokens of those bins: into the list, or their least and largest key; and the weight of those above
-            // them, summed, or as all less the rest, whichever are fewer.  (After a cut by the count the tokens
-            // below it are not in the share's total.)
-            const bool sum = share && !whole, up = k || before < (unsigned)(a.V / 2);
-            u64 above = 0;
+            // The tokens of those bins: into the list, or their least and largest key; for a share also the weight of
+            // those above them and (after a cut by the count it is known, and the tokens below that are not in it)
+            // of all.  The weights go by the threads' segments, for the choice to use.
+            const bool weigh = share && !(k && whole);
+            u64 above = 0, total = 0;
             unsigned klo = 0xffffffffu, khi = 0;
-            r.each([&](int i, float x) {
+#pragma unroll 1
+            for (int i = weigh ? i0 : tid; i < (weigh ? i1 : n); i += weigh ? 1 : kThreads) {
+                const float x = r.get(i);
                 int b;
-                if (sum) {
+                if (weigh) {
                     const u64 w = r.weight(x, &b);
-                    above += (b < b0) == up ? w : 0;
+                    total += w;
+                    above += b < b0 ? w : 0;
                 } else {
                     b = r.bin(x);
                 }
-                if (b < b0 || b > b1 || x == -INFINITY) return;
+                if (b < b0 || b > b1 || x == -INFINITY) continue;
                 const unsigned key = key_of(x);
                 klo = min(klo, key);
                 khi = max(khi, key);
@@ -547,10 +559,15 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                     const unsigned at = atomicAdd(&s.own_listed, 1u);
                     if (at < kList) s.own[at] = (u64)key << 32 | (0xffffffffu - (unsigned)(base + i));
                 }
-            });
-            if (sum) {
+            }
+            if (weigh) {
+                above_mine = above;
                 above = block_sum(s, above);
-                if (tid == 0) s.cta_weight = above;
+                total = block_sum(s, total);
+                if (tid == 0) {
+                    s.cta_weight = above;
+                    s.cta_total = total;
+                }
             }
             if (listable) {
                 __syncthreads();
@@ -561,9 +578,9 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                 if (tid < found && s.own_at + tid < kList) first->list[s.own_at + tid] = s.own[tid];
                 cl.sync();
                 if (rank == 0) {
-                    if (sum) {
+                    if (weigh) {
                         above = over_cluster(cl, s, &Shared::cta_weight);
-                        if (!up) above = all_w - above;
+                        if (!k) all_w = over_cluster(cl, s, &Shared::cta_total);
                     }
                     const int m = (int)min(s.listed, (unsigned)kList);
                     const bool mine = tid < m;
@@ -608,6 +625,7 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                 if (whole) return;
                 cut_key = first->cut_key;
                 cut_ties = first->cut_ties;
+                listed = weigh && cut_ties == kAll && !(mp > 0.0);
             } else {
                 // too many tokens next to the cut: finer and finer histograms over the keys lo .. hi of those bins
                 klo = __reduce_min_sync(0xffffffffu, klo);
@@ -617,9 +635,9 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                     atomicMax(&s.khi, khi);
                 }
                 cl.sync();
-                if (sum) {
+                if (weigh) {
                     above = over_cluster(cl, s, &Shared::cta_weight);
-                    if (!up) above = all_w - above;
+                    if (!k) all_w = over_cluster(cl, s, &Shared::cta_total);
                 }
                 const double target = share ? p * (double)all_w : 0.0;
                 u64 done_w = above;
@@ -692,6 +710,7 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                 }
             }
             cl.sync();  // the cut has been read everywhere: the list and the bounds may be used again
+            if (listed) break;  // (a share's cut is the last)
             if (tid == 0) {
                 s.listed = s.own_listed = 0;
                 s.klo = 0xffffffffu;
@@ -729,10 +748,7 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
         }
     }
 
-    // ---- the choice, in index order: each thread takes consecutive logits (an odd number of them, so
-    // that the threads' reads fall in different banks)
-    const int seg = ((n + kThreads - 1) / kThreads) | 1;
-    const int i0 = min(n, tid * seg), i1 = min(n, i0 + seg);
+    // ---- the choice, in index order
     unsigned ties_before = 0;
     if (cut_ties != kAll) {  // which of the tokens equal to the cut are kept depends on those before them
         unsigned ties = 0;
@@ -752,11 +768,21 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
     };
     u64 mine = 0;
     unsigned seen = ties_before;
+    if (listed) {
+        s.list[tid] = 0;
+        __syncthreads();
+        const u64 e = tid < s.own_listed ? s.own[tid] : 0;
+        if ((unsigned)(e >> 32) >= cut_key)
+            atomicAdd(&s.list[(unsigned)(0xffffffffu - (unsigned)e - base) / (unsigned)seg], r.weight(of_key((unsigned)(e >> 32))));
+        __syncthreads();
+        mine = above_mine + s.list[tid];
+    } else {
 #pragma unroll 1
-    for (int i = i0; i < i1; ++i) {
-        const float x = r.get(i);
-        mine += kept_weight(x, seen);
-        seen += key_of(x) == cut_key;
+        for (int i = i0; i < i1; ++i) {
+            const float x = r.get(i);
+            mine += kept_weight(x, seen);
+            seen += key_of(x) == cut_key;
+        }
     }
     const Scan z = block_scan(s, 0, mine);
     if (tid == 0) s.cta_weight = z.w_all;
@@ -862,9 +888,9 @@ int look_at_card(Card *out)
 
 // CTAs of a row's cluster.  A row takes about as long as 35000 logits of a CTA and then its CTAs' share (of a share
 // that does not fit the shared memory 2.4 times as long); rows that find no room side by side wait.  Shares are not cut
-// below 8192 logits.  Top-p of one row of 151936: 45 us with 8 CTAs, 37 with 16; of 8 rows, 46 with 8 and 74 with 16, of
-// which seven find room; of 16 rows 228, 130, 64, 52 and 83 us with 1, 2, 4, 6 and 8; of 64 rows of 50257 90, 46, 68 and
-// 139 us with 1, 2, 4 and 8; of 16 rows of 248320 156, 82 and 115 us with 4 (not resident), 6 and 8.
+// below 8192 logits.  Top-p of one row of 151936 took 45 us with 8 CTAs, 37 with 16; of 8 rows, 46 with 8 and 74 with
+// 16, of which seven find room; of 16 rows 228, 130, 64, 52 and 83 us with 1, 2, 4, 6 and 8; of 64 rows of 50257 90, 46,
+// 68 and 139 us with 1, 2, 4 and 8; of 16 rows of 248320 156, 82 and 115 us with 4 (not resident), 6 and 8.
 int cluster_of(const Card &card, int64_t rows, int64_t V)
 {
     int best = 1;
