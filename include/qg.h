@@ -1,5 +1,6 @@
 /*
- * qg.h -- C ABI of libqg, a B200 (sm_100a) dequant GEMV over GGML block-quantized weights:
+ * qg.h -- C ABI of libqg, a B200 (sm_100a) dequant GEMV over GGML block-quantized weights, and (second
+ * half) the operators between the GEMVs of a decode step:
  *
  *     y[N,B] = dequant(W[N,K]) . x[K,B]      x fp16, accumulation fp32, y fp32, 1 <= B <= 16
  *

@@ -22,10 +22,19 @@
 // Which k index a dimension has in the first product, and which lane in the second, is free: the nibble
 // order is left as it falls, q is staged in that order and O is unscrambled when it is written.
 //
-// Roles of a CTA's warps (one CTA an SM): a producer (a bulk copy of 18 D bytes for each 16 places, several
-// tiles ahead), four warps that unpack keys, four for values, four (N = 128: eight) for the softmax, and
-// one that issues the matrix instructions.  Key and value operands are double-buffered in parts of a tile
-// (kSub), scores and weights in tiles, all handed over by mbarriers.
+// Roles of a CTA's warps (one CTA an SM): a producer (bulk copies of 18 D bytes for each 16 places, those of
+// neighbours in one, several tiles ahead), one or two warpgroups that unpack keys and as many for values, one for the
+// softmax of each 32 query rows, and two warps that issue the matrix instructions, one for each product.  Key and
+// value operands have buffers of a part of a tile (kSub), scores and weights of a tile, all handed over by mbarriers.
+//
+// What bounds it, at decode (N = 16): issuing instructions.  A tile of D = 256 takes about 7100 warp instructions
+// (unpacking two thirds of them) and 2600 cycles, 64-69% of the SM's issue slots, where its bytes would arrive in
+// about 1660; a part of an item costs about 6000 cycles more (q in, the first reference, O out), which ragged
+// batches and pages of few tiles feel.  200001 places of 4 heads: 69 us, 3.3 TB/s; 16 sequences of up to 16384:
+// 54 us; 64 of up to 6000, D = 128: 101 us.  Two softmax warpgroups on alternate tiles, each with an O of its own,
+// took 77, 58 and 100 us, two producers 70, 56 and 107: the instruction caches hold these loops only just, and
+// what shortens one of them lengthens the others.  At N = 128 the softmax bounds it, a thread's 32 scores at a time:
+// 1000 tokens on 7000, 437 us, 730 TFLOP/s.
 //
 // Softmax in base 2 on fp32 scores.  A thread holds one place's scores; the reference maximum of a row is
 // shared by the 128 places and moves only when a score exceeds it by more than 8 (so hardly ever after the
@@ -1091,7 +1100,9 @@ template <int D, int N, int RB> __global__ void __launch_bounds__(512) attn_kv4_
 }
 
 // Query rows of an item: the fewest columns that hold what a sequence has (by the caller's max_q), so that
-// few rows leave tensor time and shared memory to the copies; many rows share each unpacked tile.
+// few rows leave tensor time and shared memory to the copies; many rows share each unpacked tile.  With 16, 32, 64 and
+// 128 columns, 12 rows on 200001 places took 69, 87, 89 and 136 us, 48 rows on 4 x 30000 places 112, 106, 69 and 103,
+// and 6000 rows on 8000 places 881, 586, 316 and 272.
 int rows_of(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
 struct WsLayout {

@@ -11,7 +11,10 @@
 // makes them once in shared memory, and its warps take the token's heads with a lane's eight of each in
 // registers, the next rows' loads in flight while a row is worked on.  With many tokens a block takes
 // four: their tables are made side by side, and what a block waits for before its first row is shared.  The kernels are bound by
-// instructions and memory traffic for long inputs and by launch and load latency for a few tokens.
+// instructions and memory traffic for long inputs and by launch and load latency for a few tokens: 4099 tokens of
+// 32 + 8 heads of 128, fp16, take 27 us (84 MB, 3.1 TB/s), one token 2.7; appending 6001 tokens and reading them back
+// 32 and 17 us, 16 tokens 6.8 together.  (Of the append the 64-bit arithmetic takes the most; with two blocks a
+// multiprocessor instead of three 6001 tokens took 3 us longer.)
 #include <algorithm>
 
 #include "qg_kv4.cuh"
