@@ -8,14 +8,13 @@ all computation runs in the library's CUDA kernels.  There is no CPU fallback: i
 missing, every call raises.
 
 Pointers may be given as torch tensors (their ``data_ptr()``) or plain integers; ``stream=None``
-means torch's current CUDA stream.  The operators around the GEMVs take torch CUDA tensors and read
-sizes and strides from them.
+means torch's current CUDA stream.  The operators around the GEMVs take torch CUDA tensors, whose sizes
+and strides a small C++ module (``qg_binding.so``, of ``csrc/qg_binding.cpp``) hands to the same C ABI.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 import numpy as np
 
@@ -54,6 +53,7 @@ QG_NOALLOC_SCRATCH_BYTES = 8 << 20
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqg.so")
+BINDING_PATH = os.path.join(_HERE, "qg_binding.so")
 _lib = None
 
 
@@ -285,77 +285,30 @@ def qg_hbm_read(src, nbytes: int, out, stream=None) -> None:
     _ok(lib().qg_hbm_read(_ptr(src), int(nbytes), _ptr(out), _stream(stream)), "qg_hbm_read")
 
 
-# The operators around the GEMVs are short (a few microseconds on the GPU), so what their wrappers do on the
-# host counts: torch is looked up once, views go to C as packed bytes, and the checks are a few attribute reads.
-_tc = None
-_pack_heads = struct.Struct("@Pqqqi4x").pack  # qg_heads
+# The operators around the GEMVs are short (a few microseconds on the GPU), so what a call does on the host counts:
+# their tensors are read and checked in C++ (csrc/qg_binding.cpp), which calls the library.
+_binding = None
 
 
-class _Torch:
-    def __init__(self):
-        import torch
-        self.f32, self.f16, self.f64 = torch.float32, torch.float16, torch.float64
-        self.i32, self.i64, self.u8 = torch.int32, torch.int64, torch.uint8
-        self.empty, self.device = torch.empty, torch.cuda.current_device
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self.stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+def _bound():
+    """The module that calls the operators around the GEMVs on torch tensors (raises if it has not been built)."""
+    global _binding
+    if _binding is None:
+        import importlib.util
 
-
-def _torch() -> _Torch:
-    global _tc
-    if _tc is None:
-        _tc = _Torch()
-    return _tc
-
-
-def _where(tc, what: str, *tensors) -> int:
-    """The current device; every tensor (None apart) has to be on it, where the kernels run."""
-    dev = tc.device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{what}: every tensor must be on the current CUDA device ({dev}), got {t.device}")
-    return dev
-
-
-def _handle(tc, stream, dev: int) -> int:
-    if stream is None:
-        return tc.stream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _view(tc, t, what: str, name: str) -> bytes:
-    """A [tokens, heads, dims] tensor as a qg_heads."""
-    dt, st = t.dtype, t.stride()
-    if (dt is not tc.f32 and dt is not tc.f16) or len(st) != 3:
-        raise ValueError(f"{what}: {name} is fp32 or fp16 [tokens, heads, dims], got {dt} {tuple(t.shape)}")
-    return _pack_heads(t.data_ptr(), st[0], st[1], st[2], QG_TYPE_F32 if dt is tc.f32 else QG_TYPE_F16)
-
-
-def _vec(t, dtype, n: int, what: str, name: str):
-    """The address of a contiguous vector of n elements of a type, or None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{what}: {name} is a contiguous {dtype} [{n}], got {t.dtype} {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _cache_sizes(tc, cache, page: int, what: str):
-    if cache.dtype is tc.u8 and cache.dim() == 4 and cache.is_contiguous():
-        pages, H, blocks, width = cache.shape
-        if page >= 16 and blocks * 16 == page and width % 18 == 0:
-            return pages, H, width // 18
-    raise ValueError(f"{what}: the cache is contiguous uint8 [pages, heads, page / 16, 18 D] with pages of {page} "
-                     f"tokens, got {cache.dtype} {tuple(cache.shape)}")
-
-
-def _rope(tc, pos, inv_freq, T: int, what: str):
-    if inv_freq is None:
-        return None, None, 0
-    if pos is None:
-        raise ValueError(f"{what}: a rotation needs positions")
-    n = inv_freq.numel()
-    return _vec(pos, tc.i32, T, what, "pos"), _vec(inv_freq, tc.f64, n, what, "inv_freq"), 2 * n
+        import torch  # noqa: F401  (its libraries have to be there first)
+        L = lib()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"qg_binding.so not found at {BINDING_PATH}; build it with "
+                               "`python -m quant_dequant_gemv_q4_b200.build`")
+        spec = importlib.util.spec_from_file_location("qg_binding", BINDING_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                 (L.qg_qk_norm_rope, L.qg_kv4_append, L.qg_kv4_read, L.qg_attn_kv4_workspace, L.qg_attn_kv4, L.qg_sample_workspace,
+                  L.qg_sample)))
+        _binding = m
+    return _binding
 
 
 def qg_kv4_bytes(pages: int, page: int, H: int, D: int) -> int:
@@ -374,87 +327,32 @@ def kv4_cache(pages: int, page: int, H: int, D: int, device=None):
 def qg_qk_norm_rope(q, k, wq, wk, eps: float, pos, inv_freq, pairing: int, q_out, k_out, stream=None) -> None:
     """Head norms (weights wq, wk fp32 [D]; None: no norm) and the rotation by pos * inv_freq (int32 [T],
     float64 [R / 2]; inv_freq None: no rotation) of q [T, Hq, D] and k [T, Hk, D] (either may be None)."""
-    what = "qg_qk_norm_rope"
-    tc = _tc or _torch()
-    some = q if q is not None else k
-    if some is None or some.dim() != 3:
-        raise ValueError(f"{what}: q or k, [tokens, heads, dims]")
-    dev = _where(tc, what, q, k, wq, wk, pos, inv_freq, q_out, k_out)
-    T, _, D = some.shape
-    vq = vk = oq = ok = None
-    Hq = Hk = 0
-    if q is not None:
-        Hq = q.shape[1]
-        if q_out is None or q_out.shape != q.shape:
-            raise ValueError(f"{what}: q and q_out are [{T}, heads, {D}]")
-        vq, oq = _view(tc, q, what, "q"), _view(tc, q_out, what, "q_out")
-    if k is not None:
-        Hk = k.shape[1]
-        if k_out is None or k_out.shape != k.shape or k.shape[0] != T or k.shape[2] != D:
-            raise ValueError(f"{what}: k and k_out are [{T}, heads, {D}]")
-        vk, ok = _view(tc, k, what, "k"), _view(tc, k_out, what, "k_out")
-    pp, pf, R = _rope(tc, pos, inv_freq, T, what)
-    rc = (_lib or lib()).qg_qk_norm_rope(vq, vk, T, Hq, Hk, D, _vec(wq, tc.f32, D, what, "wq"),
-                                         _vec(wk, tc.f32, D, what, "wk"), eps, pp, pf, R, pairing, oq, ok,
-                                         _handle(tc, stream, dev))
+    rc = (_binding or _bound()).qk_norm_rope(q, k, wq, wk, eps, pos, inv_freq, pairing, q_out, k_out, stream)
     if rc:
-        raise QgError(rc, what)
+        raise QgError(rc, "qg_qk_norm_rope")
 
 
 def qg_kv4_append(k, v, wk, eps: float, pos, inv_freq, pairing: int, slot, cache, page: int, stream=None) -> None:
     """Appends k, v [T, H, D] to the 4-bit cache at slot int64 [T] (-1: not written), the key with its head
     norm (wk None: none) and rotation (inv_freq None: none) applied on the way."""
-    what = "qg_kv4_append"
-    tc = _tc or _torch()
-    dev = _where(tc, what, k, v, wk, pos, inv_freq, slot, cache)
-    pages, H, D = _cache_sizes(tc, cache, page, what)
-    T = k.shape[0]
-    if k.shape != v.shape or k.shape[1:] != (H, D):
-        raise ValueError(f"{what}: k and v are [tokens, {H}, {D}], got {tuple(k.shape)} and {tuple(v.shape)}")
-    pp, pf, R = _rope(tc, pos, inv_freq, T, what)
-    rc = (_lib or lib()).qg_kv4_append(_view(tc, k, what, "k"), _view(tc, v, what, "v"), T, H, D,
-                                       _vec(wk, tc.f32, D, what, "wk"), eps, pp, pf, R, pairing,
-                                       _vec(slot, tc.i64, T, what, "slot"), cache.data_ptr(), pages, page,
-                                       _handle(tc, stream, dev))
+    rc = (_binding or _bound()).kv4_append(k, v, wk, eps, pos, inv_freq, pairing, slot, cache, page, stream)
     if rc:
-        raise QgError(rc, what)
+        raise QgError(rc, "qg_kv4_append")
 
 
 def qg_kv4_read(cache, page: int, slot, k_out, v_out, stream=None) -> None:
     """The values that the slots (int64 [T]) of the cache hold, into k_out and v_out [T, H, D]."""
-    what = "qg_kv4_read"
-    tc = _tc or _torch()
-    dev = _where(tc, what, cache, slot, k_out, v_out)
-    pages, H, D = _cache_sizes(tc, cache, page, what)
-    T = slot.numel()
-    if k_out.shape != (T, H, D) or v_out.shape != (T, H, D):
-        raise ValueError(f"{what}: k_out and v_out are [{T}, {H}, {D}]")
-    rc = (_lib or lib()).qg_kv4_read(cache.data_ptr(), pages, page, H, D, _vec(slot, tc.i64, T, what, "slot"), T,
-                                     _view(tc, k_out, what, "k_out"), _view(tc, v_out, what, "v_out"),
-                                     _handle(tc, stream, dev))
+    rc = (_binding or _bound()).kv4_read(cache, page, slot, k_out, v_out, stream)
     if rc:
-        raise QgError(rc, what)
-
-
-_attn_ws: dict = {}
-
-
-def _workspace_bytes(dev: int, Hq: int, Hk: int, D: int, max_q: int) -> int:
-    key = (dev, Hq, Hk, D, max_q)
-    n = _attn_ws.get(key)
-    if n is None:
-        n = int(lib().qg_attn_kv4_workspace(Hq, Hk, D, max_q))
-        if n == 0:
-            raise QgError(QG_ERR_SHAPE, "qg_attn_kv4_workspace")
-        if len(_attn_ws) >= 4096:
-            _attn_ws.clear()
-        _attn_ws[key] = n
-    return n
+        raise QgError(rc, "qg_kv4_read")
 
 
 def qg_attn_kv4_workspace(Hq: int, Hk: int, D: int, max_q: int) -> int:
     """Workspace bytes of qg_attn_kv4 on the current device."""
-    return _workspace_bytes(_torch().device(), int(Hq), int(Hk), int(D), int(max_q))
+    n = int(lib().qg_attn_kv4_workspace(int(Hq), int(Hk), int(D), int(max_q)))
+    if n == 0:
+        raise QgError(QG_ERR_SHAPE, "qg_attn_kv4_workspace")
+    return n
 
 
 def qg_attn_kv4(q, q_start, max_q: int, cache, page: int, table, kv_len, scale: float, out, workspace=None,
@@ -463,30 +361,9 @@ def qg_attn_kv4(q, q_start, max_q: int, cache, page: int, table, kv_len, scale: 
     over the 4-bit cache, sequence s having kv_len[s] places in the pages table[s], into out [T, Hq, D] (fp16).
     workspace: uint8, qg_attn_kv4_workspace(Hq, Hk, D, max_q) bytes, not shared with a call that may overlap;
     None takes one from torch's allocator for this call."""
-    what = "qg_attn_kv4"
-    tc = _tc or _torch()
-    dev = _where(tc, what, q, q_start, cache, table, kv_len, out, workspace)
-    pages, Hk, D = _cache_sizes(tc, cache, page, what)
-    if q.dtype is not tc.f16 or out.dtype is not tc.f16 or q.dim() != 3 or q.shape != out.shape or q.shape[2] != D:
-        raise ValueError(f"{what}: q and out are fp16 [tokens, heads, {D}]")
-    if table.dtype is not tc.i32 or table.dim() != 2 or not table.is_contiguous():
-        raise ValueError(f"{what}: table is contiguous int32 [sequences, pages]")
-    T, Hq, _ = q.shape
-    nseq, width = table.shape
-    st = _handle(tc, stream, dev)
-    if workspace is None:
-        if stream is not None and st != tc.stream(dev):
-            raise ValueError(f"{what}: a call on a stream that is not torch's current one needs a workspace")
-        n = _workspace_bytes(dev, Hq, Hk, D, max_q)
-        workspace = tc.empty(n, dtype=tc.u8, device=q.device)
-    else:
-        n = workspace.numel() * workspace.element_size()
-    rc = (_lib or lib()).qg_attn_kv4(_view(tc, q, what, "q"), T, nseq, _vec(q_start, tc.i32, nseq + 1, what, "q_start"),
-                                     max_q, Hq, Hk, D, cache.data_ptr(), pages, page, table.data_ptr(), width,
-                                     _vec(kv_len, tc.i32, nseq, what, "kv_len"), scale, _view(tc, out, what, "out"),
-                                     workspace.data_ptr(), n, st)
+    rc = (_binding or _bound()).attn_kv4(q, q_start, max_q, cache, page, table, kv_len, scale, out, workspace, stream)
     if rc:
-        raise QgError(rc, what)
+        raise QgError(rc, "qg_attn_kv4")
 
 
 def qg_sample_workspace(rows: int, V: int, elem_stride: int) -> int:
@@ -499,29 +376,9 @@ def qg_sample(logits, temperature, top_k, top_p, min_p, u, token, workspace=None
     temperature, top_k (int32), top_p and min_p (None: no such filter) from the random numbers u, into token
     (int32 [rows]).  workspace: uint8, qg_sample_workspace(rows, V, stride) bytes, not shared with a call that
     may overlap; None takes one from torch's allocator for this call."""
-    what = "qg_sample"
-    tc = _tc or _torch()
-    dev = _where(tc, what, logits, temperature, top_k, top_p, min_p, u, token, workspace)
-    if logits.dtype is not tc.f32 or logits.dim() != 2:
-        raise ValueError(f"{what}: logits are fp32 [rows, V]")
-    R, V = logits.shape
-    rs, es = logits.stride()
-    f32 = tc.f32
-    st = _handle(tc, stream, dev)
-    wp, wn = None, 0
-    if workspace is not None:
-        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    elif es != 1 and R > 1:
-        if stream is not None and st != tc.stream(dev):
-            raise ValueError(f"{what}: a call on a stream that is not torch's current one needs a workspace")
-        workspace = tc.empty(R * V, dtype=f32, device=logits.device)
-        wp, wn = workspace.data_ptr(), R * V * 4
-    rc = (_lib or lib()).qg_sample(logits.data_ptr(), R, V, rs, es, _vec(temperature, f32, R, what, "temperature"),
-                                   _vec(top_k, tc.i32, R, what, "top_k"), _vec(top_p, f32, R, what, "top_p"),
-                                   _vec(min_p, f32, R, what, "min_p"), _vec(u, f32, R, what, "u"),
-                                   _vec(token, tc.i32, R, what, "token"), wp, wn, st)
+    rc = (_binding or _bound()).sample(logits, temperature, top_k, top_p, min_p, u, token, workspace, stream)
     if rc:
-        raise QgError(rc, what)
+        raise QgError(rc, "qg_sample")
 
 
 def gemv(W, fmt: int, N: int, K: int, x, variant: int = QG_VARIANT_AUTO, stream=None):

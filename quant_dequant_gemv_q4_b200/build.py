@@ -1,4 +1,5 @@
-"""Build libqg.so in-tree: nvcc for sm_100a (CUDA sources) + the host packer, one shared object.
+"""Build libqg.so in-tree: nvcc for sm_100a (CUDA sources) + the host packer, one shared object; and qg_binding.so,
+the Python side of the operators that take torch tensors.
 
 Usage: python -m quant_dequant_gemv_q4_b200.build [--force]
 """
@@ -13,6 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libqg.so")
+BINDING = os.path.join(HERE, "qg_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "qg_binding.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("qg_api.cu", "qg_heads.cu", "qg_attn.cu", "qg_sample.cu", "qg_pack.cpp")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cuh", ".h"))] \
     + [os.path.join(INCLUDE, "qg.h")]
@@ -26,8 +29,31 @@ def nvcc_cmd(src: str, obj: str, extra=()) -> list[str]:
             "-c", src, "-o", obj]
 
 
+def build_binding(force: bool = False) -> str:
+    deps = [BINDING_SOURCE, os.path.join(INCLUDE, "qg.h")]
+    if force or not os.path.exists(BINDING) or any(os.path.getmtime(d) > os.path.getmtime(BINDING) for d in deps):
+        import sysconfig
+
+        import torch
+        root = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(NVCC))
+        paths = [x for p in (f"{root}/include", f"{root}/include/torch/csrc/api/include", f"{cuda}/include") for x in ("-isystem", p)]
+        tmp = BINDING + f".tmp{os.getpid()}"
+        try:
+            subprocess.check_call(["g++", "-O2", "-fPIC", "-shared", "-std=c++17", "-fvisibility=hidden",
+                                   f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+                                   "-I", sysconfig.get_paths()["include"], *paths, BINDING_SOURCE, "-o", tmp, "-L", f"{root}/lib",
+                                   "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+            os.replace(tmp, BINDING)
+        finally:
+            if os.path.exists(tmp):
+                os.remove(tmp)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """One object per source, compiled side by side, then linked."""
+    """One object per source, compiled side by side, then linked; and the binding."""
+    build_binding(force)
     stale = force or not os.path.exists(LIB) or any(
         os.path.getmtime(d) > os.path.getmtime(LIB) for d in DEPS)
     if stale:

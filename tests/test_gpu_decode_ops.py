@@ -585,6 +585,59 @@ def test_wrappers_refuse(qg):
         qg.kv4_cache(2, 24, 2, 64)
 
 
+def test_wrappers_refuse_what_the_c_abi_cannot_see(qg):
+    """Types, shapes, missing arguments and foreign streams, before anything is launched."""
+    import torch
+    x = torch.zeros(2, 2, 64, device="cuda")
+    h = x.half()
+    cache = qg.kv4_cache(2, 16, 2, 64)
+    slot = torch.zeros(2, dtype=torch.int64, device="cuda")
+    i32 = torch.zeros(2, dtype=torch.int32, device="cuda")
+    start = torch.arange(3, dtype=torch.int32, device="cuda")
+    table = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    f = torch.ones(2, device="cuda")
+    cols = torch.zeros(9, 2, device="cuda").t()
+    side = torch.cuda.Stream()
+    bad = [
+        lambda: qg.qg_kv4_append(x, None, None, 0.0, None, None, 0, slot, cache, 16),
+        lambda: qg.qg_kv4_append(x[0], x[0], None, 0.0, None, None, 0, slot, cache, 16),
+        lambda: qg.qg_kv4_append(x, x[:1], None, 0.0, None, None, 0, slot, cache, 16),
+        lambda: qg.qg_kv4_append(x, x, torch.ones(128, device="cuda")[::2], 0.0, None, None, 0, slot, cache, 16),
+        lambda: qg.qg_kv4_append(x, x, None, 0.0, i32, torch.ones(8, device="cuda"), 0, slot, cache, 16),
+        lambda: qg.qg_kv4_append(x, x, None, 0.0, i32, torch.ones(512, dtype=torch.float64, device="cuda"), 0, slot, cache, 16),
+        lambda: qg.qg_kv4_append(x, x, None, 0.0, None, None, 0, slot, cache.view(-1), 16),
+        lambda: qg.qg_kv4_append(x, x, None, 0.0, None, None, 0, slot, cache[:, :1], 16),
+        lambda: qg.qg_kv4_read(cache, 16, slot, x, x[:, :1]),
+        lambda: qg.qg_kv4_read(cache, 16, slot[:1], x, x),
+        lambda: qg.qg_qk_norm_rope(None, None, None, None, 0.0, None, None, 0, None, None),
+        lambda: qg.qg_qk_norm_rope(x, None, None, None, 0.0, None, None, 0, None, None),
+        lambda: qg.qg_qk_norm_rope(x, x[:1], None, None, 0.0, None, None, 0, x, x[:1]),
+        lambda: qg.qg_attn_kv4(h, start, 1, cache, 16, table, i32, 1.0, x),
+        lambda: qg.qg_attn_kv4(h, start[:2], 1, cache, 16, table, i32, 1.0, h),
+        lambda: qg.qg_attn_kv4(h, start, 1, cache, 16, table, slot, 1.0, h),
+        lambda: qg.qg_attn_kv4(h, start, 1, cache, 16, table.t(), i32, 1.0, h),
+        lambda: qg.qg_attn_kv4(h, start, 1 << 40, cache, 16, table, i32, 1.0, h),
+        lambda: qg.qg_attn_kv4(h, start, 1, cache, 16, table, i32, 1.0, torch.empty_like(h), stream=side),
+        lambda: qg.qg_sample(cols, None, None, None, None, f, i32, stream=side),
+        lambda: qg.qg_sample(cols, None, None, None, None, f, slot),
+        lambda: qg.qg_sample(cols.half(), None, None, None, None, f, i32),
+        lambda: qg.qg_sample(cols, None, f, None, None, f, i32),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was taken")
+    for call in (lambda: qg.qg_attn_kv4(h[:, :1], start, 1, cache, 16, table, i32, 1.0, h[:, 1:]),  # one query head of two
+                 lambda: qg.qg_qk_norm_rope(x, None, None, None, -1.0, None, None, 0, x, None)):
+        with pytest.raises(qg.QgError):
+            call()
+    for call in (lambda: qg.qg_sample(cols, None, None, None, None, f, i32, stream="x"),
+                 lambda: qg.qg_kv4_append(x, x, None, 0.0, None, None, 0, slot, cache, "16")):
+        with pytest.raises((AttributeError, TypeError)):
+            call()
+    torch.cuda.synchronize()
+
+
 # ---------------------------------------------------------------------------------------------
 # Together
 # ---------------------------------------------------------------------------------------------
