@@ -174,20 +174,28 @@ template <bool RESIDENT> struct Row {
     }
 };
 
+// What a block does once it does 32 warps wide, eight cycles an instruction: sums over a warp are single reductions
+// (of 64 bits three, by 24 bits), and prefixes come for counts and for weights apart.
+__device__ __forceinline__ unsigned warp_total(unsigned v) { return __reduce_add_sync(0xffffffffu, v); }
+__device__ __forceinline__ u64 warp_total(u64 v)
+{
+    const unsigned a = warp_total((unsigned)v & 0xffffffu), b = warp_total((unsigned)(v >> 24) & 0xffffffu), c = warp_total((unsigned)(v >> 48));
+    return ((u64)c << 48) + ((u64)b << 24) + a;
+}
+__device__ __forceinline__ float warp_total(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 template <typename T> __device__ __forceinline__ T warp_incl(T v, int lane)
 {
-#pragma unroll 1
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const T w = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += w;
     }
-    return v;
-}
-
-template <typename T> __device__ __forceinline__ T warp_total(T v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
@@ -202,28 +210,22 @@ __device__ __noinline__ u64 block_sum(Shared &s, u64 w)
     return warp_total(lane < kWarps ? s.scan_w[lane] : 0ull);
 }
 
-// Exclusive prefix over the block's threads of (c, w), and the totals.
-struct Scan {
-    u64 w_before, w_all;
-    unsigned c_before, c_all;
+// Exclusive prefix over the block's threads, and the total.
+template <typename T> struct Scan {
+    T before, all;
 };
-__device__ __noinline__ Scan block_scan(Shared &s, unsigned c, u64 w)
+template <typename T> __device__ __forceinline__ Scan<T> scan_over(T *parts, T v)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned ci = warp_incl(c, lane);
-    const u64 wi = warp_incl(w, lane);
+    const T incl = warp_incl(v, lane);
     __syncthreads();
-    if (lane == 31) {
-        s.scan_c[warp] = ci;
-        s.scan_w[warp] = wi;
-    }
+    if (lane == 31) parts[warp] = incl;
     __syncthreads();
-    const unsigned cw = warp_incl(lane < kWarps ? s.scan_c[lane] : 0u, lane);
-    const u64 ww = warp_incl(lane < kWarps ? s.scan_w[lane] : 0ull, lane);
-    const unsigned cb = __shfl_sync(0xffffffffu, cw, warp > 0 ? warp - 1 : 0);
-    const u64 wb = __shfl_sync(0xffffffffu, ww, warp > 0 ? warp - 1 : 0);
-    return {wi - w + (warp ? wb : 0), __shfl_sync(0xffffffffu, ww, 31), ci - c + (warp ? cb : 0), __shfl_sync(0xffffffffu, cw, 31)};
+    const T part = lane < kWarps ? parts[lane] : T(0);
+    return {incl - v + warp_total(lane < warp ? part : T(0)), warp_total(part)};
 }
+__device__ __noinline__ Scan<unsigned> block_scan(Shared &s, unsigned c) { return scan_over(s.scan_c, c); }
+__device__ __noinline__ Scan<u64> block_scan(Shared &s, u64 w) { return scan_over(s.scan_w, w); }
 
 // Sum of a CTA's value over the cluster: each warp fetches the CTAs' values with one load.
 template <typename T> __device__ __forceinline__ T over_cluster(cg::cluster_group &cl, Shared &s, T Shared::*field)
@@ -292,8 +294,8 @@ __device__ unsigned find_count(Shared &s, const unsigned (&c)[kPer], unsigned k)
     unsigned sum = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) sum += c[j];
-    const Scan z = block_scan(s, sum, 0);
-    unsigned cb = z.c_before;
+    const Scan<unsigned> z = block_scan(s, sum);
+    unsigned cb = z.before;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         if (cb < k && cb + c[j] >= k) {
@@ -304,7 +306,7 @@ __device__ unsigned find_count(Shared &s, const unsigned (&c)[kPer], unsigned k)
         cb += c[j];
     }
     __syncthreads();
-    return z.c_all;
+    return z.all;
 }
 
 // The bins between which the cut of top-p lies: the first whose lower bound, and the first whose upper bound,
@@ -344,13 +346,13 @@ __device__ void find_share(Shared &s, const unsigned (&c)[kPer], const unsigned 
     }
     float after_h = __shfl_down_sync(0xffffffffu, hs, 1), after_l = __shfl_down_sync(0xffffffffu, ls, 1);
     if (lane == 31) after_h = after_l = 0.0f;
-    const Scan z = block_scan(s, sum, 0);
-    unsigned cb = z.c_before;
+    const Scan<unsigned> z = block_scan(s, sum);
+    unsigned cb = z.before;
     if (threadIdx.x == 0) {  // (should rounding hide a border from both of its threads: all bins)
         s.bin[0] = 0;
         s.before[0] = 0;
         s.bin[1] = kBins - 1;
-        s.before[1] = z.c_all;
+        s.before[1] = z.all;
     }
     const bool later = lane > warp && lane < kWarps;
     after_h += warp_total(later ? s.scan_f[0][lane] : 0.0f);
@@ -595,24 +597,24 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                     if (whole) {
                         if (k) keep = keep && (unsigned)tid < k;
                         if (by_p) {
-                            const Scan z = block_scan(s, 0, keep ? w : 0);
-                            keep = keep && (tid == 0 || (double)z.w_before < p * (double)(share ? all_w : z.w_all));
+                            const Scan<u64> z = block_scan(s, keep ? w : 0ull);
+                            keep = keep && (tid == 0 || (double)z.before < p * (double)(share ? all_w : z.all));
                         }
                         if (mp > 0.0) keep = keep && r.at_least(of_key(key), w, mp);
                         // the kept tokens by their index, lowest first
                         const int kept = __syncthreads_count(keep);
                         const u64 f = block_sort(keep ? e << 32 | key : 0, s.list, kept);
                         const u64 fw = tid < kept ? r.weight(of_key((unsigned)f)) : 0;
-                        const Scan z = block_scan(s, 0, fw);
-                        const double target = u * (double)z.w_all;
-                        const u64 upto = z.w_before + fw;
-                        const bool last = !((double)z.w_all > target);  // u of 1 or more, or NaN: the last kept token
-                        if (fw && (last ? upto == z.w_all : (double)upto > target && !((double)z.w_before > target)))
+                        const Scan<u64> z = block_scan(s, fw);
+                        const double target = u * (double)z.all;
+                        const u64 upto = z.before + fw;
+                        const bool last = !((double)z.all > target);  // u of 1 or more, or NaN: the last kept token
+                        if (fw && (last ? upto == z.all : (double)upto > target && !((double)z.before > target)))
                             a.token[row] = (int32_t)(0xffffffffu - (unsigned)(f >> 32));
                     } else {
                         if (share) {
-                            const Scan z = block_scan(s, 0, w);
-                            keep = keep && (double)(above + z.w_before) < p * (double)all_w;
+                            const Scan<u64> z = block_scan(s, w);
+                            keep = keep && (double)(above + z.before) < p * (double)all_w;
                         } else {
                             keep = keep && before + tid < k;
                         }
@@ -675,9 +677,8 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                         fc += o->count[tid];
                         fw += o->own[tid];
                     }
-                    const Scan z = block_scan(s, fc, fw);
-                    const unsigned cb = z.c_before;
-                    const u64 wb = z.w_before;
+                    const unsigned cb = block_scan(s, fc).before;
+                    const u64 wb = block_scan(s, fw).before;
                     const bool here = share ? fc && (double)(done_w + wb) < target && !((double)(done_w + wb + fw) < target)
                                             : done_c + cb < k && done_c + cb + fc >= k;
                     if (here) {
@@ -733,10 +734,11 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                         in += r.bin(x) == bc;
                     }
                 });
-                const Scan z = block_scan(s, in, w);
+                const unsigned in_all = block_scan(s, in).all;
+                w = block_sum(s, w);
                 if (tid == 0) {
-                    s.cta_weight = z.w_all;
-                    s.cta_ties = z.c_all;
+                    s.cta_weight = w;
+                    s.cta_ties = in_all;
                 }
                 cl.sync();
                 const unsigned extra = cut_ties == kAll ? 0 : cut_ties;
@@ -757,9 +759,9 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
     if (cut_ties != kAll) {  // which of the tokens equal to the cut are kept depends on those before them
         unsigned ties = 0;
         for (int i = i0; i < i1; ++i) ties += key_of(r.get(i)) == cut_key;
-        const Scan z = block_scan(s, ties, 0);
-        ties_before = z.c_before;
-        if (tid == 0) s.cta_ties = z.c_all;
+        const Scan<unsigned> z = block_scan(s, ties);
+        ties_before = z.before;
+        if (tid == 0) s.cta_ties = z.all;
         cl.sync();
         for (int q = 0; q < rank; ++q) ties_before += cl.map_shared_rank(&s, q)->cta_ties;
     }
@@ -788,11 +790,11 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
             seen += key_of(x) == cut_key;
         }
     }
-    const Scan z = block_scan(s, 0, mine);
-    if (tid == 0) s.cta_weight = z.w_all;
+    const Scan<u64> z = block_scan(s, mine);
+    if (tid == 0) s.cta_weight = z.all;
     cl.sync();
     const u64 theirs = lane < C ? cl.map_shared_rank(&s, lane)->cta_weight : 0;
-    const u64 before = z.w_before + warp_total(lane < rank ? theirs : 0), all_w = warp_total(theirs);
+    const u64 before = z.before + warp_total(lane < rank ? theirs : 0ull), all_w = warp_total(theirs);
     const double target = u * (double)all_w;
     const bool last = !((double)all_w > target);  // u of 1 or more, or NaN: the last kept token
     const bool here = mine && (last ? before + mine == all_w : (double)(before + mine) > target && !((double)before > target));
