@@ -16,8 +16,9 @@
 //      are within a factor 2^(1/64) of each other, the weight below a bin is bounded on both sides by the
 //      counts, which leaves two or three bins.  If the tokens down to the last of these are at most kList,
 //      they are gathered in one CTA, sorted, filtered and chosen from;
-//   4. otherwise only the tokens of those bins are gathered and sorted (or, should they be too many, counted in
-//      finer and finer bins), together with the exact weight above them, which gives the cut;
+//   4. otherwise only the tokens of those bins are gathered, narrowed down to the cut's neighbours and sorted (or,
+//      should they be too many, counted in finer and finer bins), together with the exact weight above them, which
+//      gives the cut;
 //   5. the token is found from the running sums in index order: from those of 4, a thread's consecutive logits each,
 //      and the listed tokens above the cut, or by another pass where that does not do (min-p, ties at the cut).
 //
@@ -27,9 +28,9 @@
 // that of the exact formula but for u (or a filter's border) within about 1e-9 of a border.  64-bit
 // exponentials instead (exact to 2^-45) took 113 cycles of a scheduler for 32 of them.
 //
-// What bounds it is the chain of stages, most of them short and run once: about 60,000 cycles for a row of 151936
-// (38 us; its bytes would take 0.1), of which the passes over the row are 10,000, a sort of the cut's tokens 7,000 to
-// 20,000, and the rest barriers of the cluster and the block, and code that no cache holds yet.
+// What bounds it is the chain of stages, most of them short and run once, 32 warps wide: about 55,000 cycles for a row
+// of 151936 (32 us; its bytes would take 0.1), of which the passes over the row are 12,000, the list's sorts 4,000 to
+// 9,000, and the rest sums and barriers of the block and the cluster, and code that no cache holds yet.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -51,6 +52,7 @@ constexpr int kPer = kBins / kThreads;  // bins of a thread
 constexpr float kBinStep = 0.98922801319397548f;  // 2^(-1/64)
 constexpr float kDeepest = 45.9f;  // below 2^-45.9 of the largest a weight is 0
 constexpr int kList = kThreads;
+constexpr int kSortAtOnce = 128;  // (a sort of 1024 took 19,600 cycles, narrowing them down 3,000)
 constexpr double kOne = 17592186044416.0;  // the largest weight, 2^44
 typedef unsigned long long u64;
 constexpr int64_t kMostLogits = (1 << 20) - 1;  // so many weights of 2^44 fit 64 bits
@@ -378,6 +380,50 @@ __device__ void find_share(Shared &s, const unsigned (&c)[kPer], const unsigned 
     __syncthreads();
 }
 
+// Of the m listed tokens, those next to a share's cut: their weights are added up over finer bins of their keys, and
+// the tokens of the bin in which the running weight (with `above` before them) reaches the target are left in the
+// list.  All of them are, should no bin do that.
+struct Left {
+    int tokens;
+    u64 above;
+};
+template <bool RESIDENT> __device__ __noinline__ Left narrow(Shared &s, const Row<RESIDENT> &r, int m, u64 above, double target)
+{
+    u64 *bins = reinterpret_cast<u64 *>(s.count);  // (the histogram has been read)
+    const int tid = threadIdx.x;
+    const bool mine = tid < m;
+    const u64 e = mine ? s.list[tid] : 0;
+    const unsigned key = (unsigned)(e >> 32);
+    const unsigned lo = __reduce_min_sync(0xffffffffu, mine ? key : 0xffffffffu), hi = __reduce_max_sync(0xffffffffu, key);
+    if ((tid & 31) == 0) {
+        atomicMin(&s.klo, lo);
+        atomicMax(&s.khi, hi);
+    }
+    bins[tid] = 0;
+    if (tid == 0) {
+        s.bin[0] = -1;
+        s.in_bin = 0;
+    }
+    __syncthreads();
+    const unsigned top = s.khi, range = top - s.klo;
+    const int shift = range >= (unsigned)kThreads ? 22 - __clz(range) : 0;
+    const int b = mine ? (int)((top - key) >> shift) : -1;
+    if (mine) atomicAdd(&bins[b], r.weight(of_key(key)));
+    __syncthreads();
+    const u64 w = bins[tid];
+    const u64 before = above + block_scan(s, w).before;
+    if ((double)before < target && !((double)(before + w) < target)) {
+        s.bin[0] = tid;
+        s.fine_before = before;
+    }
+    __syncthreads();
+    const int cut = s.bin[0];
+    if (cut < 0) return {m, above};
+    if (b == cut) s.list[atomicAdd(&s.in_bin, 1u)] = e;
+    __syncthreads();
+    return {(int)s.in_bin, s.fine_before};
+}
+
 template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
 {
     extern __shared__ __align__(16) uint8_t dyn[];
@@ -588,7 +634,12 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                         above = over_cluster(cl, s, &Shared::cta_weight);
                         if (!k) all_w = over_cluster(cl, s, &Shared::cta_total);
                     }
-                    const int m = (int)min(s.listed, (unsigned)kList);
+                    int m = (int)min(s.listed, (unsigned)kList);
+                    if (share && !whole && m > kSortAtOnce) {
+                        const Left left = narrow(s, r, m, above, p * (double)all_w);
+                        m = left.tokens;
+                        above = left.above;
+                    }
                     const bool mine = tid < m;
                     const u64 e = block_sort(mine ? s.list[tid] : 0, s.list, m);
                     const unsigned key = (unsigned)(e >> 32);
