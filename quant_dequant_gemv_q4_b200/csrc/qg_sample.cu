@@ -14,11 +14,10 @@
 //   2. a histogram of counts over bins linear in z, 64 a factor of two, and (for top-p) the weights' sum in fp32;
 //   3. the bins in which the cut lies: exactly known for the k-th token; for top-p, since a bin's weights
 //      are within a factor 2^(1/64) of each other, the weight below a bin is bounded on both sides by the
-//      counts, which leaves two or three bins.  If the tokens down to the last of these are at most kList,
+//      counts, which leaves two or three bins.  If the tokens down to the last of these are at most 1024,
 //      they are gathered in one CTA, sorted, filtered and chosen from;
-//   4. otherwise only the tokens of those bins are gathered, narrowed down to the cut's neighbours and sorted (or,
-//      should they be too many, counted in finer and finer bins), together with the exact weight above them, which
-//      gives the cut;
+//   4. otherwise only the tokens of those bins are gathered, and counted (or weighed) in finer and finer bins, with
+//      the exact weight above them, which gives the cut (should they be too many for a list, over the row itself);
 //   5. the token is found from the running sums in index order: from those of 4, a thread's consecutive logits each,
 //      and the listed tokens above the cut, or by another pass where that does not do (min-p, ties at the cut).
 //
@@ -51,8 +50,7 @@ constexpr int kBins = 4096;
 constexpr int kPer = kBins / kThreads;  // bins of a thread
 constexpr float kBinStep = 0.98922801319397548f;  // 2^(-1/64)
 constexpr float kDeepest = 45.9f;  // below 2^-45.9 of the largest a weight is 0
-constexpr int kList = kThreads;
-constexpr int kSortAtOnce = 128;  // (a sort of 1024 took 19,600 cycles, narrowing them down 3,000)
+constexpr int kList = 2 * kThreads;
 constexpr double kOne = 17592186044416.0;  // the largest weight, 2^44
 typedef unsigned long long u64;
 constexpr int64_t kMostLogits = (1 << 20) - 1;  // so many weights of 2^44 fit 64 bits
@@ -380,48 +378,81 @@ __device__ void find_share(Shared &s, const unsigned (&c)[kPer], const unsigned 
     __syncthreads();
 }
 
-// Of the m listed tokens, those next to a share's cut: their weights are added up over finer bins of their keys, and
-// the tokens of the bin in which the running weight (with `above` before them) reaches the target are left in the
-// list.  All of them are, should no bin do that.
-struct Left {
-    int tokens;
-    u64 above;
-};
-template <bool RESIDENT> __device__ __noinline__ Left narrow(Shared &s, const Row<RESIDENT> &r, int m, u64 above, double target)
+// The cut of a share among the m listed tokens, with `above` before them: s.cut_key and s.cut_ties (all: kAll).
+// Their weights are added up over finer and finer bins of their keys (a sort of 1024 took 19,600 cycles, a round of
+// this takes 3,000, and there are two or three), until the bin in which the running weight reaches the target has
+// one key.
+constexpr unsigned kAll = 0xffffffffu;
+template <bool RESIDENT> __device__ __noinline__ void cut_of_list(Shared &s, const Row<RESIDENT> &r, int m, u64 above, double target)
 {
     u64 *bins = reinterpret_cast<u64 *>(s.count);  // (the histogram has been read)
     const int tid = threadIdx.x;
-    const bool mine = tid < m;
-    const u64 e = mine ? s.list[tid] : 0;
-    const unsigned key = (unsigned)(e >> 32);
-    const unsigned lo = __reduce_min_sync(0xffffffffu, mine ? key : 0xffffffffu), hi = __reduce_max_sync(0xffffffffu, key);
+    unsigned key[kList / kThreads], lo = 0xffffffffu, hi = 0;
+#pragma unroll
+    for (int j = 0; j < kList / kThreads; ++j) {
+        const int at = tid + j * kThreads;
+        key[j] = at < m ? (unsigned)(s.list[at] >> 32) : 0;  // (no token has key 0)
+        if (key[j]) {
+            lo = min(lo, key[j]);
+            hi = max(hi, key[j]);
+        }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
     if ((tid & 31) == 0) {
         atomicMin(&s.klo, lo);
         atomicMax(&s.khi, hi);
     }
-    bins[tid] = 0;
-    if (tid == 0) {
-        s.bin[0] = -1;
-        s.in_bin = 0;
+    __syncthreads();
+    lo = s.klo;
+    hi = s.khi;
+    for (;;) {
+        const int shift = hi - lo >= (unsigned)kThreads ? 22 - __clz(hi - lo) : 0;
+        bins[tid] = 0;
+        if (tid == 0) s.bin[0] = -1;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kList / kThreads; ++j)
+            if (key[j] >= lo && key[j] <= hi) {
+                const u64 w = r.weight(of_key(key[j]));
+                if (w) atomicAdd(&bins[(hi - key[j]) >> shift], w);
+            }
+        __syncthreads();
+        const u64 w = bins[tid];
+        const Scan<u64> z = block_scan(s, w);
+        if (w && (double)(above + z.before) < target && !((double)(above + z.before + w) < target)) {
+            s.bin[0] = tid;
+            s.fine_before = z.before;
+        }
+        __syncthreads();
+        const int b = s.bin[0];
+        if (b < 0) {  // (in the first round only) none of the list is kept, or all of it
+            if (tid == 0) {
+                s.cut_key = (double)above < target ? lo : hi;
+                s.cut_ties = (double)above < target ? kAll : above ? 0 : 1;  // (p of 0: the first token alone)
+            }
+            break;
+        }
+        above += s.fine_before;
+        hi -= (unsigned)b << shift;
+        const unsigned width = (1u << shift) - 1;
+        lo = hi - lo < width ? lo : hi - width;
+        if (lo == hi) {
+            // the fewest ties whose weight reaches the target
+            unsigned n = 0;
+#pragma unroll
+            for (int j = 0; j < kList / kThreads; ++j) n += key[j] == lo;
+            const unsigned equal = block_scan(s, n).all;
+            if (tid == 0) {
+                const double need = ceil((target - (double)above) / (double)r.weight(of_key(lo)));
+                s.cut_key = lo;
+                s.cut_ties = need < (double)equal ? (need < 1.0 ? 1u : (unsigned)need) : kAll;  // (all: no need to count them)
+            }
+            break;
+        }
+        __syncthreads();  // (the bins have been read)
     }
     __syncthreads();
-    const unsigned top = s.khi, range = top - s.klo;
-    const int shift = range >= (unsigned)kThreads ? 22 - __clz(range) : 0;
-    const int b = mine ? (int)((top - key) >> shift) : -1;
-    if (mine) atomicAdd(&bins[b], r.weight(of_key(key)));
-    __syncthreads();
-    const u64 w = bins[tid];
-    const u64 before = above + block_scan(s, w).before;
-    if ((double)before < target && !((double)(before + w) < target)) {
-        s.bin[0] = tid;
-        s.fine_before = before;
-    }
-    __syncthreads();
-    const int cut = s.bin[0];
-    if (cut < 0) return {m, above};
-    if (b == cut) s.list[atomicAdd(&s.in_bin, 1u)] = e;
-    __syncthreads();
-    return {(int)s.in_bin, s.fine_before};
 }
 
 template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
@@ -527,7 +558,6 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
     r.cl = (float)(r.c - (double)r.ch);
 
     // kept: the tokens above cut_key, and the first cut_ties equal to it
-    constexpr unsigned kAll = 0xffffffffu;
     // the logits of a thread where order counts: consecutive, an odd number of them, so that the threads' reads fall
     // in different banks
     const int seg = ((n + kThreads - 1) / kThreads) | 1;
@@ -582,9 +612,9 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                 before = s.before[0];
                 reach = before + s.in_bin;
             }
-            const bool whole = reach <= kList;  // all that can be kept fits a list
+            const bool whole = reach <= kThreads;  // all that can be kept is a list that can be sorted
             const int b0 = whole ? 0 : min(s.bin[0], s.bin[1]), b1 = s.bin[1];
-            const bool listable = whole || reach - before <= kList;
+            const bool listable = whole || reach - before <= (unsigned)(share ? kList : kThreads);
             Shared *first = cl.map_shared_rank(&s, 0);
             // The tokens of those bins: into the list, or their least and largest key; for a share also the weight of
             // those above them and (after a cut by the count it is known, and the tokens below that are not in it)
@@ -627,55 +657,50 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                 const unsigned found = min(s.own_listed, (unsigned)kList);
                 if (tid == 0) s.own_at = found ? atomicAdd(&first->listed, found) : 0;
                 __syncthreads();
-                if (tid < found && s.own_at + tid < kList) first->list[s.own_at + tid] = s.own[tid];
+                for (unsigned e = tid; e < found; e += kThreads)
+                    if (s.own_at + e < kList) first->list[s.own_at + e] = s.own[e];
                 cl.sync();
                 if (rank == 0) {
                     if (weigh) {
                         above = over_cluster(cl, s, &Shared::cta_weight);
                         if (!k) all_w = over_cluster(cl, s, &Shared::cta_total);
                     }
-                    int m = (int)min(s.listed, (unsigned)kList);
-                    if (share && !whole && m > kSortAtOnce) {
-                        const Left left = narrow(s, r, m, above, p * (double)all_w);
-                        m = left.tokens;
-                        above = left.above;
-                    }
-                    const bool mine = tid < m;
-                    const u64 e = block_sort(mine ? s.list[tid] : 0, s.list, m);
-                    const unsigned key = (unsigned)(e >> 32);
-                    const u64 w = mine ? r.weight(of_key(key)) : 0;
-                    bool keep = mine;
-                    if (whole) {
-                        if (k) keep = keep && (unsigned)tid < k;
-                        if (by_p) {
-                            const Scan<u64> z = block_scan(s, keep ? w : 0ull);
-                            keep = keep && (tid == 0 || (double)z.before < p * (double)(share ? all_w : z.all));
-                        }
-                        if (mp > 0.0) keep = keep && r.at_least(of_key(key), w, mp);
-                        // the kept tokens by their index, lowest first
-                        const int kept = __syncthreads_count(keep);
-                        const u64 f = block_sort(keep ? e << 32 | key : 0, s.list, kept);
-                        const u64 fw = tid < kept ? r.weight(of_key((unsigned)f)) : 0;
-                        const Scan<u64> z = block_scan(s, fw);
-                        const double target = u * (double)z.all;
-                        const u64 upto = z.before + fw;
-                        const bool last = !((double)z.all > target);  // u of 1 or more, or NaN: the last kept token
-                        if (fw && (last ? upto == z.all : (double)upto > target && !((double)z.before > target)))
-                            a.token[row] = (int32_t)(0xffffffffu - (unsigned)(f >> 32));
+                    const int m = (int)min(s.listed, (unsigned)kList);
+                    if (share && !whole) {
+                        cut_of_list(s, r, m, above, p * (double)all_w);
                     } else {
-                        if (share) {
-                            const Scan<u64> z = block_scan(s, w);
-                            keep = keep && (double)(above + z.before) < p * (double)all_w;
+                        const bool mine = tid < m;
+                        const u64 e = block_sort(mine ? s.list[tid] : 0, s.list, m);
+                        const unsigned key = (unsigned)(e >> 32);
+                        const u64 w = mine ? r.weight(of_key(key)) : 0;
+                        bool keep = mine;
+                        if (whole) {
+                            if (k) keep = keep && (unsigned)tid < k;
+                            if (by_p) {
+                                const Scan<u64> z = block_scan(s, keep ? w : 0ull);
+                                keep = keep && (tid == 0 || (double)z.before < p * (double)(share ? all_w : z.all));
+                            }
+                            if (mp > 0.0) keep = keep && r.at_least(of_key(key), w, mp);
+                            // the kept tokens by their index, lowest first
+                            const int kept = __syncthreads_count(keep);
+                            const u64 f = block_sort(keep ? e << 32 | key : 0, s.list, kept);
+                            const u64 fw = tid < kept ? r.weight(of_key((unsigned)f)) : 0;
+                            const Scan<u64> z = block_scan(s, fw);
+                            const double target = u * (double)z.all;
+                            const u64 upto = z.before + fw;
+                            const bool last = !((double)z.all > target);  // u of 1 or more, or NaN: the last kept token
+                            if (fw && (last ? upto == z.all : (double)upto > target && !((double)z.before > target)))
+                                a.token[row] = (int32_t)(0xffffffffu - (unsigned)(f >> 32));
                         } else {
                             keep = keep && before + tid < k;
+                            const int kept = __syncthreads_count(keep);
+                            // the last kept one and how many equal to it are kept (none: the cut is above the list)
+                            if (tid == (kept ? kept - 1 : 0)) s.cut_key = key;
+                            __syncthreads();
+                            const unsigned ties = __syncthreads_count(keep && key == s.cut_key);
+                            const unsigned equal = __syncthreads_count(mine && key == s.cut_key);
+                            if (tid == 0) s.cut_ties = ties == equal ? kAll : ties;
                         }
-                        const int kept = __syncthreads_count(keep);
-                        // the last kept one and how many equal to it are kept (none: the cut is above the list)
-                        if (tid == (kept ? kept - 1 : 0)) s.cut_key = key;
-                        __syncthreads();
-                        const unsigned ties = __syncthreads_count(keep && key == s.cut_key);
-                        const unsigned equal = __syncthreads_count(mine && key == s.cut_key);
-                        if (tid == 0) s.cut_ties = ties == equal ? kAll : ties;  // (all: no need to count them)
                     }
                 }
                 cl.sync();
@@ -828,9 +853,11 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
     if (listed) {
         s.list[tid] = 0;
         __syncthreads();
-        const u64 e = tid < s.own_listed ? s.own[tid] : 0;
-        if ((unsigned)(e >> 32) >= cut_key)
-            atomicAdd(&s.list[(unsigned)(0xffffffffu - (unsigned)e - base) / (unsigned)seg], r.weight(of_key((unsigned)(e >> 32))));
+        for (unsigned at = tid; at < s.own_listed; at += kThreads) {
+            const u64 e = s.own[at];
+            if ((unsigned)(e >> 32) >= cut_key)
+                atomicAdd(&s.list[(unsigned)(0xffffffffu - (unsigned)e - base) / (unsigned)seg], r.weight(of_key((unsigned)(e >> 32))));
+        }
         __syncthreads();
         mine = above_mine + s.list[tid];
     } else {
@@ -943,11 +970,12 @@ int look_at_card(Card *out)
     return QG_OK;
 }
 
-// CTAs of a row's cluster.  A row takes about as long as 35000 logits of a CTA and then its CTAs' share (of a share
-// that does not fit the shared memory 2.4 times as long); rows that find no room side by side wait.  Shares are not cut
-// below 8192 logits.  Top-p of one row of 151936 took 45 us with 8 CTAs, 37 with 16; of 8 rows, 46 with 8 and 74 with
-// 16, of which seven find room; of 16 rows 228, 130, 64, 52 and 83 us with 1, 2, 4, 6 and 8; of 64 rows of 50257 90, 46,
-// 68 and 139 us with 1, 2, 4 and 8; of 16 rows of 248320 156, 82 and 115 us with 4 (not resident), 6 and 8.
+// CTAs of a row's cluster.  A row takes about as long as 41000 logits of a CTA, 700 for each CTA of the cluster and then
+// a CTA's share (of a share that does not fit the shared memory 1.7 times as long; 1000 logits take 0.5 us); rows that
+// find no room side by side wait.  Shares are not cut below 8192 logits.  Top-p of one row of 151936 took 142, 85, 41,
+// 34, 31 and 32 us with 1, 2, 4, 6, 8 and 16 CTAs (the first two not resident); of 8 rows 41, 45, 33 and 62 with 4, 6, 8
+// and 16; of 16 rows 42, 36, 62 and 93; of 64 rows of 50257 63, 34, 54 and 122 with 1, 2, 4 and 8; of 4 rows of 32000 35,
+// 28, 24, 23 and 27 with 1, 2, 4, 8 and 16.
 int cluster_of(const Card &card, int64_t rows, int64_t V)
 {
     int best = 1;
@@ -956,7 +984,7 @@ int cluster_of(const Card &card, int64_t rows, int64_t V)
         const int64_t side = card.side_by_side[C], per = (V + C - 1) / C;
         if (side < 1) continue;
         const bool resident = per <= (card.optin - (int)sizeof(Shared)) / 4;
-        const double cost = (double)((rows + side - 1) / side) * (35000.0 + (double)per * (resident ? 1.0 : 2.4));
+        const double cost = (double)((rows + side - 1) / side) * (41000.0 + 700.0 * C + (double)per * (resident ? 1.0 : 1.7));
         if (C == 1 || cost < least) {
             best = C;
             least = cost;

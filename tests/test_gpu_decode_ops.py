@@ -420,6 +420,20 @@ def test_sample_ties(qg, V):
         check_sample(qg, x, u=u, **kw)
 
 
+@pytest.mark.parametrize("equal", [1000, 1500, 2500])
+def test_sample_many_equal_at_the_top(qg, equal):
+    """The cut among so many equal logits that a list holds them, just so, or does not."""
+    rng = np.random.default_rng(equal)
+    R, V = 10, 9000
+    x = rng.normal(size=(R, V)).astype("f4")
+    for i in range(R):
+        x[i, rng.permutation(V)[:equal]] = 5.0 if i % 2 else x[i].max() - 1.0
+    u = rng.random(R)
+    p = np.array([0.0, 0.0, 1e-9, 1e-9, 0.2, 0.2, 0.5, 0.5, 0.97, 0.97])
+    for kw in (dict(p=p), dict(p=p, k=np.full(R, 1300)), dict(p=p, mp=np.full(R, 0.3)), dict(k=np.full(R, equal - 3))):
+        check_sample(qg, x, u=u, **kw)
+
+
 def test_sample_masked_rows_and_odd_settings(qg):
     rng = np.random.default_rng(5)
     V = 9000
