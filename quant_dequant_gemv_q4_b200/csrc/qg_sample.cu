@@ -482,7 +482,7 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
     const float t = a.temperature ? a.temperature[row] : 1.0f;
     const int64_t k_arg = a.top_k ? a.top_k[row] : 0;
     const double p_arg = a.top_p ? (double)a.top_p[row] : 1.0;
-    const double mp = a.min_p ? (double)a.min_p[row] : 0.0;
+    double mp = a.min_p ? (double)a.min_p[row] : 0.0;
     const double u = a.u[row] < 0.0f ? 0.0 : (double)a.u[row];
     const float *x = a.x + row * a.rs + base * a.es;
     float top = -INFINITY;
@@ -530,7 +530,7 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
     if (infinite) top = 0.0f;
     Row<RESIDENT> r{x, a.es, slice, s.table, infinite, n, top, 0.0, 0.0, 0.0f, 0.0f};
 
-    if (!(t > 0.0f) || k == 1) {
+    if (!(t > 0.0f) || k == 1 || mp > 1.0) {
         // the lowest index of the largest logit
         int64_t best = INT64_MAX;
         for (int i = tid; i < n && best == INT64_MAX; i += kThreads)
@@ -595,6 +595,13 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                 find_share(s, c, kept_c, k ? (float)((1.0 - p) * (double)all_w * (1.0 / kOne)) : tail);
                 before = s.before[0];
                 reach = s.before[1];
+                if (mp > 0.0) {
+                    // A token of weight min_p lies within a bin of `least`: where the share's cut is deeper than that, it
+                    // changes nothing, and where it is higher, min-p does not.
+                    const int least = (int)(-64.0f * log2f((float)mp));
+                    if (min(s.bin[0], s.bin[1]) > least + 1) break;
+                    if (max(s.bin[0], s.bin[1]) < least - 1) mp = 0.0;
+                }
             } else {
                 if (find_count(s, c, k) < k) {
                     // fewer than k: no cut by the count

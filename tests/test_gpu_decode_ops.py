@@ -434,6 +434,29 @@ def test_sample_many_equal_at_the_top(qg, equal):
         check_sample(qg, x, u=u, **kw)
 
 
+@pytest.mark.parametrize("V", [700, 50257])
+def test_sample_share_against_min_p(qg, V):
+    """Either of top-p and min-p may be the one that cuts, far from the other's cut or next to it."""
+    rng = np.random.default_rng(V)
+    R = 24
+    x = (rng.normal(size=(R, V)) * 2).astype("f4")
+    u = rng.random(R)
+    p = rng.uniform(0.05, 0.999, R)
+    for least in (1e-30, 1e-4, 0.02, 0.3, 1.0, 1.5):
+        mp = least * rng.uniform(0.7, 1.0, R) if least < 1 else np.full(R, least)
+        check_sample(qg, x, u=u, p=p, mp=mp)
+        check_sample(qg, x, u=u, p=p, mp=mp, k=rng.integers(1, 3 * V // 2, R))
+    # min_p next to the weight of the last token that top-p keeps
+    z = np.sort(x.astype(np.float64), 1)[:, ::-1]
+    w = np.exp(z - z[:, :1])
+    n = (np.cumsum(w, 1) - w < p[:, None] * w.sum(1, keepdims=True)).sum(1)
+    edge = w[np.arange(R), n - 1]
+    for f in (0.97, 0.999, 1.001, 1.03):
+        check_sample(qg, x, u=u, p=p, mp=np.minimum(edge * f, 1.0))
+    x[:, ::7] = x.max()  # equal logits at the top: only the first is never dropped
+    check_sample(qg, x, u=u, mp=np.full(R, 1.25), p=p)
+
+
 def test_sample_masked_rows_and_odd_settings(qg):
     rng = np.random.default_rng(5)
     V = 9000
