@@ -63,6 +63,7 @@ constexpr float kMoveMax = 8.0f;                // a score this far above the re
 constexpr float kWeightShift = 7.0f;
 constexpr int kHoleBar = 10;                    // named barriers 10, 11: the value warpgroups
 constexpr int kMetas = 16;                      // tiles whose description is kept (more than any role lags)
+constexpr int64_t kNoRow = INT64_MIN;           // no row of q or out (offsets of rows are negative where strides are)
 
 // flags of a tile
 constexpr int kFirst = 1;      // first of this CTA's part of its item
@@ -237,8 +238,8 @@ template <int N> struct Small {
     int dead, produced;  // produced: tiles described so far
     alignas(16) float base[N];    // reference - kWeightShift
     alignas(16) int lim[2][N];    // last place that a row sees (of the parts of items in turn)
-    int64_t orow[2][N];           // where a row of out starts, -1: no such row
-    int64_t qrow[N];
+    int64_t orow[2][N];           // where a row of out starts, or kNoRow
+    int64_t qrow[N];              // ... and of q
     float ref[N];
     float wred[4][N];             // by warp of the warpgroup
     float inv[N];
@@ -785,8 +786,8 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                 const bool ok = tok < m.n;
                 const int64_t tt = m.first + tok, hh = m.head * a.G + (int)(row - (uint32_t)tok * (uint32_t)a.G);
                 sm.lim[which & 1][n0 + t] = ok ? m.len - m.n + tok : -1;
-                sm.orow[which & 1][n0 + t] = ok ? tt * a.out.st + hh * a.out.sh : -1;
-                sm.qrow[n0 + t] = ok ? tt * a.q.st + hh * a.q.sh : -1;
+                sm.orow[which & 1][n0 + t] = ok ? tt * a.out.st + hh * a.out.sh : kNoRow;
+                sm.qrow[n0 + t] = ok ? tt * a.q.st + hh * a.q.sh : kNoRow;
             }
             bar_sync(bar_id, 128);
             constexpr int kBatch = NS * kVec / 128 < 4 ? NS * kVec / 128 : 4;
@@ -799,7 +800,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                     const int n = n0 + (x >> 1) % NS, g = 2 * (x / (2 * NS)) + (x & 1);  // two pieces of a row side by side
                     const int64_t at = sm.qrow[n];
                     v[y][0] = v[y][1] = v[y][2] = v[y][3] = 0;
-                    if (at >= 0) {
+                    if (at != kNoRow) {
                         const __half *qp = static_cast<const __half *>(a.q.p) + at;
                         if (a.q.vec > 1) {
                             const uint4 u = *reinterpret_cast<const uint4 *>(qp + 8 * g);
@@ -988,7 +989,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                         const int64_t at = sm.orow[seg & 1][n0 + c + e];
                         const float4 v0 = *reinterpret_cast<const float4 *>(stage + e * C::kOutStride + 8 * g);
                         const float4 v1 = *reinterpret_cast<const float4 *>(stage + e * C::kOutStride + 8 * g + 4);
-                        if (at < 0) continue;
+                        if (at == kNoRow) continue;
                         if (!complete) {
                             float *dst = a.part + ((int64_t)slot * N + n0 + c + e) * D + 8 * g;
                             *reinterpret_cast<float4 *>(dst) = v0;

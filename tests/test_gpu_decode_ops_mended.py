@@ -1,0 +1,71 @@
+"""The operators between the GEMVs where they had gone wrong, or were not compared with anything: views that run
+backwards, many tokens, wrong guesses of max_q, sizes at the ends of their ranges."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import kv4_ref as ref
+from test_gpu_decode_ops import attention_case, check_attention, dev, frequencies, layout, qg, run_attention  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------------------------
+# Views with negative strides, which torch has not, through the C ABI
+# ---------------------------------------------------------------------------------------------
+def backwards(qg, t, tokens, heads):
+    """A contiguous [T, H, D] tensor as the view whose tokens and / or heads run from the last to the first."""
+    T, H, D = t.shape
+    at = t.data_ptr() + t.element_size() * D * ((T - 1) * H * tokens + (H - 1) * heads)
+    kind = qg.QG_TYPE_F32 if t.element_size() == 4 else qg.QG_TYPE_F16
+    return ctypes.byref(qg.qg_heads(at, -H * D if tokens else H * D, -D if heads else D, 1, kind))
+
+
+@pytest.mark.parametrize("lens,nq", [([90, 20], [1, 3]), ([5000], 2), ([700, 300], [40, 9])])  # whole items; cut ones
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("tokens,heads", [(1, 0), (0, 1), (1, 1)])
+def test_attention_of_views_that_run_backwards(qg, lens, nq, D, tokens, heads):
+    """The result is that of the same values in order, and goes where the view says."""
+    import torch
+    c = attention_case(31, lens, nq, 2, 4, D, 32)
+    want = run_attention(qg, c).cpu().numpy()
+    flip = tuple(a for a, on in ((0, tokens), (1, heads)) if on)
+    q, out = dev(np.flip(c["q"], flip)), dev(np.full(c["q"].shape, 9, np.float16))
+    t = [dev(c[n]) for n in ("start", "cache", "table", "lens")]
+    T, Hq, _ = c["q"].shape
+    ws = torch.empty(qg.qg_attn_kv4_workspace(Hq, 2, D, c["max_q"]), dtype=torch.uint8, device="cuda")
+    rc = qg.lib().qg_attn_kv4(backwards(qg, q, tokens, heads), T, len(lens), t[0].data_ptr(), c["max_q"], Hq, 2, D, t[1].data_ptr(),
+                              len(c["cache"]), 32, t[2].data_ptr(), t[2].shape[1], t[3].data_ptr(), c["scale"],
+                              backwards(qg, out, tokens, heads), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert rc == qg.QG_OK
+    assert np.array_equal(np.flip(out.cpu().numpy(), flip), want)
+
+
+@pytest.mark.parametrize("tokens,heads", [(1, 0), (0, 1), (1, 1)])
+def test_head_operators_on_views_that_run_backwards(qg, tokens, heads):
+    """Norm and rotation, append and read give what they give in order."""
+    import torch
+    rng = np.random.default_rng(3)
+    T, H, D, page = 21, 6, 128, 16
+    x = rng.normal(size=(T, H, D)).astype("f4")
+    flip = tuple(a for a, on in ((0, tokens), (1, heads)) if on)
+    w, pos, freq = dev(rng.uniform(0.5, 1.5, D).astype("f4")), dev(np.arange(T, dtype=np.int32)), dev(frequencies(64))
+    slot = dev(rng.permutation(4 * page)[:T].astype(np.int64))
+    st = torch.cuda.current_stream().cuda_stream
+    fwd, y = dev(x), torch.empty(T, H, D, device="cuda")
+    back, z = dev(np.flip(x, flip)), torch.empty(T, H, D, device="cuda")
+    qg.qg_qk_norm_rope(fwd, None, w, None, 1e-6, pos, freq, 0, y, None)
+    v = lambda t: backwards(qg, t, tokens, heads)  # noqa: E731
+    assert qg.lib().qg_qk_norm_rope(v(back), None, T, H, 0, D, w.data_ptr(), None, 1e-6, pos.data_ptr(), freq.data_ptr(), 64, 0, v(z),
+                                    None, st) == qg.QG_OK
+    assert torch.equal(z.flip(flip), y)
+    one, two = qg.kv4_cache(4, page, H, D), qg.kv4_cache(4, page, H, D)
+    qg.qg_kv4_append(fwd, fwd, w, 1e-6, pos, freq, 0, slot, one, page)
+    assert qg.lib().qg_kv4_append(v(back), v(back), T, H, D, w.data_ptr(), 1e-6, pos.data_ptr(), freq.data_ptr(), 64, 0, slot.data_ptr(),
+                                  two.data_ptr(), 4, page, st) == qg.QG_OK
+    assert torch.equal(one, two)
+    a, b, k, u = (torch.empty(T, H, D, device="cuda") for _ in range(4))
+    qg.qg_kv4_read(one, page, slot, a, b)
+    assert qg.lib().qg_kv4_read(one.data_ptr(), 4, page, H, D, slot.data_ptr(), T, v(k), v(u), st) == qg.QG_OK
+    assert torch.equal(k.flip(flip), a) and torch.equal(u.flip(flip), b)
