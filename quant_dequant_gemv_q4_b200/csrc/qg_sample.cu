@@ -313,6 +313,9 @@ __device__ unsigned find_count(Shared &s, const unsigned (&c)[kPer], unsigned k)
 // of the weight after it is at most `tail`.  s.before[0]: tokens before the first, s.before[1]: down to the
 // last of them (of all tokens, `c`; the weights are those of `kept` of them).  The bounds' margin of 2e-4
 // covers the bins' borders, these sums and the one in `tail`, all in fp32 (of at most 2^10 logits a thread).
+// The same sum is rounded differently by two neighbouring threads, so both may see a border between their bins, or
+// neither: of several the outermost bins are taken, by atomics, so that every CTA of a cluster, from the same
+// counts, takes the same ones (how many cluster barriers it meets depends on them), and of none all bins.
 __device__ void find_share(Shared &s, const unsigned (&c)[kPer], const unsigned (&kept)[kPer], float tail)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -348,32 +351,37 @@ __device__ void find_share(Shared &s, const unsigned (&c)[kPer], const unsigned 
     if (lane == 31) after_h = after_l = 0.0f;
     const Scan<unsigned> z = block_scan(s, sum);
     unsigned cb = z.before;
-    if (threadIdx.x == 0) {  // (should rounding hide a border from both of its threads: all bins)
-        s.bin[0] = 0;
-        s.before[0] = 0;
-        s.bin[1] = kBins - 1;
-        s.before[1] = z.all;
+    if (threadIdx.x == 0) {
+        s.bin[0] = kBins;
+        s.bin[1] = -1;
     }
     const bool later = lane > warp && lane < kWarps;
     after_h += warp_total(later ? s.scan_f[0][lane] : 0.0f);
     after_l += warp_total(later ? s.scan_f[1][lane] : 0.0f);
     __syncthreads();
     // up through the thread's bins: the weight after bin j, and after the bin before it
-    cb += sum;
 #pragma unroll
     for (int j = kPer - 1; j >= 0; --j) {
         const bool first = b0 + j == 0;
-        if (after_l <= tail && (first || after_l + lo[j] > tail)) {
-            s.bin[0] = b0 + j;
-            s.before[0] = cb - c[j];
-        }
-        if (after_h <= tail && (first || after_h + hi[j] > tail)) {
-            s.bin[1] = b0 + j;
-            s.before[1] = cb;
-        }
+        if (after_l <= tail && (first || after_l + lo[j] > tail)) atomicMin(&s.bin[0], b0 + j);
+        if (after_h <= tail && (first || after_h + hi[j] > tail)) atomicMax(&s.bin[1], b0 + j);
         after_l += lo[j];
         after_h += hi[j];
-        cb -= c[j];
+    }
+    __syncthreads();
+    const int from = s.bin[0] < kBins ? s.bin[0] : 0, to = s.bin[1] >= 0 ? s.bin[1] : kBins - 1;
+    __syncthreads();  // (read everywhere)
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        if (b0 + j == from) {
+            s.bin[0] = from;
+            s.before[0] = cb;
+        }
+        cb += c[j];
+        if (b0 + j == to) {
+            s.bin[1] = to;
+            s.before[1] = cb;
+        }
     }
     __syncthreads();
 }

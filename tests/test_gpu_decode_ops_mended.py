@@ -69,3 +69,38 @@ def test_head_operators_on_views_that_run_backwards(qg, tokens, heads):
     qg.qg_kv4_read(one, page, slot, a, b)
     assert qg.lib().qg_kv4_read(one.data_ptr(), 4, page, H, D, slot.data_ptr(), T, v(k), v(u), st) == qg.QG_OK
     assert torch.equal(k.flip(flip), a) and torch.equal(u.flip(flip), b)
+
+
+# ---------------------------------------------------------------------------------------------
+# Sampling
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("V", [20_000, 151_936])
+def test_sample_share_on_the_border_of_two_threads_bins(qg, V):
+    """Shares whose bounds fall on the border between two threads' bins of the histogram, where the two add up the
+    weight after it in another order: the bins next to the cut are the same for every CTA of a cluster, and the
+    token that of the definition, every time."""
+    import torch
+    rng = np.random.default_rng(V)
+    R = 160
+    x = (rng.normal(size=(1, V)) * 2).astype("f4").repeat(R, 0)
+    t = (x[0].max() - x[0].astype(np.float64)) * np.log2(np.e)
+    count = np.bincount(np.rint(64 * t).astype(int), minlength=4096)
+    b = np.arange(4096)
+    total = np.exp2(-t).sum()
+    p = np.empty(R, "f4")
+    for i in range(R):
+        border = 4 * (32 * (1 + i // 40) if i % 2 else 20 + i)  # between warps, and within one
+        part = (count * np.exp2(-(b + (-0.5 if i % 4 < 2 else 0.5)) / 64) * (1.0002 if i % 4 < 2 else 0.9998))[border:].sum()
+        p[i] = 1 - part / total
+    assert 0 < p.min() and p.max() < 1
+    u = rng.random(R).astype("f4")
+    want = [ref.sample(x[i], None, None, p[i], None, u[i]) for i in range(R)]
+    lx, du = dev(x), dev(u)
+    tok = torch.zeros(R, dtype=torch.int32, device="cuda")
+    for _ in range(5):
+        qg.qg_sample(lx, None, None, dev(p), None, du, tok)
+        assert tok.tolist() == want
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")  # a row alone: a larger cluster
+    for i in range(R):
+        qg.qg_sample(lx[:1], None, None, dev(p[i:i + 1]), None, du[i:i + 1], one)
+        assert one.item() == want[i]
