@@ -472,10 +472,11 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
         int item = sm.found_item;
         bool any_cut = false, from_start = false;
         const int page_blocks = a.page / kKvBlock;
-        // page of block 8 unit + lane of the cursor's item, and the block's place in it
+        // page of block 8 unit + lane of the cursor's item (up to 31 blocks past the sequence's last: their places may
+        // pass 2^31), -1 past its end
         auto look_up = [&](const Cursor &k, int unit) -> int {
             const int blk = unit * kTileBlocks + lane;
-            return blk * kKvBlock < k.q.len ? a.table[(int64_t)k.s * a.width + blk / page_blocks] : -1;
+            return (int64_t)blk * kKvBlock < k.q.len ? a.table[(int64_t)k.s * a.width + blk / page_blocks] : -1;
         };
         int ahead = 0, pages = -1, pages_next = -1;
         for (int i = 0; i < count; ++i) {

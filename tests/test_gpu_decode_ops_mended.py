@@ -104,3 +104,30 @@ def test_sample_share_on_the_border_of_two_threads_bins(qg, V):
     for i in range(R):
         qg.qg_sample(lx[:1], None, None, dev(p[i:i + 1]), None, du[i:i + 1], one)
         assert one.item() == want[i]
+
+
+# ---------------------------------------------------------------------------------------------
+# Attention
+# ---------------------------------------------------------------------------------------------
+def test_attention_over_the_longest_table(qg):
+    """A table of as many places as one may have, 2^31 - 256, its first and its last page alone there: what the same
+    pages give side by side.  (All values of v lie in 1 .. 1.15.  Both results are off by the weights' and values'
+    rounding to fp16, 2^-11 each, the scores' (below 2^-8 here) and the output's: less than 2^-6 together.)"""
+    import torch
+    page, width, D = 16 * 178481, 752, 64
+    assert page * width == 0x7fffff00
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    cache = torch.randint(0, 256, (2, 1, page // 16, 18 * D), dtype=torch.uint8, device="cuda", generator=gen)
+    for part, m in ((0, -0.075), (1, 1.0)):
+        at = cache[..., part * 9 * D + 8 * D:(part + 1) * 9 * D]
+        at.copy_(torch.tensor([0.01, m], dtype=torch.float16, device="cuda").view(torch.uint8).repeat(16))
+    q = torch.randn(3, 4, D, device="cuda", generator=gen).half()
+    start = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    table[0, 0], table[0, -1] = 0, 1
+    far, near = torch.zeros_like(q), torch.zeros_like(q)
+    qg.qg_attn_kv4(q, start, 3, cache, page, table, torch.tensor([2 ** 31 - 1], dtype=torch.int32, device="cuda"), 1.0, far)
+    qg.qg_attn_kv4(q, start, 3, cache, page, torch.tensor([[0, 1]], dtype=torch.int32, device="cuda"),
+                   torch.tensor([2 * page], dtype=torch.int32, device="cuda"), 1.0, near)
+    assert (near.float() - 1.075).abs().max() < 0.08
+    assert (far.float() - near.float()).abs().max() <= 2 * 2.0 ** -6
