@@ -701,6 +701,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                     for (int g = 0; g < F::kGroups; ++g)
                         *reinterpret_cast<uint32_t *>(smem + st * C::kTileBytes + (pl / kKvBlock) * F::kBlock + F::kPart + F::kCodes +
                                                       ((pl % kKvBlock) * F::kGroups + g) * 4) = 0;
+                fence_proxy_async_smem();  // the stage is overwritten by a bulk copy (the async proxy) later on
                 bar_sync(kHoleBar + wv, 128);
             }
 #pragma unroll 1

@@ -131,3 +131,14 @@ def test_attention_over_the_longest_table(qg):
                    torch.tensor([2 * page], dtype=torch.int32, device="cuda"), 1.0, near)
     assert (near.float() - 1.075).abs().max() < 0.08
     assert (far.float() - near.float()).abs().max() <= 2 * 2.0 ** -6
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 32), (256, 16)])
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attention_with_a_hole_in_every_other_tile(qg, D, page, nq):
+    """Pages that are not there all along long sequences: the ring's stages are zeroed in part and filled again, over
+    and over."""
+    c = attention_case(17, [2600, 1900], nq, 2, 4, D, page)
+    c["table"][0, 3::128 * 2 // page] = -1
+    c["table"][1, 1::128 * 3 // page] = 2 ** 30
+    check_attention(qg, c)
