@@ -225,6 +225,16 @@ template <int D, int N> struct Cfg {
     static constexpr int kBytes = kP + kPAll;
 };
 
+// Giving up.  A wait that lasts longer than kWaitNs sets the call's error word and `gave_up`.  The producer, the only
+// role whose waits end on that alone, then stops and sets `quiet` (as it does at its end in any case); the other roles
+// wait on until `dead`, which is set once both are, and go through their remaining tiles without waiting.  The
+// descriptions of the tiles no longer change by then, so the warps of a role take the same way through them and meet
+// at its named barriers, which have no limit of their own.  What is computed is void; every address stays that of some
+// tile that was described (a slot without one holds zeros: no rows).
+struct Stop {
+    int dead, gave_up, quiet;
+};
+
 template <int N> struct Small {
     uint64_t ring_full[8], ring_empty[8];
     uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3], s_full[2], s_empty[2], p_full[2], p_empty[2], q_full[2];
@@ -235,7 +245,9 @@ template <int N> struct Small {
     int64_t scan[2][32];
     int iscan[32];
     uint32_t tmem;
-    int dead, produced;  // produced: tiles described so far
+    uint64_t drained[2];  // the issuers' last products, after a wait that ran out
+    Stop stop;
+    int produced;         // tiles described so far
     alignas(16) float base[N];    // reference - kWeightShift
     alignas(16) int lim[2][N];    // last place that a row sees (of the parts of items in turn)
     int64_t orow[2][N];           // where a row of out starts, or kNoRow
@@ -246,38 +258,38 @@ template <int N> struct Small {
     float factor[N];
 };
 
-// Waits for a phase; gives up after kWaitNs of wall time, or at once when another warp has.
-__device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, int *dead, int *err)
+// Waits for a phase; false where it gives up.
+template <bool PRODUCER = false> __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile Stop *stop, int *err)
 {
     const uint32_t b = smem_u32(bar);
-    if (mbar_try_wait(b, parity)) return;
+    if (mbar_try_wait(b, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     for (;;) {
         // (a try suspends the warp for a while only: keep what is issued between tries short)
 #pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(b, parity)) return;
-        if (*(volatile int *)dead) return;
+        for (int i = 0; i < 8; ++i)
+            if (mbar_try_wait(b, parity)) return true;
+        if (PRODUCER ? stop->gave_up : stop->dead) return false;
         if (global_timer_ns() - t0 > kWaitNs) {
-            *(volatile int *)dead = 1;
+            stop->gave_up = 1;
             *err = 1;
-            return;
+            if (stop->quiet) stop->dead = 1;
         }
     }
 }
 
 // Waits until `need` tiles are described.
-__device__ __forceinline__ void wait_described(int *produced, int need, int *dead, int *err)
+__device__ __forceinline__ void wait_described(int *produced, int need, volatile Stop *stop, int *err)
 {
     const uint64_t t0 = global_timer_ns();
     for (;;) {
         int v;
         asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(produced)) : "memory");
-        if (v >= need || *(volatile int *)dead) return;
+        if (v >= need || stop->dead) return;
         if (global_timer_ns() - t0 > kWaitNs) {
-            *(volatile int *)dead = 1;
+            stop->gave_up = 1;
             *err = 1;
-            return;
+            if (stop->quiet) stop->dead = 1;
         }
     }
 }
@@ -361,10 +373,13 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
         }
         mbar_init(smem_u32(&sm.o_full), 1);
         mbar_init(smem_u32(&sm.o_empty), 4 * C::kSoft);
+        mbar_init(smem_u32(&sm.drained[0]), 1);
+        mbar_init(smem_u32(&sm.drained[1]), 1);
         mbar_init_fence();
-        sm.dead = 0;
+        sm.stop = {0, 0, 0};
         sm.produced = 0;
     }
+    for (int i = threadIdx.x; i < (int)(sizeof(sm.meta) / 4); i += C::kWarps * 32) reinterpret_cast<int *>(sm.meta)[i] = 0;
     // Tensor memory is taken only when the kernels before are done, and the kernels after may start only when
     // it is taken: neither then holds it while it waits for the other.
     pdl_wait();
@@ -465,7 +480,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
         __syncthreads();
     }
 
-    int *dead = &sm.dead;
+    volatile Stop *const stop = &sm.stop;
     if (warp == kProducer) {
         // ---- copies and descriptions of the tiles
         Cursor c = sm.found;
@@ -481,8 +496,8 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
         int ahead = 0, pages = -1, pages_next = -1;
         for (int i = 0; i < count; ++i) {
             const int st = i % C::kStages;
-            if (i >= C::kStages) wait(&sm.ring_empty[st], ((i / C::kStages) & 1) ^ 1, dead, a.err);
-            if (*(volatile int *)dead) break;
+            const bool free = i < C::kStages || wait<true>(&sm.ring_empty[st], ((i / C::kStages) & 1) ^ 1, stop, a.err);
+            if (!__all_sync(0xffffffffu, free)) break;
             const int pos = c.unit * kTile;
             const bool first = i == 0 || c.unit == 0;
             if (first) from_start = c.unit == 0;
@@ -552,12 +567,11 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                 ++item;
             }
         }
-        if (*(volatile int *)dead)  // copies in flight land before the shared memory is given up
-            for (int st = 0; st < C::kStages; ++st) {
-                (void)mbar_wait_bounded(smem_u32(&sm.ring_full[st]), 0);
-                (void)mbar_wait_bounded(smem_u32(&sm.ring_full[st]), 1);
-            }
-        if (lane == 0 && count > 0 && !a.by_item && !any_cut) a.cut[cta] = make_int4(0, 0, 0, 0);
+        if (lane == 0) {
+            __threadfence_block();
+            stop->quiet = 1;
+            if (count > 0 && !a.by_item && !any_cut) a.cut[cta] = make_int4(0, 0, 0, 0);
+        }
     } else if (warp >= kIssuer) {
         // ---- the matrix instructions: a warp for the scores and one for the weighted sums, so that neither waits
         // for the other's operands; a warp stays together, an elected lane issues
@@ -569,16 +583,16 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
             uint32_t qb = qa;
             for (int i = 0; i < count; ++i) {
                 const int sb = i % C::kSBufs;
-                wait_described(&sm.produced, i + 1, dead, a.err);
+                wait_described(&sm.produced, i + 1, stop, a.err);
                 if (__shfl_sync(0xffffffffu, sm.meta[i % kMetas].flags, 0) & kFirst) {
-                    wait(&sm.q_full[seg % C::kQBufs], (seg / C::kQBufs) & 1, dead, a.err);
+                    wait(&sm.q_full[seg % C::kQBufs], (seg / C::kQBufs) & 1, stop, a.err);
                     qb = qa + (seg % C::kQBufs) * C::kQBytes;
                     ++seg;
                 }
-                if (i >= C::kSBufs) wait(&sm.s_empty[sb], ((i / C::kSBufs) & 1) ^ 1, dead, a.err);
+                if (i >= C::kSBufs) wait(&sm.s_empty[sb], ((i / C::kSBufs) & 1) ^ 1, stop, a.err);
                 for (int h = 0; h < C::kSub; ++h) {
                     const int u = i * C::kSub + h, b = u % C::kBufs;
-                    wait(&sm.k_full[b], (u / C::kBufs) & 1, dead, a.err);
+                    wait(&sm.k_full[b], (u / C::kBufs) & 1, stop, a.err);
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < D / C::kSub / 16; ++k) {
@@ -594,16 +608,16 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
             const uint32_t pa = smem_u32(smem + C::kP);
             for (int i = 0; i < count; ++i) {
                 const int pb = i % C::kPBufs;
-                wait_described(&sm.produced, i + 1, dead, a.err);
+                wait_described(&sm.produced, i + 1, stop, a.err);
                 const int flags = __shfl_sync(0xffffffffu, sm.meta[i % kMetas].flags, 0);
                 if (flags & kFirst) {
-                    if (seg > 0) wait(&sm.o_empty, (seg - 1) & 1, dead, a.err);
+                    if (seg > 0) wait(&sm.o_empty, (seg - 1) & 1, stop, a.err);
                     ++seg;
                 }
-                wait(&sm.p_full[pb], (i / C::kPBufs) & 1, dead, a.err);
+                wait(&sm.p_full[pb], (i / C::kPBufs) & 1, stop, a.err);
                 for (int h = 0; h < C::kSub; ++h) {
                     const int u = i * C::kSub + h, b = u % C::kBufs;
-                    wait(&sm.v_full[b], (u / C::kBufs) & 1, dead, a.err);
+                    wait(&sm.v_full[b], (u / C::kBufs) & 1, stop, a.err);
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < C::kVTok / 16; ++k)
@@ -632,13 +646,13 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
         constexpr int kPer = N > 32 && kChunks > 1 ? 2 : 1;
         for (int i = 0; i < count; ++i) {
             const int st = i % C::kStages;
-            wait(&sm.ring_full[st], (i / C::kStages) & 1, dead, a.err);
+            wait(&sm.ring_full[st], (i / C::kStages) & 1, stop, a.err);
             const uint8_t *kb = smem + st * C::kTileBytes;
 #pragma unroll 1
             for (int h = (wk + i * C::kSub) % C::kWork; h < C::kSub; h += C::kWork) {
                 const int u = i * C::kSub + h, b = u % C::kBufs;
                 if (u >= C::kBufs) {
-                    wait(&sm.k_empty[b], ((u / C::kBufs) & 1) ^ 1, dead, a.err);
+                    wait(&sm.k_empty[b], ((u / C::kBufs) & 1) ^ 1, stop, a.err);
                     tc_fence_after();
                 }
                 const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kK + b * C::kKCols;
@@ -691,7 +705,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
         const uint32_t lanes = tmem + ((uint32_t)(w * 32) << 16) + C::kV;
         for (int i = 0; i < count; ++i) {
             const int st = i % C::kStages;
-            wait(&sm.ring_full[st], (i / C::kStages) & 1, dead, a.err);
+            wait(&sm.ring_full[st], (i / C::kStages) & 1, stop, a.err);
             const Meta &m = sm.meta[i % kMetas];
             if (m.flags & kHole) {
                 // places that are not there hold anything, NaN among it: this warpgroup zeroes the scales of its own
@@ -709,7 +723,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                 const int u = i * C::kSub + h, b = u % C::kBufs;
                 const uint8_t *vb = smem + st * C::kTileBytes + F::kPart + h * (C::kVTok / kKvBlock) * F::kBlock;
                 if (u >= C::kBufs) {
-                    wait(&sm.v_empty[b], ((u / C::kBufs) & 1) ^ 1, dead, a.err);
+                    wait(&sm.v_empty[b], ((u / C::kBufs) & 1) ^ 1, stop, a.err);
                     tc_fence_after();
                 }
                 if (!idle) {
@@ -828,7 +842,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
             if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[qb]));
         };
         if (count > 0) {
-            wait_described(&sm.produced, 1, dead, a.err);
+            wait_described(&sm.produced, 1, stop, a.err);
             stage_q(sm.meta[0].item, 0);
         }
         Item next = {};
@@ -836,7 +850,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
         int flags = 0;
         for (int i = 0; i < count; ++i) {
             const int sb = i % C::kSBufs, pb = i % C::kPBufs;
-            wait(&sm.s_full[sb], (i / C::kSBufs) & 1, dead, a.err);
+            wait(&sm.s_full[sb], (i / C::kSBufs) & 1, stop, a.err);
             tc_fence_after();
             const Meta &m = sm.meta[i % kMetas];
             flags = m.flags;
@@ -906,7 +920,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
 #pragma unroll
                     for (int n = 0; n < NS; ++n) sum[n] *= sm.factor[n0 + n];
                     // every product before this tile is in O
-                    wait(&sm.p_empty[(i - 1) % C::kPBufs], ((i - 1) / C::kPBufs) & 1, dead, a.err);
+                    wait(&sm.p_empty[(i - 1) % C::kPBufs], ((i - 1) / C::kPBufs) & 1, stop, a.err);
                     tc_fence_after();
 #pragma unroll 1
                     for (int y = 0; y < C::kMh * NS; y += 16) {
@@ -925,7 +939,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty[sb]));
-            if (i >= C::kPBufs) wait(&sm.p_empty[pb], ((i / C::kPBufs) & 1) ^ 1, dead, a.err);
+            if (i >= C::kPBufs) wait(&sm.p_empty[pb], ((i / C::kPBufs) & 1) ^ 1, stop, a.err);
             uint8_t *pp = smem + C::kP + pb * C::kPBytes + (n0 >> 3) * (16 * kTile) + (t >> 3) * 128 + (t & 7) * 16;
 #pragma unroll
             for (int n = 0; n < NS; n += 8) {
@@ -966,7 +980,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
                     sm.inv[n] = complete ? (den > 0.0f ? 1.0f / den : 0.0f) : 1.0f;
                     if (!complete) a.stat[(int64_t)slot * N + n] = make_float2(sm.ref[n], den);
                 }
-                wait(&sm.o_full, seg & 1, dead, a.err);
+                wait(&sm.o_full, seg & 1, stop, a.err);
                 tc_fence_after();
                 bar_sync(bar_id, 128);
                 // ---- O, some rows at a time through shared memory (the weights' buffers are free now)
@@ -1026,6 +1040,17 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
     }
     tc_fence_before();
     __syncthreads();
+    if (stop->gave_up) {
+        // copies and products in flight end before shared and tensor memory are given up
+        if (warp == kProducer)
+            for (int st = 0; st < C::kStages && st < sm.produced; ++st)
+                (void)mbar_wait_bounded(smem_u32(&sm.ring_full[st]), ((sm.produced - 1 - st) / C::kStages) & 1);
+        if (warp >= kIssuer) {
+            umma_commit_elect(smem_u32(&sm.drained[warp - kIssuer]));
+            (void)mbar_wait_bounded(smem_u32(&sm.drained[warp - kIssuer]), 0);
+        }
+        __syncthreads();
+    }
     if (warp == kIssuer) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -1048,7 +1073,8 @@ template <int D, int N, int RB> __global__ void __launch_bounds__(512) attn_kv4_
     pdl_launch_dependents();
     pdl_wait();
     const int4 c = a.cut[blockIdx.x];
-    if (c.w == 0) return;
+    const int gave_up = *a.err;  // (cuts and parts may be missing then)
+    if ((c.w == 0) | (gave_up != 0)) return;
     const int head = c.y & 0xffff, cta = c.y >> 16;
     const int x = threadIdx.x % TX, y = threadIdx.x / TX % TY, rl = threadIdx.x / (TX * TY);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
