@@ -1152,9 +1152,9 @@ template <int D, int N> int launch_attn(AttnArgs &a, int grid, int nseq, void *s
 {
     static std::atomic<uint64_t> raised{0};  // devices whose shared-memory limit is raised
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return QG_ERR_CUDA;
+    if (cuda_status(cudaGetDevice(&dev)) != QG_OK) return QG_ERR_CUDA;
     if (dev >= 64 || !(raised.load() >> dev & 1)) {
-        if (cudaFuncSetAttribute(attn_kv4_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, N>::kBytes) != cudaSuccess)
+        if (cuda_status(cudaFuncSetAttribute(attn_kv4_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, N>::kBytes)) != QG_OK)
             return QG_ERR_CUDA;
         if (dev < 64) raised.fetch_or(uint64_t(1) << dev);
     }

@@ -77,16 +77,25 @@ inline int check_view(const qg_heads *h, int64_t T, int H, int want, bool f16_on
     return QG_OK;
 }
 
+// The status of a runtime call.  What a failed one leaves behind is taken back: a later launch that looks at the
+// runtime's last error would take it for its own.
+inline int cuda_status(cudaError_t e)
+{
+    if (e == cudaSuccess) return QG_OK;
+    (void)cudaGetLastError();
+    return QG_ERR_CUDA;
+}
+
 // Multiprocessors of the current device (a small table, no allocation).
 inline int current_sms(int *sms)
 {
     static std::atomic<int> known[64];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return QG_ERR_CUDA;
+    if (cuda_status(cudaGetDevice(&dev)) != QG_OK) return QG_ERR_CUDA;
     const bool slot = dev >= 0 && dev < 64;
     int n = slot ? known[dev].load(std::memory_order_relaxed) : 0;
     if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return QG_ERR_CUDA;
+        if (cuda_status(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) != QG_OK) return QG_ERR_CUDA;
         if (slot) known[dev].store(n, std::memory_order_relaxed);
     }
     *sms = n;
@@ -108,7 +117,7 @@ inline int launch_pdl(void (*kernel)(Args...), dim3 grid, dim3 block, size_t sme
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

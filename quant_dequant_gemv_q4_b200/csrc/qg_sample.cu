@@ -952,14 +952,14 @@ int look_at_card(Card *out)
     static Card cards[64];
     static std::mutex lock;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return QG_ERR_CUDA;
+    if (cuda_status(cudaGetDevice(&dev)) != QG_OK || dev >= 64) return QG_ERR_CUDA;
     if (!known[dev].load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> hold(lock);
         Card c = {};
-        if (cudaDeviceGetAttribute(&c.optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess) return QG_ERR_CUDA;
+        if (cuda_status(cudaDeviceGetAttribute(&c.optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != QG_OK) return QG_ERR_CUDA;
         for (auto kernel : {sample_kernel<true>, sample_kernel<false>})
-            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, c.optin) != cudaSuccess ||
-                cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            if (cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, c.optin)) != QG_OK ||
+                cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != QG_OK)
                 return QG_ERR_CUDA;
         for (int C = 1; C <= kMostCtas; ++C) {
             cudaLaunchConfig_t cfg = {};
@@ -972,10 +972,7 @@ int look_at_card(Card *out)
             attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
             cfg.attrs = &attr;
             cfg.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&c.side_by_side[C], sample_kernel<true>, &cfg) != cudaSuccess) {
-                c.side_by_side[C] = 0;
-                (void)cudaGetLastError();
-            }
+            if (cuda_status(cudaOccupancyMaxActiveClusters(&c.side_by_side[C], sample_kernel<true>, &cfg)) != QG_OK) c.side_by_side[C] = 0;
         }
         if (c.side_by_side[1] < 1) return QG_ERR_CUDA;
         cards[dev] = c;
@@ -1072,7 +1069,7 @@ int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t row_stride, 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, resident ? sample_kernel<true> : sample_kernel<false>, a) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+    return cuda_status(cudaLaunchKernelEx(&cfg, resident ? sample_kernel<true> : sample_kernel<false>, a));
 }
 
 }  // extern "C"

@@ -142,3 +142,44 @@ def test_attention_with_a_hole_in_every_other_tile(qg, D, page, nq):
     c["table"][0, 3::128 * 2 // page] = -1
     c["table"][1, 1::128 * 3 // page] = 2 ** 30
     check_attention(qg, c)
+
+
+# ---------------------------------------------------------------------------------------------
+# Errors
+# ---------------------------------------------------------------------------------------------
+def test_a_launch_that_failed_leaves_no_error_behind(qg):
+    """While some stream is captured in the global mode, nothing can be launched on the legacy stream: QG_ERR_CUDA.
+    The next call, of the GEMVs' kind, launches and says so."""
+    import torch
+    rt = ctypes.CDLL("libcudart.so.12")
+    x, y = torch.ones(2, 2, 64, device="cuda"), torch.zeros(2, 2, 64, device="cuda")
+    h, out = x.half(), torch.zeros(2, 2, 64, device="cuda", dtype=torch.float16)
+    cache = qg.kv4_cache(2, 16, 2, 64)
+    slot, i32 = torch.arange(2, device="cuda"), torch.ones(2, dtype=torch.int32, device="cuda")
+    start, table = torch.arange(3, dtype=torch.int32, device="cuda"), torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    u = torch.zeros(2, device="cuda")
+    ws = torch.empty(qg.qg_attn_kv4_workspace(2, 2, 64, 1), dtype=torch.uint8, device="cuda")
+    src, dst = torch.ones(64, device="cuda"), torch.zeros(64, device="cuda")
+    calls = [lambda: qg.qg_qk_norm_rope(x, None, None, None, 0.0, None, None, 0, y, None, stream=0),
+             lambda: qg.qg_kv4_append(x, x, None, 0.0, None, None, 0, slot, cache, 16, stream=0),
+             lambda: qg.qg_kv4_read(cache, 16, slot, x, y, stream=0),
+             lambda: qg.qg_attn_kv4(h, start, 1, cache, 16, table, i32, 1.0, out, workspace=ws, stream=0),
+             lambda: qg.qg_sample(x.view(2, 128), None, None, None, None, u, i32, stream=0)]
+    for call in calls:
+        call()  # what is set up once is
+    qg.qg_hbm_copy(src, dst, 256)
+    torch.cuda.synchronize()
+    for call in calls:
+        s = ctypes.c_void_p()
+        assert rt.cudaStreamCreate(ctypes.byref(s)) == 0
+        assert rt.cudaStreamBeginCapture(s, 0) == 0
+        with pytest.raises(qg.QgError) as e:
+            call()
+        g = ctypes.c_void_p()
+        rt.cudaStreamEndCapture(s, ctypes.byref(g))  # (invalidated: no graph)
+        rt.cudaGetLastError()
+        assert rt.cudaStreamDestroy(s) == 0
+        assert e.value.status == qg.QG_ERR_CUDA
+        dst.zero_()
+        qg.qg_hbm_copy(src, dst, 256)
+        assert torch.equal(src, dst)
