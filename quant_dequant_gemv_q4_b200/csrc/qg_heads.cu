@@ -451,11 +451,12 @@ template <int D> __global__ void __launch_bounds__(kHeadWarps * 32) kv4_read_ker
 
 bool good_dim(int D) { return D == 64 || D == 128 || D == 256; }
 
-int check_rope(const int32_t *pos, const double *freq, int R, int pairing, int D, RopeArgs *out)
+// (without tokens there are no positions: an empty tensor has no address)
+int check_rope(const int32_t *pos, const double *freq, int R, int pairing, int D, int64_t T, RopeArgs *out)
 {
     if (R < 0 || R > D || R % 2) return QG_ERR_SHAPE;
     if (pairing != QG_ROPE_HALVES && pairing != QG_ROPE_ADJACENT) return QG_ERR_VARIANT;
-    if (R > 0 && (!pos || !freq)) return QG_ERR_NULL;
+    if (R > 0 && T > 0 && (!pos || !freq)) return QG_ERR_NULL;
     if (reinterpret_cast<uintptr_t>(pos) % 4 || reinterpret_cast<uintptr_t>(freq) % 8) return QG_ERR_ALIGN;
     out->pos = pos;
     out->freq = freq;
@@ -525,7 +526,7 @@ int qg_qk_norm_rope(const qg_heads *q, const qg_heads *k, int64_t T, int Hq, int
         return QG_ERR_SHAPE;
     if (!(eps >= 0.0)) return QG_ERR_RANGE;
     NormRopeArgs a = {};
-    int rc = check_rope(pos, inv_freq, R, pairing, D, &a.rope);
+    int rc = check_rope(pos, inv_freq, R, pairing, D, T, &a.rope);
     if (rc != QG_OK) return rc;
     if (T == 0 || Hq + Hk == 0) return QG_OK;
     if (Hq > 0) {
@@ -565,7 +566,7 @@ int qg_kv4_append(const qg_heads *k, const qg_heads *v, int64_t T, int H, int D,
     if (T < 0 || T > kMostTokens) return QG_ERR_SHAPE;
     if (!(eps >= 0.0)) return QG_ERR_RANGE;
     AppendArgs a = {};
-    if ((rc = check_rope(pos, inv_freq, R, pairing, D, &a.rope)) != QG_OK) return rc;
+    if ((rc = check_rope(pos, inv_freq, R, pairing, D, T, &a.rope)) != QG_OK) return rc;
     if (T == 0 || pages == 0) return QG_OK;
     if (!slot) return QG_ERR_NULL;
     if ((rc = check_view(k, T, H, kV, false, &a.k)) != QG_OK) return rc;

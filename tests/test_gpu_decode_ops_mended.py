@@ -183,3 +183,28 @@ def test_a_launch_that_failed_leaves_no_error_behind(qg):
         dst.zero_()
         qg.qg_hbm_copy(src, dst, 256)
         assert torch.equal(src, dst)
+
+
+def test_empty_tensors(qg):
+    """No tokens, no rows, no sequences, no places: nothing is done, nothing is refused."""
+    import torch
+    x, h = torch.empty(0, 2, 64, device="cuda"), torch.empty(0, 2, 64, device="cuda", dtype=torch.float16)
+    i32, i64, f = (torch.empty(0, dtype=t, device="cuda") for t in (torch.int32, torch.int64, torch.float32))
+    freq, w = dev(frequencies(32)), torch.ones(64, device="cuda")
+    cache = qg.kv4_cache(2, 16, 2, 64).fill_(7)
+    qg.qg_qk_norm_rope(x, x[:, :1], w, w, 1e-6, i32, freq, 0, h, h[:, :1])
+    qg.qg_kv4_append(x, x, w, 1e-6, i32, freq, 0, i64, cache, 16)
+    qg.qg_kv4_append(x, x, w, 1e-6, i32, freq, 0, i64, cache[:0], 16)
+    qg.qg_kv4_read(cache, 16, i64, x, h)
+    start, table = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    qg.qg_attn_kv4(h, start, 0, cache, 16, table, i32, 1.0, torch.empty_like(h))
+    out = torch.full((3, 2, 64), 9.0, device="cuda", dtype=torch.float16)
+    q = torch.ones_like(out)
+    qg.qg_attn_kv4(q, start, 0, cache, 16, table, i32, 1.0, out)  # rows, but no sequences
+    assert (out == 9).all()
+    one = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    qg.qg_attn_kv4(q, one, 3, cache[:0], 16, torch.empty(1, 0, dtype=torch.int32, device="cuda"), one[1:], 1.0, out)  # no pages at all
+    assert (out == 0).all()
+    qg.qg_sample(torch.empty(0, 50, device="cuda"), f, i32, f, f, f, i32)
+    torch.cuda.synchronize()
+    assert (cache == 7).all()
