@@ -364,7 +364,7 @@ int qg_qk_norm_rope(const qg_heads *q, const qg_heads *k, int64_t T, int Hq, int
 size_t qg_kv4_bytes(int64_t pages, int page, int H, int D);
 
 /* Appends keys and values, quantized, with the key's head norm and rotation applied on the way:
- * per 64 dimensions m = fp16(min), d = fp16((max - min) / 15), code = the whole number nearest to
+ * per 64 dimensions m = fp16(fp32(min)), d = fp16(fp32((max - min) / 15)), code = the whole number nearest to
  * (x - m) / d (ties to even), within 0..15 (0 where d is 0).
  *   k, v       views of [T][H][D], fp32 or fp16 each; k before its norm and rotation
  *   wk, eps, pos, inv_freq, R, pairing   as for qg_qk_norm_rope (wk NULL: no norm; R == 0: no rotation)
@@ -373,7 +373,9 @@ size_t qg_kv4_bytes(int64_t pages, int page, int H, int D);
  *              ends up with parts of both tokens).
  *   cache      device, qg_kv4_bytes(pages, page, H, D) bytes, 16-byte aligned; other entries are left
  *              as they are
- * Norm, rotation and quantization are evaluated in 64 bits, so that the stored codes are the formula's.
+ * Norm, rotation, the range and the codes are evaluated in 64 bits, so that the stored bytes are the formula's.
+ * m and d are rounded twice, as a conversion from 64 to 16 bits by way of 32 does: next to a tie of fp16 that
+ * may give the neighbour of the nearest fp16 (for about one group in 15000 whose values are not fp32).
  * Inputs are finite.  Scales saturate at fp16's largest value.  Errors as qg_qk_norm_rope. */
 int qg_kv4_append(const qg_heads *k, const qg_heads *v, int64_t T, int H, int D, const float *wk,
                   double eps, const int32_t *pos, const double *inv_freq, int R, int pairing,

@@ -274,8 +274,8 @@ template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32, 4)
 // other by the rounding of the sums before it.  So that the stored bytes are those of the formula, the norm,
 // the rotation, the group's range and d are in 64 bits; the quotient is in fp32 but where it comes within its
 // own error of a border, where it is formed again in 64 bits (for about one value in ten thousand).  d and m
-// are rounded to fp16 first and the codes are found against the rounded pair, which is what a reader
-// multiplies by.
+// are rounded to fp32 and then to fp16, two steps of the cache's definition (what conversions from 64 to 16 bits
+// commonly do), and the codes are found against the rounded pair, which is what a reader multiplies by.
 template <int D, int KIND> __global__ void __launch_bounds__(kHeadWarps * 32, 3) kv4_append_kernel(const AppendArgs a)
 {
     constexpr int LR = D / kV, RW = 32 / LR;

@@ -208,3 +208,31 @@ def test_empty_tensors(qg):
     qg.qg_sample(torch.empty(0, 50, device="cuda"), f, i32, f, f, f, i32)
     torch.cuda.synchronize()
     assert (cache == 7).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# The cache's scales
+# ---------------------------------------------------------------------------------------------
+def test_scales_are_rounded_to_fp32_and_then_to_fp16(qg):
+    """A group whose least value is 1 + 2^-11 + 2^-40 (a rotation by 2^-41 makes it): as fp32 that is 1 + 2^-11, a tie
+    of fp16 that goes to 1; one rounding would give 1 + 2^-10.  d likewise: fp16(fp32(range / 15))."""
+    import torch
+    D, page = 64, 16
+    x = np.full((2, 1, D), 2.0, "f4")
+    x[0, 0, 0] = 1 + 2.0 ** -11
+    x[1, 0, 1], x[1, 0, 33] = 2 - 15 * (1 + 2.0 ** -11), -3.75   # a range of 15 (1 + 2^-11 + 2^-40), nearly
+    freq = np.zeros(32)
+    freq[:2] = 2.0 ** -41, 2.0 ** -38
+    pos = np.array([-1, -1], np.int32)
+    kk = ref.rope(x.astype(np.float64), pos, freq, 0)
+    assert kk[0].min() == 1 + 2.0 ** -11 + 2.0 ** -40
+    once = kk[0].min().astype(np.float16)
+    code, d, m = ref.quantize(kk)
+    assert m[0, 0, 0] == 1 and once == np.float16(1 + 2.0 ** -10)
+    assert d[1, 0, 0] == 1 and ((kk[1].max() - kk[1].min()) / 15).astype(np.float16) == np.float16(1 + 2.0 ** -10)
+    cache, slot = torch.zeros(1, 1, 1, 18 * D, dtype=torch.uint8, device="cuda"), torch.arange(2, device="cuda")
+    qg.qg_kv4_append(dev(x), dev(x), None, 0.0, dev(pos), dev(freq), 0, slot, cache, page)
+    want = np.zeros((1, 1, 1, 18 * D), np.uint8)
+    ref.store(want, page, np.arange(2), 0, code, d, m)
+    ref.store(want, page, np.arange(2), 1, *ref.quantize(x.astype(np.float64)))
+    assert np.array_equal(cache.cpu().numpy(), want)
