@@ -304,6 +304,10 @@ def _bound():
         spec = importlib.util.spec_from_file_location("qg_binding", BINDING_PATH)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
+        from . import build
+        if m.built_for != build.built_for():
+            raise RuntimeError(f"{BINDING_PATH} was built for {m.built_for}, this is {build.built_for()}; build it again with "
+                               "`python -m quant_dequant_gemv_q4_b200.build`")
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
                  (L.qg_qk_norm_rope, L.qg_kv4_append, L.qg_kv4_read, L.qg_attn_kv4_workspace, L.qg_attn_kv4, L.qg_sample_workspace,
                   L.qg_sample)))

@@ -1,13 +1,16 @@
-"""Build libqg.so in-tree: nvcc for sm_100a (CUDA sources) + the host packer, one shared object; and qg_binding.so,
-the Python side of the operators that take torch tensors.
+"""Build libqg.so in-tree: nvcc for sm_100a (CUDA sources) + the host packer, one shared object; and, where torch is
+installed, qg_binding.so, the Python side of the operators that take torch tensors.
 
 Usage: python -m quant_dequant_gemv_q4_b200.build [--force]
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -29,11 +32,34 @@ def nvcc_cmd(src: str, obj: str, extra=()) -> list[str]:
             "-c", src, "-o", obj]
 
 
-def build_binding(force: bool = False) -> str:
-    deps = [BINDING_SOURCE, os.path.join(INCLUDE, "qg.h")]
-    if force or not os.path.exists(BINDING) or any(os.path.getmtime(d) > os.path.getmtime(BINDING) for d in deps):
-        import sysconfig
+def has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
 
+
+def built_for() -> str:
+    """What a binding that is built now is built for: it is compiled against one torch and one Python."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        import torch
+        version = str(torch.__version__)
+    return f"torch {version}, {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_is_for(path: str) -> str | None:
+    """What the binding at `path` was built for: noted beside it (and in it, for whoever loads it)."""
+    try:
+        with open(path + ".for") as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def build_binding(force: bool = False) -> str:
+    """Needs torch, its headers and Python's."""
+    deps = [BINDING_SOURCE, os.path.join(INCLUDE, "qg.h")]
+    if force or not os.path.exists(BINDING) or binding_is_for(BINDING) != built_for() or any(
+            os.path.getmtime(d) > os.path.getmtime(BINDING) for d in deps):
         import torch
         root = os.path.dirname(torch.__file__)
         cuda = os.path.dirname(os.path.dirname(NVCC))
@@ -41,10 +67,13 @@ def build_binding(force: bool = False) -> str:
         tmp = BINDING + f".tmp{os.getpid()}"
         try:
             subprocess.check_call(["g++", "-O2", "-fPIC", "-shared", "-std=c++17", "-fvisibility=hidden",
-                                   f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+                                   f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                                   f'-DQG_BUILT_FOR="{built_for()}"', "-I", INCLUDE,
                                    "-I", sysconfig.get_paths()["include"], *paths, BINDING_SOURCE, "-o", tmp, "-L", f"{root}/lib",
                                    "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
             os.replace(tmp, BINDING)
+            with open(BINDING + ".for", "w") as f:
+                f.write(built_for())
         finally:
             if os.path.exists(tmp):
                 os.remove(tmp)
@@ -52,8 +81,7 @@ def build_binding(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """One object per source, compiled side by side, then linked; and the binding."""
-    build_binding(force)
+    """One object per source, compiled side by side, then linked; then the binding, which libqg.so does without."""
     stale = force or not os.path.exists(LIB) or any(
         os.path.getmtime(d) > os.path.getmtime(LIB) for d in DEPS)
     if stale:
@@ -69,6 +97,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             for o in objs:
                 if os.path.exists(o):
                     os.remove(o)
+    if has_torch():
+        build_binding(force)
     return LIB
 
 

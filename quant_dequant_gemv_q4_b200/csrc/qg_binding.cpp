@@ -364,4 +364,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "qg_binding", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_qg_binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit_qg_binding()
+{
+    PyObject *const m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", QG_BUILT_FOR) < 0) {  // the torch and the Python of the build
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

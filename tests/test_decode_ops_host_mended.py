@@ -1,5 +1,12 @@
 """The operators between the GEMVs without a GPU, where they had gone wrong: empty calls, the build."""
+import os
+import subprocess
+import sys
+
+import pytest
+
 import quant_dequant_gemv_q4_b200 as qg
+from quant_dequant_gemv_q4_b200 import build
 from test_decode_ops_host import A, L, heads, norm_rope  # noqa: F401
 
 
@@ -14,3 +21,44 @@ def test_no_tokens_need_no_addresses(L):
     assert L.qg_kv4_read(A, 4, 32, 2, 128, None, 0, none, none, None) == qg.QG_OK
     assert L.qg_attn_kv4(none, 0, 0, None, 0, 4, 2, 128, None, 0, 32, None, 0, None, 1.0, none, None, 0, None) == qg.QG_OK
     assert L.qg_sample(None, 0, 100, 100, 1, None, None, None, None, None, None, None, 0, None) == qg.QG_OK
+
+
+def test_the_library_is_built_without_torch(L, tmp_path):
+    """Where torch is missing, build() leaves the binding out and makes libqg.so."""
+    run = ("import sys; sys.modules['torch'] = None; from quant_dequant_gemv_q4_b200 import build; "
+           f"build.BINDING = {str(tmp_path / 'qg_binding.so')!r}; print(build.build())")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", run], cwd=root, capture_output=True, text=True)
+    assert done.returncode == 0, done.stderr
+    assert done.stdout.strip() == build.LIB and os.listdir(tmp_path) == []
+
+
+def test_the_binding_is_built_again_for_another_torch(L, tmp_path, monkeypatch):
+    made = []
+
+    def compiler(cmd):
+        made.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+
+    path = str(tmp_path / "qg_binding.so")
+    monkeypatch.setattr(build, "BINDING", path)
+    monkeypatch.setattr(build.subprocess, "check_call", compiler)
+    build.build_binding()
+    assert len(made) == 1 and build.binding_is_for(path) == build.built_for()
+    build.build_binding()
+    assert len(made) == 1
+    monkeypatch.setattr(build, "built_for", lambda: "torch 99, cpython-0")
+    build.build_binding()
+    assert len(made) == 2 and build.binding_is_for(path) == "torch 99, cpython-0"
+    os.remove(path + ".for")
+    build.build_binding()
+    assert len(made) == 3
+
+
+def test_a_binding_of_another_torch_is_refused(L, monkeypatch):
+    monkeypatch.setattr(qg, "_binding", None)
+    qg._bound()
+    monkeypatch.setattr(qg, "_binding", None)
+    monkeypatch.setattr(build, "built_for", lambda: "torch 99, cpython-0")
+    with pytest.raises(RuntimeError, match="build it again"):
+        qg._bound()
