@@ -404,7 +404,8 @@ int qg_kv4_read(const void *cache, int64_t pages, int page, int H, int D, const 
  *   workspace  device, at least qg_attn_kv4_workspace(Hq, Hk, D, max_q) bytes (0 for arguments out of
  *              range, or without a device), 256-byte aligned, contents of no matter.  Calls that may overlap on the GPU
  *              (two streams, two graphs) need one each.  Its first word is nonzero afterwards only if
- *              a wait inside the kernel ran out after two seconds (the results are then void).
+ *              a wait inside the kernel ran out after two seconds (the results are then void); that is also
+ *              noted for qg_attn_kv4_device_error, whatever becomes of the workspace.
  * Scores, softmax statistics and sums are fp32; cache values and softmax weights enter the products as
  * fp16, rounded once.  Errors as above (QG_ERR_SHAPE also where T * (Hq/Hk) exceeds 2^31 - 257), plus
  * QG_ERR_SCRATCH. */
@@ -413,6 +414,11 @@ int qg_attn_kv4(const qg_heads *q, int64_t T, int nseq, const int32_t *q_start, 
                 int D, const void *cache, int64_t pages, int page, const int32_t *table, int width,
                 const int32_t *kv_len, float scale, const qg_heads *out, void *workspace,
                 size_t workspace_bytes, void *stream);
+
+/* Reads and clears the current device's note of qg_attn_kv4 calls whose waits ran out, after synchronizing
+ * `stream` (the stream of the calls to check; NULL = the legacy default stream).  *flag = 0 if there was none
+ * since it was last read.  Not to be called while a stream is captured. */
+int qg_attn_kv4_device_error(void *stream, int *flag);
 
 /* One token a row from its logits and a given random number.  With z = logit / temperature, tokens in
  * descending order of their logits (equal ones: the lower index first) and w = exp(z - z_max):

@@ -124,6 +124,8 @@ def lib() -> ctypes.CDLL:
         L.qg_attn_kv4_workspace.restype = SZ
         L.qg_attn_kv4.argtypes = [HP, I64, I, P, I, I, I, I, P, I64, I, P, I, P, F, HP, P, SZ, P]
         L.qg_attn_kv4.restype = I
+        L.qg_attn_kv4_device_error.argtypes = [P, ctypes.POINTER(I)]
+        L.qg_attn_kv4_device_error.restype = I
         L.qg_sample_workspace.argtypes = [I64, I64, I64]
         L.qg_sample_workspace.restype = SZ
         L.qg_sample.argtypes = [P, I64, I64, I64, I64, P, P, P, P, P, P, P, SZ, P]
@@ -364,10 +366,18 @@ def qg_attn_kv4(q, q_start, max_q: int, cache, page: int, table, kv_len, scale: 
     """Causal attention of the new tokens q [T, Hq, D] (fp16; sequence s: rows q_start[s] .. q_start[s + 1] - 1)
     over the 4-bit cache, sequence s having kv_len[s] places in the pages table[s], into out [T, Hq, D] (fp16).
     workspace: uint8, qg_attn_kv4_workspace(Hq, Hk, D, max_q) bytes, not shared with a call that may overlap;
-    None takes one from torch's allocator for this call."""
+    None takes one from torch's allocator for this call.  Device-side timeouts: qg_attn_kv4_device_error()."""
     rc = (_binding or _bound()).attn_kv4(q, q_start, max_q, cache, page, table, kv_len, scale, out, workspace, stream)
     if rc:
         raise QgError(rc, "qg_attn_kv4")
+
+
+def qg_attn_kv4_device_error(stream=None) -> int:
+    """Nonzero if a wait inside a qg_attn_kv4 call on the current device ran out (its results are void) since this was
+    last asked; synchronizes the stream."""
+    flag = ctypes.c_int(0)
+    _ok(lib().qg_attn_kv4_device_error(_stream(stream), ctypes.byref(flag)), "qg_attn_kv4_device_error")
+    return flag.value
 
 
 def qg_sample_workspace(rows: int, V: int, elem_stride: int) -> int:

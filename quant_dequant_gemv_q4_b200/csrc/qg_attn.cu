@@ -225,6 +225,9 @@ template <int D, int N> struct Cfg {
     static constexpr int kBytes = kP + kPAll;
 };
 
+// Whether a call on this device has given up since qg_attn_kv4_device_error was last asked.
+__device__ int g_gave_up;
+
 // Giving up.  A wait that lasts longer than kWaitNs sets the call's error word and `gave_up`.  The producer, the only
 // role whose waits end on that alone, then stops and sets `quiet` (as it does at its end in any case); the other roles
 // wait on until `dead`, which is set once both are, and go through their remaining tiles without waiting.  The
@@ -1041,6 +1044,7 @@ template <int D, int N> __global__ void __launch_bounds__(Cfg<D, N>::kWarps * 32
     tc_fence_before();
     __syncthreads();
     if (stop->gave_up) {
+        if (threadIdx.x == 0) g_gave_up = 1;
         // copies and products in flight end before shared and tensor memory are given up
         if (warp == kProducer)
             for (int st = 0; st < C::kStages && st < sm.produced; ++st)
@@ -1239,6 +1243,21 @@ int qg_attn_kv4(const qg_heads *q, int64_t T, int nseq, const int32_t *q_start, 
     case 128: return launch_rows<128>(a, N, sms, nseq, stream);
     default: return launch_rows<256>(a, N, sms, nseq, stream);
     }
+}
+
+int qg_attn_kv4_device_error(void *stream, int *flag)
+{
+    if (!flag) return QG_ERR_NULL;
+    *flag = 0;
+    void *p = nullptr;
+    int v = 0;
+    if (cuda_status(cudaGetSymbolAddress(&p, g_gave_up)) != QG_OK ||
+        cuda_status(cudaStreamSynchronize(static_cast<cudaStream_t>(stream))) != QG_OK ||
+        cuda_status(cudaMemcpy(&v, p, sizeof(v), cudaMemcpyDeviceToHost)) != QG_OK)
+        return QG_ERR_CUDA;
+    if (v != 0 && cuda_status(cudaMemset(p, 0, sizeof(v))) != QG_OK) return QG_ERR_CUDA;
+    *flag = v;
+    return QG_OK;
 }
 
 }  // extern "C"

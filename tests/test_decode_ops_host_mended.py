@@ -23,6 +23,10 @@ def test_no_tokens_need_no_addresses(L):
     assert L.qg_sample(None, 0, 100, 100, 1, None, None, None, None, None, None, None, 0, None) == qg.QG_OK
 
 
+def test_attention_device_error_needs_a_flag(L):
+    assert L.qg_attn_kv4_device_error(None, None) == qg.QG_ERR_NULL
+
+
 def test_the_library_is_built_without_torch(L, tmp_path):
     """Where torch is missing, build() leaves the binding out and makes libqg.so."""
     run = ("import sys; sys.modules['torch'] = None; from quant_dequant_gemv_q4_b200 import build; "

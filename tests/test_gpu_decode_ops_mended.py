@@ -236,3 +236,17 @@ def test_scales_are_rounded_to_fp32_and_then_to_fp16(qg):
     ref.store(want, page, np.arange(2), 0, code, d, m)
     ref.store(want, page, np.arange(2), 1, *ref.quantize(x.astype(np.float64)))
     assert np.array_equal(cache.cpu().numpy(), want)
+
+
+def test_attention_says_whether_it_gave_up(qg):
+    """No wait has run out in the calls of these tests, with workspaces of their own or torch's, on any stream."""
+    import torch
+    c = attention_case(2, [3000, 50], [1, 2], 1, 4, 64, 16)
+    run_attention(qg, c)
+    assert qg.qg_attn_kv4_device_error() == 0
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run_attention(qg, c)
+        assert qg.qg_attn_kv4_device_error() == 0
+    assert qg.qg_attn_kv4_device_error(s) == 0
