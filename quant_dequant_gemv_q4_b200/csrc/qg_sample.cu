@@ -779,10 +779,10 @@ template <bool RESIDENT> __global__ void __launch_bounds__(kThreads, 1) sample_k
                     }
                     __syncthreads();
                     const int b = s.bin[0];
-                    if (b < 0) {
-                        // the cut is above these bins (or p is 0: the first token alone)
-                        cut_key = done_c ? hi : key_of(top);
-                        cut_ties = done_c ? 0 : 1;
+                    if (b < 0) {  // (in the first round only, as in cut_of_list) all of these bins' tokens are kept, or none
+                        const bool all = share && (double)done_w < target;
+                        cut_key = all ? lo : done_c ? hi : key_of(top);  // (p of 0: the first token alone)
+                        cut_ties = all ? kAll : done_c ? 0 : 1;
                         break;
                     }
                     done_c += s.before[0];

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import kv4_ref as ref
-from test_gpu_decode_ops import attention_case, check_attention, dev, frequencies, layout, qg, run_attention  # noqa: F401
+from test_gpu_decode_ops import attention_case, check_attention, dev, frequencies, layout, qg, run_attention, run_sample  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -104,6 +104,29 @@ def test_sample_share_on_the_border_of_two_threads_bins(qg, V):
     for i in range(R):
         qg.qg_sample(lx[:1], None, None, dev(p[i:i + 1]), None, du[i:i + 1], one)
         assert one.item() == want[i]
+
+
+@pytest.mark.parametrize("middle", [900, 1200, 1800, 2040, 2300, 3000, 20_000])  # lists sorted, listed, and over the row
+def test_sample_share_that_ends_where_a_deep_tail_begins(qg, middle):
+    """A share of 1 - 2^-24 that ends just behind the middle weights, by the weight of a million of the smallest that
+    there are: all of the middle is kept (what the tail weighs decides no more than the tail), through every path."""
+    V = (1 << 20) - 1
+    rng = np.random.default_rng(middle)
+    x = np.empty((4, V), "f4")
+    level = 12 + np.log2(middle / 3000)
+    x[:] = -(44 - np.log2(1.7)) * np.log(2)             # the tail: 1.7 x 2^-44 each, less than 2^-24 of all
+    x[:, rng.permutation(V)[:middle]] = -level * np.log(2)
+    x[:, V // 2] = 0
+    p = np.full(4, 1 - 2.0 ** -24, "f4")
+    u = np.array([0.05, 0.4, 0.6, 0.95], "f4")
+    w = np.exp(x[0].astype(np.float64))
+    kept = np.where(x[0] > -20, w, 0.0)
+    assert w.sum() - kept.sum() < (1 - float(p[0])) * w.sum()
+    c = np.cumsum(kept)
+    got = run_sample(qg, x, p=p, u=u)
+    for i in range(4):
+        j = got[i]
+        assert kept[j] > 0 and (c[j] - kept[j]) / c[-1] - 2.0 ** -22 <= u[i] <= c[j] / c[-1] + 2.0 ** -22
 
 
 # ---------------------------------------------------------------------------------------------
