@@ -439,7 +439,9 @@ int qg_attn_kv4_device_error(void *stream, int *flag);
  *   workspace    device, 4-byte aligned, qg_sample_workspace(rows, V, elem_stride) bytes (0 for rows that
  *                stand one after another), not shared with a call that may overlap; NULL does without, more
  *                slowly
- * Weights are summed as 64-bit whole numbers: the token does not depend on timing.  Errors: QG_ERR_SHAPE,
+ * Weights are summed as 64-bit whole numbers of 2^-44 of the largest: the token does not depend on timing.  Each is
+ * off by 2^-30 of itself and 2^-45 of the largest at most (below that it counts as nothing, and is not chosen), so the
+ * token is that of the formula for a u within 2^-30 + V 2^-45 of the given one.  Errors: QG_ERR_SHAPE,
  * _NULL, _ALIGN, _SCRATCH (a workspace too small), _CUDA. */
 size_t qg_sample_workspace(int64_t rows, int64_t V, int64_t elem_stride);
 int qg_sample(const float *logits, int64_t rows, int64_t V, int64_t row_stride, int64_t elem_stride,

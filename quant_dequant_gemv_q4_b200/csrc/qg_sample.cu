@@ -23,9 +23,10 @@
 //
 // Weights are whole multiples of 2^-44 of the largest (64-bit integers): their sums do not depend on the order
 // of the additions, so a call gives the same token every time.  A weight is off by about 2^-30 of itself
-// (Row::weight), in either direction, so running sums over many tokens are off by far less, and the choice is
-// that of the exact formula but for u (or a filter's border) within about 1e-9 of a border.  64-bit
-// exponentials instead (exact to 2^-45) took 113 cycles of a scheduler for 32 of them.
+// (Row::weight), in either direction, and by half of 2^-44 at most from its rounding to a whole number, of which
+// those below 2^-45 lose all.  The choice is that of the exact formula but for u (or a filter's border) within
+// 2^-30 + V 2^-45 of a border: 1e-9 where the weights in the sums are large, 3e-8 (half a step of u next to 1) for a
+// million of the smallest.  64-bit exponentials instead (exact to 2^-45) took 113 cycles of a scheduler for 32 of them.
 //
 // What bounds it is the chain of stages, most of them short and run once, 32 warps wide: about 55,000 cycles for a row
 // of 151936 (32 us; its bytes would take 0.1), of which the passes over the row are 12,000, the list's sorts 4,000 to
@@ -49,7 +50,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 4096;
 constexpr int kPer = kBins / kThreads;  // bins of a thread
 constexpr float kBinStep = 0.98922801319397548f;  // 2^(-1/64)
-constexpr float kDeepest = 45.9f;  // below 2^-45.9 of the largest a weight is 0
+constexpr float kDeepest = 45.9f;  // the bins go down to 2^-45.9 of the largest weight (from 2^-45 on weights are 0)
 constexpr int kList = 2 * kThreads;
 constexpr double kOne = 17592186044416.0;  // the largest weight, 2^44
 typedef unsigned long long u64;
@@ -136,7 +137,7 @@ template <bool RESIDENT> struct Row {
     // t = (xmax - x) c is formed as a sum of two floats (the difference and the product with their rounding
     // errors: about 2^-46 of t).  With n = 64 t rounded, which is the bin (monotone in x), t = n / 64 + r and
     // |r| <= 1/128: 2^-t = 2^-q 2^(j/64) e^y, y = -r ln 2; a table, and the Taylor series of e^y - 1 to the third
-    // power in fp32 (2^-24 of at most 0.0055; the fourth power is below 4e-11), multiplied in 62 bits.
+    // power in fp32 (2^-24 of at most 0.0055; the fourth power is below 4e-11), multiplied in 62 bits and rounded.
     __device__ __forceinline__ u64 weight(float x, int *bin) const
     {
         const float d = xmax - x;
@@ -144,7 +145,7 @@ template <bool RESIDENT> struct Row {
         const float dl = (xmax - (d - v)) - (x + v);
         const float t0 = d * ch;
         const float t = fminf(t0, kDeepest);
-        const float tl = fmaf(d, ch, -t0) + fmaf(d, cl, dl * ch);  // (NaN at -inf: y is then of no matter)
+        const float tl = fmaf(d, ch, -t0) + fmaf(d, cl, dl * ch);  // (NaN at -inf)
         const float m = fmaf(t, 64.0f, 12582912.0f);  // 1.5 * 2^23: the sum's low bits are 64 t, rounded
         const int n64 = __float_as_int(m) - 0x4b400000;
         const float y = (fmaf(m - 12582912.0f, -1.0f / 64.0f, t) + tl) * -0.693147180559945f;
@@ -152,7 +153,8 @@ template <bool RESIDENT> struct Row {
         const int q = (n64 + 63) >> 6;
         const unsigned factor = 0x80000000u + (unsigned)__float2int_rn(e * 2147483648.0f);
         *bin = n64;
-        return ((u64)table[(q << 6) - n64] * factor) >> (17 + q);
+        const u64 w = ((u64)table[(q << 6) - n64] * factor + (1ull << (16 + q))) >> (17 + q);
+        return t0 < kDeepest ? w : 0;  // (deeper, y is of no matter)
     }
     __device__ __forceinline__ u64 weight(float x) const
     {
@@ -313,6 +315,8 @@ __device__ unsigned find_count(Shared &s, const unsigned (&c)[kPer], unsigned k)
 // of the weight after it is at most `tail`.  s.before[0]: tokens before the first, s.before[1]: down to the
 // last of them (of all tokens, `c`; the weights are those of `kept` of them).  The bounds' margin of 2e-4
 // covers the bins' borders, these sums and the one in `tail`, all in fp32 (of at most 2^10 logits a thread).
+// A tail of weights below 2^-32 is off by more than that margin as whole numbers of 2^-44; the cut may then lie past the
+// last of these bins (all of them are kept) or before the first (none), by less than the tail weighs.
 // The same sum is rounded differently by two neighbouring threads, so both may see a border between their bins, or
 // neither: of several the outermost bins are taken, by atomics, so that every CTA of a cluster, from the same
 // counts, takes the same ones (how many cluster barriers it meets depends on them), and of none all bins.

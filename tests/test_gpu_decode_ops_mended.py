@@ -106,6 +106,29 @@ def test_sample_share_on_the_border_of_two_threads_bins(qg, V):
         assert one.item() == want[i]
 
 
+@pytest.mark.parametrize("V", [151_936, (1 << 20) - 1])
+@pytest.mark.parametrize("deep", [43.01, 44.4, 40.3, 43.5, 36.7, 45.5, 24.0])
+def test_sample_of_one_logit_and_a_long_flat_tail(qg, V, deep):
+    """Weights next to the least that counts, a vocabulary full of them.  A weight is off by 2^-45 at most and 2^-30 of
+    itself, so a token is right for a u that is off by V 2^-45 and 2^-29 (the sum and the total)."""
+    x = np.full((2, V), -deep * np.log(2), "f4")
+    x[0, V - 1] = 0   # the tail first
+    x[1, 0] = 0       # ... and last
+    w = np.exp(x.astype(np.float64))
+    c = np.cumsum(w, 1)
+    total = c[:, -1]
+    near = np.array([0.03, 0.2, 0.5, 0.8, 0.97]) * w[0, 0] * (V - 1)
+    u = np.stack([near / total[0], (1 + near) / total[1]]).clip(0, 1 - 2.0 ** -24).astype("f4")
+    far = V * 2.0 ** -45 + 2.0 ** -29
+    for i in range(u.shape[1]):
+        got = run_sample(qg, x, u=u[:, i])
+        for r in range(2):
+            j = got[r]
+            assert 0 <= j < V
+            at, before = c[r, j] / total[r], (c[r, j] - w[r, j]) / total[r]
+            assert before - far <= u[r, i] <= at + far, (r, i, j, u[r, i], before, at)
+
+
 @pytest.mark.parametrize("middle", [900, 1200, 1800, 2040, 2300, 3000, 20_000])  # lists sorted, listed, and over the row
 def test_sample_share_that_ends_where_a_deep_tail_begins(qg, middle):
     """A share of 1 - 2^-24 that ends just behind the middle weights, by the weight of a million of the smallest that
