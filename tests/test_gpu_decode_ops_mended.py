@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 import kv4_ref as ref
+import test_gpu_decode_ops as decode
 from test_gpu_decode_ops import attention_case, check_attention, dev, frequencies, layout, qg, run_attention, run_sample  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -296,3 +297,70 @@ def test_attention_says_whether_it_gave_up(qg):
         run_attention(qg, c)
         assert qg.qg_attn_kv4_device_error() == 0
     assert qg.qg_attn_kv4_device_error(s) == 0
+
+
+# ---------------------------------------------------------------------------------------------
+# Many tokens: blocks of four, whose tables stand side by side
+# ---------------------------------------------------------------------------------------------
+def many(over):
+    """A number of tokens from which on a block takes four (16 a multiprocessor), and `over` more."""
+    import torch
+    return 16 * torch.cuda.get_device_properties(0).multi_processor_count + over
+
+
+@pytest.mark.parametrize("over", [0, 1, 2, 3, 1731])  # whole blocks and a last one of one, two and three tokens
+@pytest.mark.parametrize("D,Hq,Hk,R,pairing,norm,how,src,dst", [
+    (64, 3, 2, 64, 0, True, "rows", "f2", "f2"), (64, 17, 0, 6, 1, True, "odd", "f4", "f4"), (128, 12, 3, 128, 0, True, "rows", "f4", "f2"),
+    (128, 1, 1, 10, 0, False, "heads first", "f2", "f2"), (256, 9, 2, 64, 1, True, "rows", "f2", "f2"),
+    (256, 1, 0, 0, 0, True, "rows", "f4", "f4"), (256, 2, 1, 20, 0, True, "gemv", "f4", "f2")])
+def test_norm_rope_of_many_tokens(qg, over, D, Hq, Hk, R, pairing, norm, how, src, dst):
+    decode.test_norm_rope(qg, D, many(over), Hq, Hk, R, pairing, norm, 250000, how, src, dst)
+
+
+@pytest.mark.parametrize("over", [1, 3, 1731])
+@pytest.mark.parametrize("D,H,page,R,pairing,norm,how,src", [
+    (64, 5, 16, 64, 0, True, "rows", "f2"), (64, 1, 48, 2, 1, True, "odd", "f2"), (128, 2, 32, 10, 0, True, "rows", "f4"),
+    (128, 3, 16, 0, 0, False, "rows", "f2"), (256, 1, 64, 64, 1, False, "heads first", "f4"), (256, 2, 16, 256, 0, True, "gemv", "f4")])
+def test_append_and_read_of_many_tokens(qg, over, D, H, page, R, pairing, norm, how, src):
+    decode.test_append_and_read(qg, D, many(over), H, page, R, pairing, norm, how, src)
+
+
+def test_append_of_the_same_token_twice(qg):
+    """Two tokens of one slot, the same values: the slot holds them, and nothing else is touched."""
+    import torch
+    x = torch.randn(1, 3, 128, device="cuda")
+    slot = torch.tensor([37], device="cuda")
+    one, two = qg.kv4_cache(4, 16, 3, 128).fill_(85), qg.kv4_cache(4, 16, 3, 128).fill_(85)
+    qg.qg_kv4_append(x, -x, None, 0.0, None, None, 0, slot, one, 16)
+    qg.qg_kv4_append(x.expand(9, 3, 128), -x.expand(9, 3, 128), None, 0.0, None, None, 0, slot.repeat(9), two, 16)
+    assert torch.equal(one, two)
+
+
+# ---------------------------------------------------------------------------------------------
+# Attention told less than the truth
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("max_q", [0, 1, 2, 9, 33, 100_000])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_with_any_max_q(qg, D, max_q):
+    """How many query rows are worked through together is only a matter of time; items cut between CTAs among them."""
+    for lens, nq, Hk, G in (([777, 33, 1300, 0], [1, 4, 3, 2], 2, 4), ([3000, 90], [37, 5], 1, 7)):
+        c = attention_case(41, lens, nq, Hk, G, D, 32)
+        c["max_q"] = max_q
+        check_attention(qg, c)
+
+
+def test_attention_leaves_rows_outside_of_falling_starts(qg):
+    """Starts that fall or lie outside of 0 .. T: those sequences have no rows.  Rows of none stay, what lies around
+    out stays, and so does the cache."""
+    import torch
+    c = attention_case(6, [64, 32, 40, 50], 2, 1, 2, 64, 32)
+    c["start"] = np.array([3, 5, 2, -4, -1], np.int32)
+    T = len(c["q"])
+    wide = torch.full((T + 4, 2, 64), 9, dtype=torch.float16, device="cuda")
+    cache = dev(c["cache"])
+    qg.qg_attn_kv4(dev(c["q"]), dev(c["start"]), 2, cache, 32, dev(c["table"]), dev(c["lens"]), c["scale"], wide[2:-2])
+    got = wide.cpu().numpy()
+    assert (np.delete(got, [5, 6], 0) == 9).all() and np.array_equal(cache.cpu().numpy(), c["cache"])
+    one = dict(c, start=np.array([3, 5], np.int32), table=c["table"][:1], lens=c["lens"][:1])
+    want, bound = ref.attention(one["q"], one["start"], one["cache"], 32, one["table"], one["lens"], one["scale"], np.full(c["q"].shape, 9.0))
+    assert (np.abs(got[2:-2].astype(np.float64) - want) <= bound).all()
