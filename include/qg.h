@@ -76,18 +76,20 @@ enum { QG_FMT_Q8_0 = 8, QG_FMT_Q4_K = 12, QG_FMT_Q5_K = 13, QG_FMT_Q6_K = 14, QG
 enum {
     QG_OK = 0,
     QG_ERR_NULL = 1,    /* a required pointer is NULL */
-    QG_ERR_FMT = 2,     /* unknown format flag */
-    QG_ERR_SHAPE = 3,   /* N < 0, K < 1, or K not a multiple of the block size */
+    QG_ERR_FMT = 2,     /* unknown format flag or element type */
+    QG_ERR_SHAPE = 3,   /* N < 0, K < 1, or K not a multiple of the block size; a size out of an entry's range */
     QG_ERR_BATCH = 4,   /* B outside 1..8 (1..16 for Q4_K, Q5_K, Q6_K and Q8_0 with K % 256 == 0,
                            and IQ4_XS with an even K / 256) */
-    QG_ERR_ALIGN = 5,   /* W not 16-byte aligned, x not 2-byte aligned or y not 4-byte aligned */
+    QG_ERR_ALIGN = 5,   /* W not 16-byte aligned, x not 2-byte aligned or y not 4-byte aligned; other
+                           pointers as their entries say */
     QG_ERR_CUDA = 6,    /* a CUDA runtime call failed (device query, launch, copy) */
     QG_ERR_NOMEM = 7,   /* the workspace could not be allocated */
     QG_ERR_RANGE = 8,   /* a packer field is out of range (sc, m > 63; q above 15 / 31 / 63 / 15
-                           for Q4_K / Q5_K / Q6_K / IQ4_XS; Q8_0 q = -128) */
-    QG_ERR_VARIANT = 9, /* unknown kernel variant, or a variant that does not take this format */
+                           for Q4_K / Q5_K / Q6_K / IQ4_XS; Q8_0 q = -128); eps is below 0 or NaN */
+    QG_ERR_VARIANT = 9, /* unknown kernel variant, or a variant that does not take this format; unknown
+                           pairing of a rotation */
     QG_ERR_SCRATCH = 10 /* qg_gemv_noalloc: the call needs more scratch than its fixed array holds;
-                           qg_attn_kv4: the workspace is smaller than qg_attn_kv4_workspace says */
+                           qg_attn_kv4, qg_sample: the workspace is smaller than their sizes say */
 };
 
 /* Kernel variants of the GEMV (qg_gemv_variant).  QG_VARIANT_AUTO is what qg_gemv uses: when

@@ -1172,15 +1172,15 @@ const char *qg_status_string(int status)
     switch (status) {
     case QG_OK: return "ok";
     case QG_ERR_NULL: return "a required pointer is NULL";
-    case QG_ERR_FMT: return "unknown format flag";
-    case QG_ERR_SHAPE: return "invalid shape (N < 0, K < 1 or K not a multiple of the block size)";
+    case QG_ERR_FMT: return "unknown format flag or element type";
+    case QG_ERR_SHAPE: return "invalid shape or size (of a GEMV: N < 0, K < 1 or K not a multiple of the block size)";
     case QG_ERR_BATCH: return "B must be in 1..8 (1..16 for Q4_K, Q5_K, Q6_K with K % 256 == 0)";
-    case QG_ERR_ALIGN: return "misaligned pointer (W 16 B, x 2 B, y 4 B)";
+    case QG_ERR_ALIGN: return "misaligned pointer (a GEMV's W 16 B, x 2 B, y 4 B; views their element, a cache 16 B, its attention's workspace 256 B)";
     case QG_ERR_CUDA: return "CUDA runtime error";
     case QG_ERR_NOMEM: return "workspace allocation failed";
-    case QG_ERR_RANGE: return "packer field out of range";
-    case QG_ERR_VARIANT: return "kernel variant not available for this format/shape";
-    case QG_ERR_SCRATCH: return "call needs more scratch than the fixed no-allocation array holds";
+    case QG_ERR_RANGE: return "packer field or eps out of range";
+    case QG_ERR_VARIANT: return "kernel variant not available for this format/shape, or unknown rotation pairing";
+    case QG_ERR_SCRATCH: return "the workspace is too small, or the call needs more scratch than the fixed no-allocation array holds";
     default: return "unknown status";
     }
 }

@@ -27,6 +27,14 @@ def test_attention_device_error_needs_a_flag(L):
     assert L.qg_attn_kv4_device_error(None, None) == qg.QG_ERR_NULL
 
 
+def test_status_texts_cover_the_operators(L):
+    """A status that an operator between the GEMVs gives is not explained by the GEMVs' reasons alone."""
+    text = {s: L.qg_status_string(s).decode() for s in range(11)}
+    assert "workspace" in text[qg.QG_ERR_SCRATCH] and "element type" in text[qg.QG_ERR_FMT] and "eps" in text[qg.QG_ERR_RANGE]
+    assert "pairing" in text[qg.QG_ERR_VARIANT] and "size" in text[qg.QG_ERR_SHAPE] and "cache" in text[qg.QG_ERR_ALIGN]
+    assert len(set(text.values())) == 11
+
+
 def test_the_library_is_built_without_torch(L, tmp_path):
     """Where torch is missing, build() leaves the binding out and makes libqg.so."""
     run = ("import sys; sys.modules['torch'] = None; from quant_dequant_gemv_q4_b200 import build; "
