@@ -308,7 +308,8 @@ int qg_noalloc_device_error(void *stream, int *flag);
  *
  * Common to all: pointers are device pointers of the current device; calls are asynchronous on
  * `stream`, allocate nothing, keep nothing between calls and may be captured into a CUDA graph from
- * the first call on.  Results are bitwise identical run to run.  Argument errors are found on the host
+ * the first call on.  Results are bitwise identical run to run (but for tokens appended to one slot by the
+ * same call).  Argument errors are found on the host
  * before anything is enqueued; sizes and indices that stand in device memory (slots, page ids, lengths)
  * are checked by the kernels, which never read or write outside the arrays that the arguments
  * describe: each entry says what becomes of a bad one.
@@ -345,7 +346,8 @@ enum { QG_ROPE_HALVES = 0, QG_ROPE_ADJACENT = 1 };
  *   eps        >= 0
  *   pos        device, int32 [T]; inv_freq device, double [R/2] (both may be NULL with R == 0)
  *   R          rotated dimensions, even, 0 .. D; pairing QG_ROPE_*
- * Sums in fp32; the angle is reduced in 64 bits, so far positions lose nothing; outputs rounded once.
+ * Sums in fp32 (the squares of a row with a norm add up to a finite number, and with an eps below 1e-30 to at
+ * least that); the angle is reduced in 64 bits, so far positions lose nothing; outputs rounded once.
  * Errors: QG_ERR_SHAPE, _FMT (a view's type), _VARIANT (pairing), _RANGE (eps), _NULL, _ALIGN (a view's
  * pointer not a multiple of its element, wq, wk, pos 4 B, inv_freq 8 B), _CUDA. */
 int qg_qk_norm_rope(const qg_heads *q, const qg_heads *k, int64_t T, int Hq, int Hk, int D,
@@ -409,7 +411,8 @@ int qg_kv4_read(const void *cache, int64_t pages, int page, int H, int D, const 
  *              a wait inside the kernel ran out after two seconds (the results are then void); that is also
  *              noted for qg_attn_kv4_device_error, whatever becomes of the workspace.
  * Scores, softmax statistics and sums are fp32; cache values and softmax weights enter the products as
- * fp16, rounded once.  Errors as above (QG_ERR_SHAPE also where T * (Hq/Hk) exceeds 2^31 - 257), plus
+ * fp16, rounded once: the values of a sequence's kv_len places are at most 65504 (a larger one, which an
+ * append of fp32 may store, or a NaN also reaches rows of the sequence that do not see its place).  Errors as above (QG_ERR_SHAPE also where T * (Hq/Hk) exceeds 2^31 - 257), plus
  * QG_ERR_SCRATCH. */
 size_t qg_attn_kv4_workspace(int Hq, int Hk, int D, int max_q);
 int qg_attn_kv4(const qg_heads *q, int64_t T, int nseq, const int32_t *q_start, int max_q, int Hq, int Hk,
