@@ -412,8 +412,8 @@ int qg_kv4_read(const void *cache, int64_t pages, int page, int H, int D, const 
  *              noted for qg_attn_kv4_device_error, whatever becomes of the workspace.
  * Scores, softmax statistics and sums are fp32; cache values and softmax weights enter the products as
  * fp16, rounded once: the values of a sequence's kv_len places are at most 65504 (a larger one, which an
- * append of fp32 may store, or a NaN also reaches rows of the sequence that do not see its place).  Errors as above (QG_ERR_SHAPE also where T * (Hq/Hk) exceeds 2^31 - 257), plus
- * QG_ERR_SCRATCH. */
+ * append of fp32 may store, or a NaN also reaches rows of the sequence that do not see its place).  Errors as
+ * above (QG_ERR_SHAPE also where T * (Hq/Hk) exceeds 2^31 - 257), plus QG_ERR_SCRATCH. */
 size_t qg_attn_kv4_workspace(int Hq, int Hk, int D, int max_q);
 int qg_attn_kv4(const qg_heads *q, int64_t T, int nseq, const int32_t *q_start, int max_q, int Hq, int Hk,
                 int D, const void *cache, int64_t pages, int page, const int32_t *table, int width,

@@ -146,7 +146,7 @@ struct RowsAt {
             float x[kV];
             HeadsView w = v;
             w.p = v.type == QG_TYPE_F32 ? static_cast<void *>(static_cast<float *>(v.p) + at) : static_cast<void *>(static_cast<__half *>(v.p) + at);
-            load_dims<kV>(w, 0, 0, 0, x);
+            load_dims(w, 0, 0, 0, x);
             raw[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
             raw[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
         }

@@ -123,66 +123,50 @@ inline int launch_pdl(void (*kernel)(Args...), dim3 grid, dim3 block, size_t sme
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// V consecutive dimensions (V = 2, 4 or 8, starting at a multiple of V) of one head of one token.
-template <int V> __device__ __forceinline__ void load_dims(const HeadsView &h, int64_t t, int head, int dim, float (&x)[V])
+// Eight consecutive dimensions (from a multiple of eight on) of one head of one token.
+__device__ __forceinline__ void load_dims(const HeadsView &h, int64_t t, int head, int dim, float (&x)[8])
 {
     const int64_t at = t * h.st + head * h.sh + dim * h.sd;
     if (h.type == QG_TYPE_F32) {
         const float *p = static_cast<const float *>(h.p) + at;
         if (h.vec > 1) {
-            if constexpr (V == 2) {
-                const float2 v = *reinterpret_cast<const float2 *>(p);
-                x[0] = v.x, x[1] = v.y;
-            } else {
 #pragma unroll
-                for (int i = 0; i < V; i += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(p + i);
-                    x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-                }
+            for (int i = 0; i < 8; i += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(p + i);
+                x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[i] = p[i * h.sd];
+            for (int i = 0; i < 8; ++i) x[i] = p[i * h.sd];
         }
     } else {
         const __half *p = static_cast<const __half *>(h.p) + at;
         if (h.vec > 1) {
-            uint32_t w[V / 2];
-            if constexpr (V == 2) {
-                w[0] = *reinterpret_cast<const uint32_t *>(p);
-            } else if constexpr (V == 4) {
-                const uint2 v = *reinterpret_cast<const uint2 *>(p);
-                w[0] = v.x, w[1] = v.y;
-            } else {
-                const uint4 v = *reinterpret_cast<const uint4 *>(p);
-                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-            }
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < V / 2; ++i) {
-                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-                x[2 * i] = v.x, x[2 * i + 1] = v.y;
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                x[2 * i] = f.x, x[2 * i + 1] = f.y;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[i] = __half2float(p[i * h.sd]);
+            for (int i = 0; i < 8; ++i) x[i] = __half2float(p[i * h.sd]);
         }
     }
 }
 
-// The same V dimensions written (fp16: each rounded once).
+// V dimensions (4 or 8, from a multiple of V on) written (fp16: each rounded once).
 template <int V> __device__ __forceinline__ void store_dims(const HeadsView &h, int64_t t, int head, int dim, const float (&x)[V])
 {
+    static_assert(V == 4 || V == 8, "one 8- or 16-byte access of fp16, one or two of fp32");
     const int64_t at = t * h.st + head * h.sh + dim * h.sd;
     if (h.type == QG_TYPE_F32) {
         float *p = static_cast<float *>(h.p) + at;
         if (h.vec > 1) {
-            if constexpr (V == 2) {
-                *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
-            } else {
 #pragma unroll
-                for (int i = 0; i < V; i += 4)
-                    *reinterpret_cast<float4 *>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-            }
+            for (int i = 0; i < V; i += 4)
+                *reinterpret_cast<float4 *>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) p[i * h.sd] = x[i];
@@ -196,9 +180,7 @@ template <int V> __device__ __forceinline__ void store_dims(const HeadsView &h, 
                 const __half2 v = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
                 w[i] = *reinterpret_cast<const uint32_t *>(&v);
             }
-            if constexpr (V == 2)
-                *reinterpret_cast<uint32_t *>(p) = w[0];
-            else if constexpr (V == 4)
+            if constexpr (V == 4)
                 *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
             else
                 *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);

@@ -158,13 +158,6 @@ template <> struct TmemWrite16<4> {
                      : "memory");
     }
 };
-template <> struct TmemWrite16<8> {
-    static __device__ __forceinline__ void run(uint32_t taddr, const uint32_t (&r)[16])
-    {
-        asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-                     : "memory");
-    }
-};
 
 // The same instructions for a converged warp: one elected lane issues them.  The operands stay
 // warp-uniform; issued from a one-thread branch they cost about 100 cycles each in moves to uniform
