@@ -45,11 +45,11 @@ FALLBACK_HBM_GBS = 6650.0
 
 
 # The sources the headline's CUDA-core kernel (rows_gemv_kernel) is built and launched from: its
-# device code and the host planner/launcher.  The tensor-core kernel's file (qg_mma.cuh) and the
+# device code, the wrappers it includes and the host planner/launcher.  The tensor-core kernel's file (qg_mma.cuh) and the
 # host packer are not among them, so a change there leaves the headline's DRAM capture valid.
-ROWS_KERNEL_FILES = ("qg_api.cu", "qg_device.cuh", "qg_rows.cuh")
+ROWS_KERNEL_FILES = ("qg_api.cu", "qg_device.cuh", "qg_ptx.cuh", "qg_rows.cuh")
 MMA_KERNEL_FILES = ROWS_KERNEL_FILES + ("qg_codes.cuh", "qg_mma.cuh")  # the B >= 2 tensor-core kernel
-UMMA_KERNEL_FILES = ROWS_KERNEL_FILES + ("qg_codes.cuh", "qg_umma.cuh")  # the tcgen05 variant
+UMMA_KERNEL_FILES = ROWS_KERNEL_FILES + ("qg_codes.cuh", "qg_tcgen05.cuh", "qg_umma.cuh")  # the tcgen05 variant
 
 
 def kernel_source_hash(files=None) -> str:

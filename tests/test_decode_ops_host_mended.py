@@ -74,3 +74,30 @@ def test_a_binding_of_another_torch_is_refused(L, monkeypatch):
     monkeypatch.setattr(build, "built_for", lambda: "torch 99, cpython-0")
     with pytest.raises(RuntimeError, match="build it again"):
         qg._bound()
+
+
+def test_the_hashes_of_the_gemv_kernels_cover_what_they_include():
+    """The captured DRAM traffic is reported only while the kernel's sources are those of the capture: its list of files
+    has to hold every header that its files include."""
+    import re
+
+    import bench
+    csrc = os.path.join(os.path.dirname(build.__file__), "csrc")
+    for files, own in ((bench.ROWS_KERNEL_FILES, "qg_rows.cuh"), (bench.MMA_KERNEL_FILES, "qg_mma.cuh"), (bench.UMMA_KERNEL_FILES, "qg_umma.cuh")):
+        assert own in files
+        todo = [f for f in files if f.endswith(".cuh")]
+        for f in todo:
+            with open(os.path.join(csrc, f)) as h:
+                for name in re.findall(r'#include "(qg_\w+\.cuh)"', h.read()):
+                    assert name in files, (own, f, name)
+
+
+def test_the_traffic_record_is_of_these_sources():
+    """profiles/traffic.json was captured on the kernels as they stand, so that the bench reports it."""
+    import json
+
+    import bench
+    with open(os.path.join(bench.ROOT, "profiles", "traffic.json")) as f:
+        t = json.load(f)
+    assert bench.load_traffic(bench.kernel_source_hash(bench.ROWS_KERNEL_FILES)) == t
+    assert t["b8"]["mma_kernel_hash"] == bench.kernel_source_hash(bench.MMA_KERNEL_FILES)
