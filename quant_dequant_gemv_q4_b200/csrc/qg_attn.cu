@@ -27,14 +27,15 @@
 // softmax of each 32 query rows, and two warps that issue the matrix instructions, one for each product.  Key and
 // value operands have buffers of a part of a tile (kSub), scores and weights of a tile, all handed over by mbarriers.
 //
-// What bounds it, at decode (N = 16): issuing instructions.  A tile of D = 256 takes about 7100 warp instructions
-// (unpacking two thirds of them) and 2600 cycles, 64-69% of the SM's issue slots, where its bytes would arrive in
+// What bounds it, at decode (N = 16), D = 256: issuing instructions.  A tile takes about 7450 warp instructions
+// (unpacking two thirds of them) and 2600 cycles, 68% of the SM's issue slots, where its bytes would arrive in
 // about 1660; a part of an item costs about 6000 cycles more (q in, the first reference, O out), which ragged
-// batches and pages of few tiles feel.  200001 places of 4 heads: 69 us, 3.3 TB/s; 16 sequences of up to 16384:
-// 54 us; 64 of up to 6000, D = 128: 101 us.  Two softmax warpgroups on alternate tiles, each with an O of its own,
+// batches and pages of few tiles feel.  200001 places of 4 heads: 69 us, 3.3 TB/s; 16 sequences of up to 16000:
+// 53 us.  At D = 128 a tile has half the unpacking and takes about as long: 64 sequences of up to 6000 use 49% of the
+// slots, their warps wait for what passes between the roles (101-105 us).  Two softmax warpgroups on alternate tiles, each with an O of its own,
 // took 77, 58 and 100 us, two producers 70, 56 and 107: the instruction caches hold these loops only just, and
 // what shortens one of them lengthens the others.  At N = 128 the softmax bounds it, a thread's 32 scores at a time:
-// 1000 tokens on 7000, 437 us, 730 TFLOP/s.
+// 1000 tokens on 7000, 425 us, 750 TFLOP/s, with 72 registers a thread and spills in the softmax.
 //
 // Softmax in base 2 on fp32 scores.  A thread holds one place's scores; the reference maximum of a row is
 // shared by the 128 places and moves only when a score exceeds it by more than 8 (so hardly ever after the

@@ -10,11 +10,12 @@
 // A_i = w_i cos a, B_i = -+ w_j sin a and r the norm's factor.  A and B depend on the token alone: a block
 // makes them once in shared memory, and its warps take the token's heads with a lane's eight of each in
 // registers, the next rows' loads in flight while a row is worked on.  With many tokens a block takes
-// four: their tables are made side by side, and what a block waits for before its first row is shared.  The kernels are bound by
-// instructions and memory traffic for long inputs and by launch and load latency for a few tokens: 4099 tokens of
-// 32 + 8 heads of 128, fp16, take 27 us (84 MB, 3.1 TB/s), one token 2.7; appending 6001 tokens and reading them back
-// 32 and 17 us, 16 tokens 6.8 together.  (Of the append the 64-bit arithmetic takes the most; with two blocks a
-// multiprocessor instead of three 6001 tokens took 3 us longer.)
+// four: their tables are made side by side, and what a block waits for before its first row is shared.  For a few tokens
+// the kernels are bound by launch and load latency (one token 2.3 us, 16 tokens appended and read back 6.5), for many by
+// issuing instructions: 4099 tokens of 32 + 8 heads of 128, fp16, take 26 us (84 MB, 3.2 TB/s) with 74% of the issue slots of
+// the active cycles used, and 1.7 waves of blocks; appending 6001 tokens 32 us (68% of the slots; the fp64 pipe 8%
+// busy, the XU pipe, which converts between 64 and 32 bits, 38%), reading them back 17 (65%, and a row in flight a
+// lane).  With two blocks a multiprocessor instead of three the append of 6001 tokens took 3 us longer.
 #include <algorithm>
 
 #include "qg_kv4.cuh"
