@@ -364,3 +364,92 @@ def test_attention_leaves_rows_outside_of_falling_starts(qg):
     one = dict(c, start=np.array([3, 5], np.int32), table=c["table"][:1], lens=c["lens"][:1])
     want, bound = ref.attention(one["q"], one["start"], one["cache"], 32, one["table"], one["lens"], one["scale"], np.full(c["q"].shape, 9.0))
     assert (np.abs(got[2:-2].astype(np.float64) - want) <= bound).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# The ends of the ranges
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("nseq,Hk,G,D", [(1000, 2, 1, 64), (2301, 1, 3, 128)])
+def test_attention_of_more_sequences_than_a_block_has_threads(qg, nseq, Hk, G, D):
+    """The line of tiles is added up over several rounds of the block; most sequences short, one long, some empty."""
+    rng = np.random.default_rng(nseq)
+    lens = rng.integers(0, 40, nseq)
+    lens[nseq // 2], lens[-1] = 1500, 70
+    check_attention(qg, attention_case(nseq, [int(n) for n in lens], list(rng.integers(0, 3, nseq)), Hk, G, D, 16, spare=1))
+
+
+@pytest.mark.parametrize("Hk,G,D", [(1, 1024, 64), (1024, 1, 64), (2, 300, 128), (1, 129, 256)])
+def test_attention_of_many_heads(qg, Hk, G, D):
+    check_attention(qg, attention_case(G, [40, 150], [1, 2], Hk, G, D, 32))
+
+
+def test_attention_with_large_pages_and_scales(qg):
+    """Pages of 2048 places and of nine blocks; a scale of zero (the mean of what is seen), a negative and a large one.
+    (The reference's bound takes the scale as positive: a negative one is that of -q with its opposite, since
+    scale q . k = -scale (-q) . k and a sign costs no rounding.)"""
+    c = attention_case(51, [3000, 5], [2, 1], 2, 3, 128, 2048)
+    for scale in (0.0, -0.1, 3.0):
+        got = run_attention(qg, dict(c, scale=scale)).cpu().numpy().astype(np.float64)
+        want, bound = ref.attention(c["q"] if scale >= 0 else -c["q"], c["start"], c["cache"], 2048, c["table"], c["lens"], abs(scale),
+                                    np.full(c["q"].shape, 9.0))
+        assert (np.abs(got - want) <= bound).all()
+    check_attention(qg, attention_case(52, [1000, 290, 144], [1, 3, 2], 1, 5, 64, 144))
+
+
+@pytest.mark.parametrize("D,R,pairing", [(256, 256, 0), (256, 254, 0), (128, 128, 1), (64, 62, 1), (64, 2, 1)])
+def test_norm_rope_of_whole_heads(qg, D, R, pairing):
+    decode.test_norm_rope(qg, D, 19, 5, 2, R, pairing, True, 2 ** 31 - 20, "rows", "f2", "f2")
+    decode.test_norm_rope(qg, D, 19, 5, 2, R, pairing, True, -2 ** 31, "gemv", "f4", "f2")
+
+
+@pytest.mark.parametrize("pairing,R", [(0, 128), (0, 20), (1, 128)])
+def test_norm_rope_in_place_in_one_projection(qg, pairing, R):
+    """q and k side by side in one [T, (Hq + 2 Hk) D] array, each onto itself; v stays."""
+    import torch
+    T, Hq, Hk, D = 70, 6, 2, 128
+    rng = np.random.default_rng(R)
+    a = dev(rng.normal(size=(T, (Hq + 2 * Hk) * D)).astype("f2"))
+    b = a.clone()
+    part = lambda x, at, H: x[:, at * D:(at + H) * D].unflatten(1, (H, D))  # noqa: E731
+    wq, wk = (dev(rng.uniform(0.5, 1.5, D).astype("f4")) for _ in range(2))
+    pos, freq = dev(np.arange(T, dtype=np.int32)), dev(frequencies(R))
+    q, k = torch.empty(T, Hq, D, dtype=torch.float16, device="cuda"), torch.empty(T, Hk, D, dtype=torch.float16, device="cuda")
+    qg.qg_qk_norm_rope(part(a, 0, Hq), part(a, Hq, Hk), wq, wk, 1e-6, pos, freq, pairing, q, k)
+    qg.qg_qk_norm_rope(part(b, 0, Hq), part(b, Hq, Hk), wq, wk, 1e-6, pos, freq, pairing, part(b, 0, Hq), part(b, Hq, Hk))
+    assert torch.equal(part(b, 0, Hq), q) and torch.equal(part(b, Hq, Hk), k)
+    assert torch.equal(part(b, Hq + Hk, Hk), part(a, Hq + Hk, Hk))
+
+
+@pytest.mark.parametrize("major", ["row", "vocabulary"])
+def test_sample_of_very_many_rows(qg, major):
+    rng = np.random.default_rng(8)
+    R, V = 70_001, 5
+    x = rng.normal(size=(R, V)).astype("f4")
+    u = rng.random(R).astype("f4")
+    k = rng.integers(0, 4, R)
+    got = run_sample(qg, x, k=k, u=u, major=major)
+    at = np.concatenate([rng.integers(0, R, 500), [0, 65535, 65536, R - 1]])
+    assert [got[i] for i in at] == [ref.sample(x[i], None, int(k[i]), None, None, u[i]) for i in at]
+
+
+def test_sample_settings_at_their_ends(qg):
+    """An infinite temperature (all equally likely), counts and shares at their ends, logits of one value, strides of zero."""
+    import torch
+    rng = np.random.default_rng(4)
+    R, V = 8, 3001
+    x = (rng.normal(size=(R, V)) * 3).astype("f4")
+    x[:, ::5] = -np.inf
+    u = rng.random(R)
+    inf = np.full(R, np.inf)
+    for kw in (dict(t=inf), dict(t=inf, p=np.full(R, 0.5)), dict(t=inf, k=np.full(R, 1700), p=np.full(R, 0.9)),
+               dict(k=np.full(R, 2 ** 31 - 1)), dict(k=np.full(R, -2 ** 31)), dict(k=np.full(R, V)), dict(k=np.full(R, V - 1), p=np.full(R, 0.999)),
+               dict(p=np.full(R, -1.0)), dict(p=np.full(R, 1e-45)), dict(mp=np.full(R, 1e-45)), dict(mp=np.full(R, -3.0))):
+        decode.check_sample(qg, x, u=u, **kw)
+    one, tok = dev(x[0]), torch.zeros(4, dtype=torch.int32, device="cuda")
+    uu = dev(np.array([0.1, 0.3, 0.6, 0.99], "f4"))
+    qg.qg_sample(one.expand(4, V), None, None, None, None, uu, tok)   # every row the same memory
+    assert tok.tolist() == [ref.sample(x[0], None, None, None, None, v) for v in uu.cpu().numpy()]
+    qg.qg_sample(dev(x[:4, :1]).expand(4, 100), None, None, None, None, uu, tok)   # every token the same logit
+    assert tok.tolist() == [-1] * 4
+    qg.qg_sample(dev(x[:4, 1:2]).expand(4, 100), None, None, None, None, uu, tok)
+    assert tok.tolist() == [10, 30, 60, 99]
